@@ -324,7 +324,7 @@ def run(s):
         return rp.balance_loss(s["logits"], s["ids"], scoring=scoring, seq_offsets=s["offsets"], row_mask=s["mask"],
                                alpha=case["alpha"])
     return rp.gate_backward(s["logits"], s["ids"], s["gw"], scoring=scoring, renormalize=case["renorm"],
-                            scale=case["scale"], grad_loss=s["gl"], coef=s["coef"], seq_offsets=s["offsets"],
+                            scale=case["scale"], grad_loss=s["gl"], coef=s["coef"].contiguous(), seq_offsets=s["offsets"],
                             row_mask=s["mask"])
 
 
