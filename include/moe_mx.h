@@ -394,6 +394,68 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
                                 void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The router: what makes topk_ids / topk_weights from the gate's logits, the   */
+/* load-balance loss over them, and the gradient of both.                       */
+/*                                                                            */
+/* Common arguments:                                                            */
+/*   logits       device, [rows, num_experts] of dtype (FP32, FP16 or BF16). A    */
+/*                logit of -inf or NaN takes its expert out of the row: score 0,   */
+/*                gradient 0, ranked behind every other expert; +inf counts as the */
+/*                largest finite fp32 value.                                       */
+/*   num_experts  E in [1, 1024]; k in [1, min(32, E)]; rows < 2^31                */
+/*   scoring      MOE_GATE_SOFTMAX: s_e = exp(l_e) / sum_i exp(l_i) over all E;     */
+/*                MOE_GATE_SIGMOID: s_e = 1 / (1 + exp(-l_e)). Held in fp32.       */
+/*   seq_offsets  device, int32 [num_seqs + 1], non-decreasing: the rows of         */
+/*                sequence b are [off[b], off[b + 1]); rows outside [off[0],        */
+/*                off[num_seqs]) belong to none. NULL: all rows are one sequence    */
+/*                (num_seqs must be 1). num_seqs in [1, 65535].                     */
+/*   row_mask     device, uint8 [rows] or NULL: rows with 0 (padding) do not count. */
+/* moe_gate_topk                                                                 */
+/*   Rank of an expert: r_e = s_e + bias_e (bias fp32 [E] or NULL; it takes part   */
+/*   in the choice only). num_groups G > 1 (E % G == 0, G <= 64): of the G groups   */
+/*   of E / G neighbouring experts only the topk_groups with the largest sums of    */
+/*   their two best ranks take part (k <= topk_groups E / G; an expert taken out    */
+/*   adds 0, a group without any other expert comes last). topk_ids: the k best     */
+/*   ranks, largest first, equal ranks (and equal groups) by ascending index, so     */
+/*   they are distinct; the order is that of the exact ranks (ranks too close for    */
+/*   fp32 are compared in 64 bits). topk_weights[j] = scale s_j, or with             */
+/*   renormalize scale s_j / sum_i s_i over the k chosen (0 where that sum is 0).    */
+/*   topk_ids int32 [rows, k], topk_weights fp32 [rows, k]: as mega_moe takes them.  */
+/* moe_balance_loss                                                              */
+/*   With p = s (softmax) or s / sum_e s_e (sigmoid), T_b the counted rows of        */
+/*   sequence b, c_be their choices of expert e in topk_ids (k a row, distinct; an   */
+/*   id outside [0, E) is not counted) and B' the sequences with T_b > 0:            */
+/*     loss = alpha / B' sum_b E / (k T_b^2) sum_e c_be sum_{counted t in b} p_te    */
+/*   (0 when no row counts), fp32 [1];                                              */
+/*   counts int32 [num_seqs, E] = c_be;                                             */
+/*   coef fp32 [num_seqs, E] = alpha E c_be / (k T_b^2 B'): the derivative of the    */
+/*   loss by p_te of each counted row t of b.                                        */
+/*   Sums over rows are fp32 over a few rows and 64 bits beyond, in a fixed order.   */
+/* moe_gate_backward: d / d logits, [rows, E] of dtype, of                         */
+/*     sum_tj grad_weights[t, j] topk_weights[t, j] + grad_loss[0] loss             */
+/*   grad_weights fp32 [rows, k] or NULL (no gradient of the weights): the choice     */
+/*   topk_ids is held fixed, scoring / renormalize / scale as in moe_gate_topk;       */
+/*   grad_loss fp32 [1] or NULL (no gradient of the loss): with the coef, seq_offsets */
+/*   and row_mask of moe_balance_loss (the counts are held fixed). Both are added in  */
+/*   one pass over the logits. An id outside [0, E) adds nothing.                     */
+/* ------------------------------------------------------------------------ */
+enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 };
+#define MOE_GATE_MAX_EXPERTS 1024
+moe_status moe_gate_topk(const void* logits, int dtype, int64_t rows, int64_t num_experts, int64_t k, int scoring,
+                         const float* bias, int64_t num_groups, int64_t topk_groups, int renormalize, float scale,
+                         int32_t* topk_ids, float* topk_weights, void* stream);
+moe_status moe_balance_loss_workspace_size(int64_t rows, int64_t num_experts, int64_t num_seqs,
+                                           size_t* bytes /* host out */);
+moe_status moe_balance_loss(const void* logits, int dtype, int64_t rows, int64_t num_experts, const int32_t* topk_ids,
+                            int64_t k, int scoring, const int32_t* seq_offsets, int64_t num_seqs,
+                            const uint8_t* row_mask, float alpha, float* loss, int32_t* counts, float* coef,
+                            void* workspace, size_t workspace_bytes, void* stream);
+moe_status moe_gate_backward(const void* logits, int dtype, int64_t rows, int64_t num_experts, const int32_t* topk_ids,
+                             int64_t k, int scoring, int renormalize, float scale, const float* grad_weights,
+                             const float* grad_loss, const float* coef, const int32_t* seq_offsets, int64_t num_seqs,
+                             const uint8_t* row_mask, void* grad_logits, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Measured peaks for the roofline report (one launch each; the caller times   */
 /* it with events on `stream`).                                                */
 /* moe_probe_stream: mode 0 reads `bytes` from src (dst receives nothing      */

@@ -25,11 +25,13 @@ __all__ = [
     "mx_scale_cols", "token_permute_out_rows", "mx_quantize", "init_routing", "init_routing_noalloc", "token_permute",
     "mega_moe", "mega_moe_workspace_bytes", "gmm1_swiglu_quant", "gmm2_combine", "combine_finalize",
     "pack_weights", "WEIGHTS_ND", "WEIGHTS_PACKED", "DTYPE_FP8_E5M2", "DTYPE_FP8_E4M3", "DTYPE_FP4_E2M1",
+    "gate_topk", "balance_loss", "gate_backward", "GATE_SOFTMAX", "GATE_SIGMOID",
 ]
 
 QUANT_NONE, QUANT_E5M2, QUANT_E4M3, QUANT_MXFP4 = -1, 2, 3, 9
 FP8_E5M2, FP8_E4M3 = 23, 24
 WEIGHTS_ND, WEIGHTS_PACKED = 0, 1
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1   # scores of the router's logits
 _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int32: 3, torch.int64: 4}
 # x dtypes of MX codes for init_routing's pass-through (one FP8 code a byte, two FP4 codes a byte)
 DTYPE_FP8_E5M2, DTYPE_FP8_E4M3, DTYPE_FP4_E2M1 = 5, 6, 7
@@ -100,6 +102,12 @@ _SIGS = {
     "moe_gmm2_combine": ([_VP, _VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _INT, _INT, _VP, _VP, _I64, _VP,
                           _VP, _VP, _SZ, _VP], _INT),
     "moe_combine_finalize": ([_VP, _I64, _I64, _VP, _VP], _INT),
+    "moe_gate_topk": ([_VP, _INT, _I64, _I64, _I64, _INT, _VP, _I64, _I64, _INT, ctypes.c_float, _VP, _VP, _VP], _INT),
+    "moe_balance_loss_workspace_size": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "moe_balance_loss": ([_VP, _INT, _I64, _I64, _VP, _I64, _INT, _VP, _I64, _VP, ctypes.c_float, _VP, _VP, _VP,
+                          _VP, _SZ, _VP], _INT),
+    "moe_gate_backward": ([_VP, _INT, _I64, _I64, _VP, _I64, _INT, _INT, ctypes.c_float, _VP, _VP, _VP, _VP, _I64,
+                           _VP, _VP, _VP], _INT),
     "moe_probe_stream": ([_INT, _VP, _VP, _I64, _VP], _INT),
     "moe_probe_mfma": ([_INT, _VP, ctypes.POINTER(_I64), ctypes.POINTER(ctypes.c_double), _VP], _INT),
 }
@@ -495,6 +503,153 @@ def combine_finalize(y_accum):
     y = torch.empty((n, h), dtype=torch.bfloat16, device=y_accum.device)
     _check(lib.moe_combine_finalize(_ptr(y_accum), n, h, _ptr(y), _stream(y_accum.device)))
     return y
+
+
+class _on:
+    """The tensors' device as the current one while a call is made on it (a no-op, without
+    the cost of torch's device context, where it is current already)."""
+
+    __slots__ = ("want", "was")
+
+    def __init__(self, index: int):
+        self.want, self.was = index, torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.want != self.was:
+            torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.want != self.was:
+            torch.cuda.set_device(self.was)
+        return False
+
+
+def _device_of(first, **others):
+    """The index of the GPU that holds `first` and every other given tensor, all contiguous."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if not first.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    for name, t in others.items():
+        if t is not None:
+            if t.device != first.device:
+                raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    return first.device.index
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(index: int):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _gate_logits(logits, topk_ids=None):
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"logits must be float32, float16 or bfloat16 [rows, experts] (got {logits.dtype} "
+                         f"{tuple(logits.shape)})")
+    if topk_ids is not None and (topk_ids.dtype != torch.int32 or topk_ids.dim() != 2
+                                 or topk_ids.shape[0] != logits.shape[0]):
+        raise ValueError(f"topk_ids must be int32 [rows, k] with the logits' rows (got {topk_ids.dtype} "
+                         f"{tuple(topk_ids.shape)})")
+    return logits.shape
+
+
+def _gate_seqs(rows, seq_offsets, row_mask):
+    """The number of sequences, after the checks of their offsets and of the row mask."""
+    if row_mask is not None and (row_mask.dtype not in (torch.uint8, torch.bool) or tuple(row_mask.shape) != (rows,)):
+        raise ValueError(f"row_mask must be uint8 or bool [rows] (got {row_mask.dtype} {tuple(row_mask.shape)})")
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError(f"seq_offsets must be int32 [sequences + 1] (got {seq_offsets.dtype} "
+                         f"{tuple(seq_offsets.shape)})")
+    return seq_offsets.numel() - 1
+
+
+def gate_topk(logits, k: int, *, scoring: int = GATE_SOFTMAX, bias=None, num_groups: int = 1, topk_groups: int = 1,
+              renormalize: bool = True, scale: float = 1.0):
+    """The router's choice: (topk_ids int32 [N, K], topk_weights fp32 [N, K]) of logits [N, E]
+    (fp32, fp16 or bf16), as init_routing and mega_moe take them.
+
+    scoring: GATE_SOFTMAX (over all E) or GATE_SIGMOID. bias: fp32 [E] added to the scores for
+    the choice only. num_groups / topk_groups: only the topk_groups best of num_groups equal
+    groups of neighbouring experts (by the sum of their two best ranks) take part. The ids come
+    in descending order of rank, ties by the lowest index. renormalize: the weights of a row
+    sum to `scale` (else they are scale * score). A logit of -inf or NaN takes its expert out
+    (score 0, chosen last)."""
+    lib = load()
+    n, e = _gate_logits(logits)
+    index = _device_of(logits, bias=bias)
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (e,)):
+        raise ValueError(f"bias must be float32 [{e}] (got {bias.dtype} {tuple(bias.shape)})")
+    dev = logits.device
+    with _on(index):
+        ids = torch.empty((n, max(k, 0)), dtype=torch.int32, device=dev)
+        w = torch.empty((n, max(k, 0)), dtype=torch.float32, device=dev)
+        _check(lib.moe_gate_topk(logits.data_ptr(), _DT[logits.dtype], n, e, k, scoring, _raw(bias), num_groups,
+                                 topk_groups, int(bool(renormalize)), scale, ids.data_ptr(), w.data_ptr(),
+                                 _raw_stream(index)))
+    return ids, w
+
+
+def balance_loss(logits, topk_ids, *, scoring: int = GATE_SOFTMAX, seq_offsets=None, row_mask=None,
+                 alpha: float = 1.0):
+    """The load-balance loss of a router's rows: (loss fp32 [1], counts int32 [B, E], coef fp32
+    [B, E]) of logits [N, E] and the ids gate_topk chose.
+
+    loss = alpha * mean over the sequences with a counted row of sum_e f_e P_e, f_e = E times
+    the share of the sequence's choices that went to expert e, P_e = the mean score of e
+    (sigmoid scores divided by their sum). seq_offsets: int32 [B + 1] (None: all rows are one
+    sequence); row_mask: uint8 or bool [N], rows with 0 do not count. counts: the choices of
+    each expert. coef: the derivative of the loss by the scores of a counted row, for
+    gate_backward."""
+    lib = load()
+    n, e = _gate_logits(logits, topk_ids)
+    seqs = _gate_seqs(n, seq_offsets, row_mask)
+    index = _device_of(logits, topk_ids=topk_ids, seq_offsets=seq_offsets, row_mask=row_mask)
+    dev = logits.device
+    nbytes = ctypes.c_size_t()
+    _check(lib.moe_balance_loss_workspace_size(n, e, seqs, ctypes.byref(nbytes)))
+    with _on(index):
+        loss = torch.empty((1,), dtype=torch.float32, device=dev)
+        counts = torch.empty((seqs, e), dtype=torch.int32, device=dev)
+        coef = torch.empty((seqs, e), dtype=torch.float32, device=dev)
+        ws = _workspace(nbytes.value, dev)
+        _check(lib.moe_balance_loss(logits.data_ptr(), _DT[logits.dtype], n, e, topk_ids.data_ptr(), topk_ids.shape[1],
+                                    scoring, _raw(seq_offsets), seqs, _raw(row_mask), alpha, loss.data_ptr(),
+                                    counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(index)))
+    return loss, counts, coef
+
+
+def gate_backward(logits, topk_ids, grad_weights=None, *, scoring: int = GATE_SOFTMAX, renormalize: bool = True,
+                  scale: float = 1.0, grad_loss=None, coef=None, seq_offsets=None, row_mask=None):
+    """The logits' gradient ([N, E], the logits' type) in one pass: of gate_topk's weights, given
+    grad_weights fp32 [N, K] (scoring, renormalize and scale as in that call; the choice is held
+    fixed), and of balance_loss's loss, given grad_loss fp32 [1] with that call's coef,
+    seq_offsets and row_mask (the counts are held fixed). Either may be None."""
+    lib = load()
+    n, e = _gate_logits(logits, topk_ids)
+    seqs = _gate_seqs(n, seq_offsets, row_mask)
+    k = topk_ids.shape[1]
+    if grad_weights is not None and (grad_weights.dtype != torch.float32 or tuple(grad_weights.shape) != (n, k)):
+        raise ValueError(f"grad_weights must be float32 [{n}, {k}] (got {grad_weights.dtype} "
+                         f"{tuple(grad_weights.shape)})")
+    if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
+        raise ValueError("grad_loss must be one float32 value")
+    if coef is not None and (coef.dtype != torch.float32 or tuple(coef.shape) != (seqs, e)):
+        raise ValueError(f"coef must be float32 [{seqs}, {e}] (got {coef.dtype} {tuple(coef.shape)})")
+    index = _device_of(logits, topk_ids=topk_ids, grad_weights=grad_weights, grad_loss=grad_loss, coef=coef,
+                       seq_offsets=seq_offsets, row_mask=row_mask)
+    with _on(index):
+        grad = torch.empty_like(logits)
+        _check(lib.moe_gate_backward(logits.data_ptr(), _DT[logits.dtype], n, e, topk_ids.data_ptr(), k, scoring,
+                                     int(bool(renormalize)), scale, _raw(grad_weights), _raw(grad_loss), _raw(coef),
+                                     _raw(seq_offsets), seqs, _raw(row_mask), grad.data_ptr(), _raw_stream(index)))
+    return grad
 
 
 def probe_stream(src, dst=None, copy: bool = False, fill_caches: bool = False):

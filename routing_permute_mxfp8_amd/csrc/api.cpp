@@ -407,6 +407,40 @@ moe_status check_ws(const char* who, size_t need, void* ws, size_t have) {
   return MOE_OK;
 }
 
+// ---- router ------------------------------------------------------------------------
+moe_status check_gate(const char* who, int dtype, int64_t rows, int64_t experts, int64_t k, int scoring) {
+  if (rows < 0 || rows > INT32_MAX) return fail(MOE_ERR_SHAPE, "%s: rows %lld outside [0, 2^31)", who, (long long)rows);
+  if (experts < 1 || experts > MOE_GATE_MAX_EXPERTS)
+    return fail(MOE_ERR_SHAPE, "%s: num_experts %lld outside [1, %d]", who, (long long)experts, MOE_GATE_MAX_EXPERTS);
+  if (k < 1 || k > 32 || k > experts)
+    return fail(MOE_ERR_SHAPE, "%s: k %lld outside [1, min(32, num_experts %lld)]", who, (long long)k,
+                (long long)experts);
+  if (!valid_x_dtype(dtype)) return fail(MOE_ERR_DTYPE, "%s: dtype %d not FP32/FP16/BF16", who, dtype);
+  if (scoring != MOE_GATE_SOFTMAX && scoring != MOE_GATE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARG, "%s: scoring %d not 0 (softmax) or 1 (sigmoid)", who, scoring);
+  return MOE_OK;
+}
+
+moe_status check_seqs(const char* who, const int32_t* seq_offsets, int64_t num_seqs) {
+  if (num_seqs < 1 || num_seqs > 65535)
+    return fail(MOE_ERR_SHAPE, "%s: num_seqs %lld outside [1, 65535]", who, (long long)num_seqs);
+  if (!seq_offsets && num_seqs != 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: num_seqs %lld needs seq_offsets", who, (long long)num_seqs);
+  return MOE_OK;
+}
+
+moe::BalanceParams carve_balance(Carver& cv, int64_t rows, int64_t experts, int64_t seqs) {
+  moe::BalanceParams p;
+  p.splits = moe::balance_splits(rows, seqs);
+  const size_t parts = (size_t)seqs * p.splits;
+  p.sums = cv.take<float>(parts * experts);
+  p.part_counts = cv.take<int32_t>(parts * experts);
+  p.held = cv.take<int32_t>(parts);
+  p.seq_loss = cv.take<double>((size_t)seqs);
+  p.done = cv.take<unsigned>(1);
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -923,6 +957,93 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
   if (e != hipSuccess) return hip_fail(e, "finalize launch");
   return ok();
 }
+// ---- router ------------------------------------------------------------------------
+moe_status moe_gate_topk(const void* logits, int dtype, int64_t rows, int64_t num_experts, int64_t k, int scoring,
+                         const float* bias, int64_t num_groups, int64_t topk_groups, int renormalize, float scale,
+                         int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (moe_status s = check_gate("moe_gate_topk", dtype, rows, num_experts, k, scoring)) return s;
+  if (num_groups < 1 || num_groups > 64 || num_experts % num_groups != 0)
+    return fail(MOE_ERR_SHAPE, "moe_gate_topk: num_groups %lld must divide num_experts %lld and be in [1, 64]",
+                (long long)num_groups, (long long)num_experts);
+  if (topk_groups < 1 || topk_groups > num_groups)
+    return fail(MOE_ERR_SHAPE, "moe_gate_topk: topk_groups %lld outside [1, num_groups %lld]", (long long)topk_groups,
+                (long long)num_groups);
+  if (k > topk_groups * (num_experts / num_groups))
+    return fail(MOE_ERR_SHAPE, "moe_gate_topk: k %lld > the %lld experts of topk_groups groups", (long long)k,
+                (long long)(topk_groups * (num_experts / num_groups)));
+  if (renormalize != 0 && renormalize != 1) return fail(MOE_ERR_INVALID_ARG, "moe_gate_topk: renormalize must be 0 or 1");
+  if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARG, "moe_gate_topk: scale must be finite");
+  if (rows == 0) return ok();
+  if (!logits || !topk_ids || !topk_weights)
+    return fail(MOE_ERR_INVALID_ARG, "moe_gate_topk: logits, topk_ids and topk_weights must be non-NULL");
+  moe::GateParams p;
+  p.logits = logits; p.dtype = dtype; p.rows = rows; p.experts = (int)num_experts; p.k = (int)k;
+  p.sigmoid = scoring == MOE_GATE_SIGMOID; p.bias = bias; p.groups = (int)num_groups; p.topk_groups = (int)topk_groups;
+  p.renorm = renormalize != 0; p.scale = scale; p.ids = topk_ids; p.weights = topk_weights;
+  hipError_t e = moe::launch_gate(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_gate_topk launch");
+  return ok();
+}
+
+moe_status moe_balance_loss_workspace_size(int64_t rows, int64_t num_experts, int64_t num_seqs, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss_workspace_size: bytes is NULL");
+  if (moe_status s = check_gate("moe_balance_loss", MOE_DTYPE_FP32, rows, num_experts, 1, MOE_GATE_SOFTMAX)) return s;
+  if (num_seqs < 1 || num_seqs > 65535)
+    return fail(MOE_ERR_SHAPE, "moe_balance_loss: num_seqs %lld outside [1, 65535]", (long long)num_seqs);
+  Carver cv(nullptr);
+  carve_balance(cv, rows, num_experts, num_seqs);
+  *bytes = cv.off;
+  return ok();
+}
+
+moe_status moe_balance_loss(const void* logits, int dtype, int64_t rows, int64_t num_experts, const int32_t* topk_ids,
+                            int64_t k, int scoring, const int32_t* seq_offsets, int64_t num_seqs,
+                            const uint8_t* row_mask, float alpha, float* loss, int32_t* counts, float* coef,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (moe_status s = check_gate("moe_balance_loss", dtype, rows, num_experts, k, scoring)) return s;
+  if (moe_status s = check_seqs("moe_balance_loss", seq_offsets, num_seqs)) return s;
+  if (!std::isfinite(alpha)) return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: alpha must be finite");
+  if (!loss || !counts || !coef || (rows > 0 && (!logits || !topk_ids)))
+    return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: logits, topk_ids, loss, counts and coef must be non-NULL");
+  Carver cv(nullptr);
+  carve_balance(cv, rows, num_experts, num_seqs);
+  if (moe_status s = check_ws("moe_balance_loss", cv.off, workspace, workspace_bytes)) return s;
+  Carver wc(workspace);
+  moe::BalanceParams p = carve_balance(wc, rows, num_experts, num_seqs);
+  p.logits = logits; p.dtype = dtype; p.rows = rows; p.experts = (int)num_experts; p.k = (int)k;
+  p.sigmoid = scoring == MOE_GATE_SIGMOID; p.ids = topk_ids; p.off = seq_offsets; p.seqs = (int)num_seqs;
+  p.mask = row_mask; p.alpha = alpha; p.loss = loss; p.counts = counts; p.coef = coef;
+  hipError_t e = moe::launch_balance(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_balance_loss launch");
+  return ok();
+}
+
+moe_status moe_gate_backward(const void* logits, int dtype, int64_t rows, int64_t num_experts, const int32_t* topk_ids,
+                             int64_t k, int scoring, int renormalize, float scale, const float* grad_weights,
+                             const float* grad_loss, const float* coef, const int32_t* seq_offsets, int64_t num_seqs,
+                             const uint8_t* row_mask, void* grad_logits, void* stream) {
+  if (moe_status s = check_gate("moe_gate_backward", dtype, rows, num_experts, k, scoring)) return s;
+  if (moe_status s = check_seqs("moe_gate_backward", seq_offsets, num_seqs)) return s;
+  if (renormalize != 0 && renormalize != 1)
+    return fail(MOE_ERR_INVALID_ARG, "moe_gate_backward: renormalize must be 0 or 1");
+  if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARG, "moe_gate_backward: scale must be finite");
+  if (rows == 0) return ok();   // (the tensors of no rows have no address)
+  if ((grad_loss != nullptr) != (coef != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "moe_gate_backward: grad_loss and coef go together");
+  if (!grad_weights && !grad_loss)
+    return fail(MOE_ERR_INVALID_ARG, "moe_gate_backward: neither grad_weights nor grad_loss is given");
+  if (!logits || !topk_ids || !grad_logits)
+    return fail(MOE_ERR_INVALID_ARG, "moe_gate_backward: logits, topk_ids and grad_logits must be non-NULL");
+  moe::GateGradParams p;
+  p.logits = logits; p.dtype = dtype; p.rows = rows; p.experts = (int)num_experts; p.k = (int)k;
+  p.sigmoid = scoring == MOE_GATE_SIGMOID; p.renorm = renormalize != 0; p.scale = scale; p.ids = topk_ids;
+  p.grad_weights = grad_weights; p.grad_loss = grad_loss; p.coef = coef; p.off = seq_offsets; p.seqs = (int)num_seqs;
+  p.mask = row_mask; p.grad = grad_logits;
+  hipError_t e = moe::launch_gate_backward(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_gate_backward launch");
+  return ok();
+}
+
 
 moe_status moe_probe_stream(int mode, const void* src, void* dst, int64_t bytes, void* stream) {
   if (mode < 0 || mode > 2) return fail(MOE_ERR_INVALID_ARG, "moe_probe_stream: mode %d not 0, 1 or 2", mode);

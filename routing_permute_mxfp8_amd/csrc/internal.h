@@ -237,6 +237,68 @@ hipError_t launch_scatter_add(const float* o, int64_t rows, int hidden, const in
                               const float* row_weight, float* y_accum, hipStream_t stream);
 hipError_t launch_finalize(const float* acc, int64_t count, uint16_t* y, hipStream_t stream);
 
+// ---- router (gate.hip) ---------------------------------------------------------------
+// dtype: MOE_DTYPE_FP32 / _FP16 / _BF16 of logits (and of the logits' gradient). The
+// sequences of the balance loss: rows [off[b], off[b + 1]), all rows when off is null;
+// rows with mask 0 do not count. experts <= 1024, k <= 32, groups <= 64 (divides experts).
+struct GateParams {
+  const void* logits = nullptr;
+  int dtype = 0;
+  int64_t rows = 0;
+  int experts = 0, k = 0;
+  bool sigmoid = false;
+  const float* bias = nullptr;
+  int groups = 1, topk_groups = 1;
+  bool renorm = true;
+  float scale = 1.0f;
+  int32_t* ids = nullptr;
+  float* weights = nullptr;
+};
+hipError_t launch_gate(const GateParams& p, hipStream_t stream);
+
+int balance_splits(int64_t rows, int64_t seqs);
+struct BalanceParams {
+  const void* logits = nullptr;
+  int dtype = 0;
+  int64_t rows = 0;
+  int experts = 0, k = 0;
+  bool sigmoid = false;
+  const int32_t* ids = nullptr;
+  const int32_t* off = nullptr;
+  int seqs = 1, splits = 1;
+  const uint8_t* mask = nullptr;
+  float alpha = 1.0f;
+  // workspace
+  float* sums = nullptr;           // [seqs, splits, experts]
+  int32_t* part_counts = nullptr;  // [seqs, splits, experts]
+  int32_t* held = nullptr;         // [seqs, splits]
+  double* seq_loss = nullptr;      // [seqs]
+  unsigned* done = nullptr;        // [1]
+  // outputs
+  float* loss = nullptr;
+  int32_t* counts = nullptr;
+  float* coef = nullptr;
+};
+hipError_t launch_balance(const BalanceParams& p, hipStream_t stream);
+
+struct GateGradParams {
+  const void* logits = nullptr;
+  int dtype = 0;
+  int64_t rows = 0;
+  int experts = 0, k = 0;
+  bool sigmoid = false, renorm = true;
+  float scale = 1.0f;
+  const int32_t* ids = nullptr;
+  const float* grad_weights = nullptr;
+  const float* grad_loss = nullptr;
+  const float* coef = nullptr;
+  const int32_t* off = nullptr;
+  int seqs = 1;
+  const uint8_t* mask = nullptr;
+  void* grad = nullptr;
+};
+hipError_t launch_gate_backward(const GateGradParams& p, hipStream_t stream);
+
 
 // ---- static scratch of the allocation-free entry point (noalloc.hip) ---------------------
 // Bytes of the per-device scratch array moe_init_routing_noalloc uses instead of a
