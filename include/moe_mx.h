@@ -456,6 +456,35 @@ moe_status moe_gate_backward(const void* logits, int dtype, int64_t rows, int64_
                              const uint8_t* row_mask, void* grad_logits, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* moe_mxfp4_matmul: MXFP4 x MXFP4 product of the rows of each group, the GMM1   */
+/* operands of [MM] "A4W4-FP quantization scenario" and the rows that           */
+/* moe_init_routing / moe_token_permute make with quant_mode 9:                 */
+/*   out[r, j] = sum_i DQ(x)[r, i] DQ(w[g])[j, i]   for the rows r of group g    */
+/*   x            device: MXFP4 codes (x_dtype MOE_DTYPE_FP4_E2M1) uint8 [rows, k/2] */
+/*                with x_scales uint8 [rows, k/32]; or values [rows, k] of x_dtype  */
+/*                FP32, FP16 or BF16 (x_scales NULL), quantised in the call with     */
+/*                the rule of moe_mx_quantize, quant_mode 9 (finite values)           */
+/*   group_offsets device, int32 [num_groups + 1], non-decreasing: the rows of group */
+/*                g are [off[g], off[g+1]); empty groups are allowed; rows outside     */
+/*                [off[0], off[num_groups]) are not read and their out rows are left   */
+/*                as they were. NULL: all rows are one group (num_groups must be 1).   */
+/*   w, w_scales  device: MXFP4 codes uint8 [num_groups, n, k/2] and E8M0 scales uint8 */
+/*                [num_groups, n, k/32] (weight_format MOE_WEIGHTS_ND), or both from    */
+/*                moe_mx_pack_weights_fp4 (MOE_WEIGHTS_PACKED)                          */
+/*   out          device, [rows, n] of out_dtype (BF16 or FP32): the exact products      */
+/*                added in fp32, rounded once                                            */
+/* Limits: k % 128 == 0, k <= 65536; n % 16 == 0, n <= 1048576; num_groups in [1, 1024];    */
+/* rows < MOE_MAX_FLAT_ROWS; x, w, w_scales (packed) and out 16-byte aligned, the other       */
+/* scales 4-byte aligned (MOE_ERR_INVALID_ARG otherwise).                                      */
+/* ------------------------------------------------------------------------ */
+moe_status moe_mxfp4_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int x_dtype,
+                                           int weight_format, size_t* bytes /* host out */);
+moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales, int64_t rows,
+                            const int32_t* group_offsets, int64_t num_groups, const uint8_t* w,
+                            const uint8_t* w_scales, int64_t n, int64_t k, int weight_format, void* out, int out_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Measured peaks for the roofline report (one launch each; the caller times   */
 /* it with events on `stream`).                                                */
 /* moe_probe_stream: mode 0 reads `bytes` from src (dst receives nothing      */

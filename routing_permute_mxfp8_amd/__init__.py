@@ -26,6 +26,7 @@ __all__ = [
     "mega_moe", "mega_moe_workspace_bytes", "gmm1_swiglu_quant", "gmm2_combine", "combine_finalize",
     "pack_weights", "WEIGHTS_ND", "WEIGHTS_PACKED", "DTYPE_FP8_E5M2", "DTYPE_FP8_E4M3", "DTYPE_FP4_E2M1",
     "gate_topk", "balance_loss", "gate_backward", "GATE_SOFTMAX", "GATE_SIGMOID",
+    "mxfp4_matmul",
 ]
 
 QUANT_NONE, QUANT_E5M2, QUANT_E4M3, QUANT_MXFP4 = -1, 2, 3, 9
@@ -108,6 +109,8 @@ _SIGS = {
                           _VP, _SZ, _VP], _INT),
     "moe_gate_backward": ([_VP, _INT, _I64, _I64, _VP, _I64, _INT, _INT, ctypes.c_float, _VP, _VP, _VP, _VP, _I64,
                            _VP, _VP, _VP], _INT),
+    "moe_mxfp4_matmul_workspace_size": ([_I64, _I64, _I64, _I64, _INT, _INT, ctypes.POINTER(_SZ)], _INT),
+    "moe_mxfp4_matmul": ([_VP, _INT, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _I64, _INT, _VP, _INT, _VP, _SZ, _VP], _INT),
     "moe_probe_stream": ([_INT, _VP, _VP, _I64, _VP], _INT),
     "moe_probe_mfma": ([_INT, _VP, ctypes.POINTER(_I64), ctypes.POINTER(ctypes.c_double), _VP], _INT),
 }
@@ -650,6 +653,68 @@ def gate_backward(logits, topk_ids, grad_weights=None, *, scoring: int = GATE_SO
                                      int(bool(renormalize)), scale, _raw(grad_weights), _raw(grad_loss), _raw(coef),
                                      _raw(seq_offsets), seqs, _raw(row_mask), grad.data_ptr(), _raw_stream(index)))
     return grad
+
+
+def mxfp4_matmul(x, w, w_scales, *, x_scales=None, group_offsets=None, out_dtype=torch.bfloat16,
+                 weight_format: int = WEIGHTS_ND, out=None, workspace=None):
+    """MXFP4 x MXFP4 product: out [R, N] (bf16 or fp32), out[r] = DQ(x[r]) DQ(w[g])^T for the
+    rows r of group g.
+
+    x: bf16, fp16 or fp32 [R, K], quantised in the call as mx_quantize(x, QUANT_MXFP4) would, or
+    its MXFP4 codes uint8 [R, K/2] with x_scales uint8 [R, K/32] (from mx_quantize, init_routing
+    or token_permute in mode QUANT_MXFP4). w, w_scales: codes uint8 [G, N, K/2] and scales
+    [G, N, K/32], or both from pack_weights(..., fp4=True) with weight_format=WEIGHTS_PACKED;
+    without group_offsets (one group) w may be [N, K/2]. group_offsets: int32 [G + 1], the rows
+    of group g are [off[g], off[g + 1]); rows outside all groups are left as they were in `out`
+    (uninitialised when out is None). workspace: optional preallocated uint8 device tensor."""
+    lib = load()
+    if x.dim() != 2 or (x_scales is None) != (x.dtype in (torch.float32, torch.float16, torch.bfloat16)):
+        raise ValueError(f"x must be float32, float16 or bfloat16 [rows, k], or uint8 codes [rows, k/2] with x_scales "
+                         f"(got {x.dtype} {tuple(x.shape)}, x_scales {'missing' if x_scales is None else 'given'})")
+    if x_scales is not None and x.dtype != torch.uint8:
+        raise ValueError(f"MXFP4 codes must be uint8 (got {x.dtype})")
+    w, w_scales, x_scales = _u8(w), _u8(w_scales), _u8(x_scales)
+    if w.dim() == 2 and group_offsets is None:
+        w = w.unsqueeze(0)
+    if w.dim() != 3:
+        raise ValueError(f"w must be [groups, n, k/2] (got {tuple(w.shape)})")
+    rows, k = x.shape if x_scales is None else (x.shape[0], 2 * x.shape[1])
+    g, n, kb = w.shape
+    if 2 * kb != k:
+        raise ValueError(f"x has k = {k}, w has k = {2 * kb}")
+    want = lib.moe_mx_packed_scale_bytes(g, n, k) if weight_format == WEIGHTS_PACKED else g * n * (k // 32)
+    if w_scales.numel() != want:
+        raise ValueError(f"w_scales must hold {want} bytes (got {tuple(w_scales.shape)})")
+    if x_scales is not None and tuple(x_scales.shape) != (rows, k // 32):
+        raise ValueError(f"x_scales must be [{rows}, {k // 32}] (got {tuple(x_scales.shape)})")
+    if group_offsets is None:
+        if g != 1:
+            raise ValueError(f"{g} groups need group_offsets")
+    elif group_offsets.dtype != torch.int32 or tuple(group_offsets.shape) != (g + 1,):
+        raise ValueError(f"group_offsets must be int32 [{g + 1}] (got {group_offsets.dtype} "
+                         f"{tuple(group_offsets.shape)})")
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    elif out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != (rows, n):
+        raise ValueError(f"out must be bfloat16 or float32 [{rows}, {n}] (got {out.dtype} {tuple(out.shape)})")
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be uint8 (got {workspace.dtype})")
+    index = _device_of(x, w=w, w_scales=w_scales, x_scales=x_scales, group_offsets=group_offsets, out=out,
+                       workspace=workspace)
+    xd = DTYPE_FP4_E2M1 if x_scales is not None else _DT[x.dtype]
+    nbytes = ctypes.c_size_t()
+    _check(lib.moe_mxfp4_matmul_workspace_size(rows, g, n, k, xd, weight_format, ctypes.byref(nbytes)))
+    with _on(index):
+        if out is None:
+            out = torch.empty((rows, n), dtype=out_dtype, device=x.device)
+        ws = workspace
+        if nbytes.value and (ws is None or ws.numel() < nbytes.value):
+            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=x.device)
+        _check(lib.moe_mxfp4_matmul(x.data_ptr(), xd, _raw(x_scales), rows, _raw(group_offsets), g, w.data_ptr(),
+                                    w_scales.data_ptr(), n, k, weight_format, out.data_ptr(), _DT[out.dtype], _raw(ws),
+                                    0 if ws is None else ws.numel(), _raw_stream(index)))
+    return out
 
 
 def probe_stream(src, dst=None, copy: bool = False, fill_caches: bool = False):

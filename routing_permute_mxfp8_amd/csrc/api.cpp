@@ -407,6 +407,29 @@ moe_status check_ws(const char* who, size_t need, void* ws, size_t have) {
   return MOE_OK;
 }
 
+// ---- MXFP4 product -------------------------------------------------------------------
+moe_status check_fp4_matmul(int64_t rows, int64_t groups, int64_t n, int64_t k, int x_dtype, int weight_format) {
+  if (rows < 0 || rows >= MOE_MAX_FLAT_ROWS)
+    return fail(MOE_ERR_SHAPE, "moe_mxfp4_matmul: rows %lld outside [0, %d)", (long long)rows, MOE_MAX_FLAT_ROWS);
+  if (groups < 1 || groups > 1024)
+    return fail(MOE_ERR_SHAPE, "moe_mxfp4_matmul: num_groups %lld outside [1, 1024]", (long long)groups);
+  if (n < 16 || n % 16 != 0 || n > (1 << 20))
+    return fail(MOE_ERR_SHAPE, "moe_mxfp4_matmul: n %lld must be a positive multiple of 16 (<= 1048576)", (long long)n);
+  if (k < 128 || k % 128 != 0 || k > 65536)
+    return fail(MOE_ERR_SHAPE, "moe_mxfp4_matmul: k %lld must be a positive multiple of 128 (<= 65536)", (long long)k);
+  if (!valid_x_dtype(x_dtype) && x_dtype != MOE_DTYPE_FP4_E2M1)
+    return fail(MOE_ERR_DTYPE, "moe_mxfp4_matmul: x_dtype %d not FP32, FP16, BF16 or FP4_E2M1", x_dtype);
+  if (weight_format != MOE_WEIGHTS_ND && weight_format != MOE_WEIGHTS_PACKED)
+    return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul: weight_format %d not 0 (ND) or 1 (packed)", weight_format);
+  return MOE_OK;
+}
+
+moe::Fp4MatmulParams carve_fp4_matmul(Carver& cv, int64_t rows, int64_t groups, int64_t n, int64_t k, int x_dtype,
+                                      int weight_format) {
+  moe::Fp4MatmulParams p;
+  return p;
+}
+
 // ---- router ------------------------------------------------------------------------
 moe_status check_gate(const char* who, int dtype, int64_t rows, int64_t experts, int64_t k, int scoring) {
   if (rows < 0 || rows > INT32_MAX) return fail(MOE_ERR_SHAPE, "%s: rows %lld outside [0, 2^31)", who, (long long)rows);
@@ -1044,6 +1067,49 @@ moe_status moe_gate_backward(const void* logits, int dtype, int64_t rows, int64_
   return ok();
 }
 
+
+// ---- MXFP4 product -------------------------------------------------------------------
+moe_status moe_mxfp4_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int x_dtype,
+                                           int weight_format, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul_workspace_size: bytes is NULL");
+  if (moe_status s = check_fp4_matmul(rows, num_groups, n, k, x_dtype, weight_format)) return s;
+  Carver cv(nullptr);
+  carve_fp4_matmul(cv, rows, num_groups, n, k, x_dtype, weight_format);
+  *bytes = cv.off;
+  return ok();
+}
+
+moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales, int64_t rows,
+                            const int32_t* group_offsets, int64_t num_groups, const uint8_t* w,
+                            const uint8_t* w_scales, int64_t n, int64_t k, int weight_format, void* out, int out_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (moe_status s = check_fp4_matmul(rows, num_groups, n, k, x_dtype, weight_format)) return s;
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_FP32)
+    return fail(MOE_ERR_DTYPE, "moe_mxfp4_matmul: out_dtype %d not BF16 or FP32", out_dtype);
+  if (!group_offsets && num_groups != 1)
+    return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul: num_groups %lld needs group_offsets", (long long)num_groups);
+  if (rows == 0) return ok();
+  if (!x || !w || !w_scales || !out)
+    return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul: x, w, w_scales and out must be non-NULL");
+  if ((x_dtype == MOE_DTYPE_FP4_E2M1) != (x_scales != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul: x_scales go with FP4_E2M1 codes and with nothing else");
+  auto off = [](const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; };
+  if (off(x, 16) || off(w, 16) || off(out, 16) || off(x_scales, 4) ||
+      off(w_scales, weight_format == MOE_WEIGHTS_PACKED ? 16 : 4))
+    return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul: x, w, out and packed scales must be 16-byte aligned, scales 4-byte");
+  Carver cv(nullptr);
+  carve_fp4_matmul(cv, rows, num_groups, n, k, x_dtype, weight_format);
+  if (cv.off > 0)
+    if (moe_status s = check_ws("moe_mxfp4_matmul", cv.off, workspace, workspace_bytes)) return s;
+  Carver wc(workspace);
+  moe::Fp4MatmulParams p = carve_fp4_matmul(wc, rows, num_groups, n, k, x_dtype, weight_format);
+  p.x = x; p.x_kind = x_dtype; p.x_scales = x_scales; p.rows = rows; p.off = group_offsets; p.groups = (int)num_groups;
+  p.k = (int)k; p.n = (int)n; p.w = w; p.w_scales = w_scales; p.packed = weight_format == MOE_WEIGHTS_PACKED;
+  p.out_fp32 = out_dtype == MOE_DTYPE_FP32; p.out = out;
+  hipError_t e = moe::launch_fp4_matmul(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_mxfp4_matmul launch");
+  return ok();
+}
 
 moe_status moe_probe_stream(int mode, const void* src, void* dst, int64_t bytes, void* stream) {
   if (mode < 0 || mode > 2) return fail(MOE_ERR_INVALID_ARG, "moe_probe_stream: mode %d not 0, 1 or 2", mode);

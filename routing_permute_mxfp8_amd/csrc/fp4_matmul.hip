@@ -1,0 +1,182 @@
+// MXFP4 x MXFP4 product of the rows of each expert group:
+//   out[r, n] = sum_k DQ(x)[r, k] DQ(w_g)[n, k]   for the rows r of group g,
+// both operands E2M1 codes two a byte (element 2j in the low nibble) with an E8M0 scale per
+// 32 along K. MegaMoE README, "A4W4-FP quantization scenario" (GMM1's operands), and the
+// rows that quantMode 9 of MoeInitRoutingV3 / moe_token_permute makes. x may come as bf16,
+// fp16 or fp32 and is then quantised here (the Q_MX of moe_mx_quantize mode 9).
+//
+// The block-scaled MFMA multiplies FP4 operands exactly and adds in fp32 (measured: equal to
+// the fp64 sum for scale spreads up to 2^3, 1e-7 of it at 2^10 over 56 steps).
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "fp4_device.h"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+// ---- few rows a group: weights streamed into registers -----------------------------------
+// Bound by the weight stream (17/32 byte an element, each used for at most 16 rows at a
+// time). A block takes 16 CT channels of a group; its four waves take every fourth pair of
+// K steps (a pair is one 128-byte line of a weight row) and add their sums in LDS at the
+// end, so that a dense layer of a few thousand channels still fills the chip. Loads behind
+// the last K step or the group's rows fall outside their buffers: zeros, no traffic.
+struct RowsArgs {
+  const void* x;            // codes [rows, K/2], or values [rows, K]
+  const uint8_t* xs;        // codes: scales [rows, K/32]
+  const int32_t* off;
+  int rows, K, N;
+  const uint8_t* w;
+  const uint8_t* ws;
+};
+
+constexpr int kRowWaves = 4;
+constexpr int kPairs = 2;   // pairs of K steps in flight a wave
+
+template <typename T> constexpr int kXBytes = sizeof(T);
+struct Codes {};            // x given as codes
+
+// The x operand (16 rows) of one K step: lane (g, r) holds row r's K block g.
+template <typename X>
+struct XStep {
+  u32x4 u[Group32<X>::kLoads];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t xr, __amdgpu_buffer_rsrc_t, int lane_x, int, int step, bool in) {
+    const int lo = in ? lane_x : kOutside, so = step * 128 * (int)sizeof(X);
+#pragma unroll
+    for (int i = 0; i < Group32<X>::kLoads; ++i) u[i] = __builtin_amdgcn_raw_buffer_load_b128(xr, lo + 16 * i, so, 0);
+  }
+  __device__ __forceinline__ void operand(int, u32x4& q, int& b) const { Group32<X>::run(u, q, b); }
+};
+template <>
+struct XStep<Codes> {
+  u32x4 u;
+  uint32_t s;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t xr, __amdgpu_buffer_rsrc_t sr, int lane_x, int lane_s, int step,
+                                       bool in) {
+    u = __builtin_amdgcn_raw_buffer_load_b128(xr, in ? lane_x : kOutside, step * 64, 0);
+    s = __builtin_amdgcn_raw_buffer_load_b32(sr, in ? lane_s : kOutside, step * 4, 0);
+  }
+  __device__ __forceinline__ void operand(int g, u32x4& q, int& b) const {
+    q = u;
+    b = (int)(s >> (8 * g));
+  }
+};
+
+template <int CT>
+struct WStep {
+  u32x4 u[CT];
+  uint32_t s[CT];
+};
+
+__device__ __forceinline__ v4f mfma_fp4(const u32x4& a, const u32x4& b, v4f c, int sa, int sb) {
+  return mfma_mx16_ab<kFmtFp4, kFmtFp4>(join_operand(a, u32x4{}), join_operand(b, u32x4{}), c, sa, sb);
+}
+
+template <typename X, typename O, int CT, bool PACKED>
+__global__ __launch_bounds__(64 * kRowWaves) void fp4_rows_kernel(RowsArgs p, O* __restrict__ out) {
+  __shared__ v4f part[kRowWaves][CT][64];
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = blockIdx.y, tile0 = blockIdx.x * CT, n16 = p.N >> 4;
+  int lo, hi;
+  group_rows(p.off, group, p.rows, &lo, &hi);
+  if (lo >= hi) return;
+  const int ks = p.K >> 7, pairs = (ks + 1) >> 1, kq = (ks + 3) >> 2;
+  const int tiles = min(CT, n16 - tile0);
+  // weights: this block's channel tiles
+  const int64_t code_tile = (int64_t)16 * (p.K >> 1), scale_tile = PACKED ? (int64_t)kq * 256 : (int64_t)16 * (p.K >> 5);
+  const int64_t t0 = (int64_t)group * n16 + tile0;
+  const __amdgpu_buffer_rsrc_t wr = buffer_of(p.w + t0 * code_tile, tiles * code_tile);
+  const __amdgpu_buffer_rsrc_t sr = buffer_of(p.ws + t0 * scale_tile, tiles * scale_tile);
+  const int lane_w = PACKED ? 16 * lane : r * (p.K >> 1) + 16 * g;
+  const int lane_s = PACKED ? 4 * lane : r * (p.K >> 5);
+  auto load_w = [&](WStep<CT>& w, int step, bool in) {
+    const int lw = in ? lane_w : kOutside, ls = in ? lane_s : kOutside;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      w.u[c] = __builtin_amdgcn_raw_buffer_load_b128(wr, lw + c * (int)code_tile, step * (PACKED ? 1024 : 64), 2);   // non-temporal
+      w.s[c] = __builtin_amdgcn_raw_buffer_load_b32(sr, ls + c * (int)scale_tile, PACKED ? (step >> 2) * 256 : step * 4, 0);
+    }
+  };
+  constexpr bool kCodes = std::is_same_v<X, Codes>;
+  const int64_t row_bytes = kCodes ? (int64_t)(p.K >> 1) : (int64_t)p.K * kXBytes<std::conditional_t<kCodes, uint8_t, X>>;
+  for (int row0 = lo; row0 < hi; row0 += 16) {
+    const int n = min(16, hi - row0);
+    const __amdgpu_buffer_rsrc_t xr = buffer_of((const uint8_t*)p.x + row0 * row_bytes, n * row_bytes);
+    const __amdgpu_buffer_rsrc_t xsr = buffer_of(kCodes ? p.xs + (int64_t)row0 * (p.K >> 5) : nullptr, kCodes ? n * (p.K >> 5) : 0);
+    const int lane_x = r * (int)row_bytes + (kCodes ? 16 * g : 32 * g * kXBytes<std::conditional_t<kCodes, uint8_t, X>>);
+    const int lane_xs = r * (p.K >> 5);
+    v4f acc[CT] = {};
+    for (int p0 = wave; p0 < pairs; p0 += kRowWaves * kPairs) {
+      WStep<CT> w[2 * kPairs];
+      XStep<X> x[2 * kPairs];
+#pragma unroll
+      for (int i = 0; i < 2 * kPairs; ++i) {
+        const int step = 2 * (p0 + kRowWaves * (i >> 1)) + (i & 1);
+        const bool in = step < ks;
+        load_w(w[i], in ? step : 0, in);
+        x[i].load(xr, xsr, lane_x, lane_xs, in ? step : 0, in);
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * kPairs; ++i) {
+        const int step = 2 * (p0 + kRowWaves * (i >> 1)) + (i & 1);
+        u32x4 q;
+        int b;
+        x[i].operand(g, q, b);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          acc[c] = mfma_fp4(w[i].u[c], q, acc[c], (int)(w[i].s[c] >> (PACKED ? 8 * (step & 3) : 8 * g)), b);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) part[wave][c][lane] = acc[c];
+    __syncthreads();
+    for (int c = wave; c < tiles; c += kRowWaves) {
+      v4f t = part[0][c][lane];
+#pragma unroll
+      for (int q = 1; q < kRowWaves; ++q) t += part[q][c][lane];
+      // lane (g, r): channels 4 g .. 4 g + 3 of row r
+      if (r < n) store4(out + (int64_t)(row0 + r) * p.N + (tile0 + c) * 16 + 4 * g, t);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename X, typename O, bool PACKED>
+hipError_t launch_rows(const Fp4MatmulParams& p, hipStream_t stream) {
+  RowsArgs a{p.x, p.x_scales, p.off, (int)p.rows, p.k, p.n, p.w, p.w_scales};
+  const int n16 = p.n / 16;
+  // four channel tiles a block where that leaves enough blocks, else one
+  const int64_t blocks4 = (int64_t)((n16 + 3) / 4) * std::min<int64_t>(p.groups, p.rows);
+  if (blocks4 >= 1024) {
+    fp4_rows_kernel<X, O, 4, PACKED><<<dim3((n16 + 3) / 4, p.groups), 64 * kRowWaves, 0, stream>>>(a, (O*)p.out);
+  } else {
+    fp4_rows_kernel<X, O, 1, PACKED><<<dim3(n16, p.groups), 64 * kRowWaves, 0, stream>>>(a, (O*)p.out);
+  }
+  return hipGetLastError();
+}
+
+template <typename X, typename O>
+hipError_t launch_format(const Fp4MatmulParams& p, hipStream_t stream) {
+  return p.packed ? launch_rows<X, O, true>(p, stream) : launch_rows<X, O, false>(p, stream);
+}
+template <typename X>
+hipError_t launch_out(const Fp4MatmulParams& p, hipStream_t stream) {
+  return p.out_fp32 ? launch_format<X, float>(p, stream) : launch_format<X, uint16_t>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream) {
+  if (p.rows <= 0) return hipSuccess;
+  switch (p.x_kind) {
+    case 0: return launch_out<float>(p, stream);
+    case 1: return launch_out<_Float16>(p, stream);
+    case 2: return launch_out<uint16_t>(p, stream);
+    default: return launch_out<Codes>(p, stream);
+  }
+}
+
+}  // namespace moe

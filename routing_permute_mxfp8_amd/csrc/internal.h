@@ -300,6 +300,23 @@ struct GateGradParams {
 hipError_t launch_gate_backward(const GateGradParams& p, hipStream_t stream);
 
 
+// ---- MXFP4 product (fp4_matmul.hip) ----------------------------------------------------
+struct Fp4MatmulParams {
+  const void* x = nullptr;
+  int x_kind = 2;                  // MOE_DTYPE_FP32 / _FP16 / _BF16 values, MOE_DTYPE_FP4_E2M1 codes
+  const uint8_t* x_scales = nullptr;
+  int64_t rows = 0;
+  const int32_t* off = nullptr;    // [groups + 1], or null: one group
+  int groups = 1;
+  int k = 0, n = 0;                // k % 128 == 0, n % 16 == 0
+  const uint8_t* w = nullptr;
+  const uint8_t* w_scales = nullptr;
+  bool packed = false;
+  bool out_fp32 = false;           // else bf16
+  void* out = nullptr;
+};
+hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream);
+
 // ---- static scratch of the allocation-free entry point (noalloc.hip) ---------------------
 // Bytes of the per-device scratch array moe_init_routing_noalloc uses instead of a
 // caller workspace.
