@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libmoe_mx.so"
 SOURCES = ["csrc/api.cpp", "csrc/routing.hip", "csrc/permute_quant.hip", "csrc/tiles.hip", "csrc/gmm.hip",
            "csrc/gmm_stream.hip", "csrc/combine.hip", "csrc/peaks.hip", "csrc/noalloc.hip", "csrc/gate.hip",
-           "csrc/fp4_matmul.hip"]
+           "csrc/fp4_matmul.hip", "csrc/fp4_tile.hip"]
 ARCH = os.environ.get("MOE_MX_ARCH", "gfx950")
 
 
@@ -32,7 +32,7 @@ FLAGS = [
     # keep fp32 denormals: MX quantization of subnormal bf16 inputs depends on them
     "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-Wno-unused-result",
+    "-Wno-unused-result", "-Werror=return-type",
 ]
 NOISE = "is not a recognized feature for this target"
 

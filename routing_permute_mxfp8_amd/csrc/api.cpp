@@ -424,9 +424,13 @@ moe_status check_fp4_matmul(int64_t rows, int64_t groups, int64_t n, int64_t k, 
   return MOE_OK;
 }
 
-moe::Fp4MatmulParams carve_fp4_matmul(Carver& cv, int64_t rows, int64_t groups, int64_t n, int64_t k, int x_dtype,
-                                      int weight_format) {
+moe::Fp4MatmulParams carve_fp4_matmul(Carver& cv, int64_t rows, int64_t groups, int64_t n, int64_t k, int x_dtype) {
   moe::Fp4MatmulParams p;
+  p.mt = moe::fp4_tile_rows(rows, groups, n, k);
+  if (p.mt != 0 && x_dtype != MOE_DTYPE_FP4_E2M1) {
+    p.x_codes = cv.take<uint8_t>((size_t)(rows * (k / 2)));
+    p.x_code_scales = cv.take<uint8_t>((size_t)(rows * (k / 32)));
+  }
   return p;
 }
 
@@ -1074,7 +1078,7 @@ moe_status moe_mxfp4_matmul_workspace_size(int64_t rows, int64_t num_groups, int
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul_workspace_size: bytes is NULL");
   if (moe_status s = check_fp4_matmul(rows, num_groups, n, k, x_dtype, weight_format)) return s;
   Carver cv(nullptr);
-  carve_fp4_matmul(cv, rows, num_groups, n, k, x_dtype, weight_format);
+  carve_fp4_matmul(cv, rows, num_groups, n, k, x_dtype);
   *bytes = cv.off;
   return ok();
 }
@@ -1098,11 +1102,11 @@ moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales,
       off(w_scales, weight_format == MOE_WEIGHTS_PACKED ? 16 : 4))
     return fail(MOE_ERR_INVALID_ARG, "moe_mxfp4_matmul: x, w, out and packed scales must be 16-byte aligned, scales 4-byte");
   Carver cv(nullptr);
-  carve_fp4_matmul(cv, rows, num_groups, n, k, x_dtype, weight_format);
+  carve_fp4_matmul(cv, rows, num_groups, n, k, x_dtype);
   if (cv.off > 0)
     if (moe_status s = check_ws("moe_mxfp4_matmul", cv.off, workspace, workspace_bytes)) return s;
   Carver wc(workspace);
-  moe::Fp4MatmulParams p = carve_fp4_matmul(wc, rows, num_groups, n, k, x_dtype, weight_format);
+  moe::Fp4MatmulParams p = carve_fp4_matmul(wc, rows, num_groups, n, k, x_dtype);
   p.x = x; p.x_kind = x_dtype; p.x_scales = x_scales; p.rows = rows; p.off = group_offsets; p.groups = (int)num_groups;
   p.k = (int)k; p.n = (int)n; p.w = w; p.w_scales = w_scales; p.packed = weight_format == MOE_WEIGHTS_PACKED;
   p.out_fp32 = out_dtype == MOE_DTYPE_FP32; p.out = out;

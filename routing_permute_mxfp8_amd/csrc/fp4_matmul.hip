@@ -169,8 +169,15 @@ hipError_t launch_out(const Fp4MatmulParams& p, hipStream_t stream) {
 
 }  // namespace
 
+int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k) {
+  const int64_t per = (rows + groups - 1) / groups;
+  if (per <= 16) return 0;
+  return per <= 64 ? 64 : per <= 128 ? 128 : 256;
+}
+
 hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream) {
   if (p.rows <= 0) return hipSuccess;
+  if (p.mt) return launch_fp4_tiles(p, stream);
   switch (p.x_kind) {
     case 0: return launch_out<float>(p, stream);
     case 1: return launch_out<_Float16>(p, stream);

@@ -1,0 +1,469 @@
+// MXFP4 x MXFP4 product of expert groups of many rows: both operands staged in LDS.
+//
+// A work item is a tile of MT rows of one group by 256 output channels, computed by four
+// waves (one per SIMD), each holding CB x RB accumulators of 32 channels x 32 rows
+// (V_MFMA_SCALE_F32_32X32X64_F8F6F4, weights in the A slot: a lane holds 4 consecutive
+// channels of one row). Blocks are persistent and XCD-aware.
+//
+// FP4 doubles the MFMA's rate against FP8 at the same operand rows, so the LDS reads are
+// what a wave's tile shape decides: 128 x 128 a wave takes 64 of the 128 bytes a clock the
+// CU's LDS delivers, 128 x 64 takes 96, 64 x 64 all of them. One wave a SIMD with 256
+// accumulator registers is therefore better than more, smaller waves.
+//
+// Per K step of 128 the codes of 256 weight rows and MT rows of x go straight from memory
+// into one of four LDS slots, issued four steps ahead, and are read from there half a step
+// ahead of their MFMAs; one barrier a step, between its two halves. The loads go on across
+// items, so an item's first steps are under way while the last ones of the item before are
+// multiplied. The E8M0 scales of four steps (a quad) come through registers, 16 bytes a row.
+//
+// LDS rows hold 64 bytes, four 16-byte chunks (32 K elements each); chunk c of row r sits at
+// place c ^ (r / 2 % 4), so that the eight lanes of a read pass (eight rows, one chunk) touch
+// all banks once. The direct-to-LDS loads write linearly; their lanes fetch the chunk that
+// belongs at their place, wherever the weight format has it.
+
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "device_common.h"
+#include "fp4_device.h"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// ---- x given as values: its codes and scales ----------------------------------------------
+// One thread per group of 32; row-major codes [rows, K/2] and scales [rows, K/32].
+template <typename X>
+__global__ __launch_bounds__(256) void fp4_quantise_kernel(const X* __restrict__ x, int64_t groups,
+                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= groups) return;
+  constexpr int L = Group32<X>::kLoads;
+  u32x4 u[L], c;
+  const u32x4* src = reinterpret_cast<const u32x4*>(x + 32 * i);
+#pragma unroll
+  for (int j = 0; j < L; ++j) u[j] = src[j];
+  int b;
+  Group32<X>::run(u, c, b);
+  reinterpret_cast<u32x4*>(codes)[i] = c;
+  scales[i] = (uint8_t)b;
+}
+
+// ---- product --------------------------------------------------------------------------------
+struct TileArgs {
+  const uint8_t* x;         // codes [rows, K/2]
+  const uint8_t* xs;        // scales [rows, K/32]
+  const uint8_t* w;
+  const uint8_t* ws;
+  const int32_t* off;
+  int groups, rows, K, N;
+};
+
+constexpr int kNT = 256;          // channels of an item
+constexpr int kThreads = 256;
+constexpr int kMaxGroups = 1024;
+constexpr int kList = kThreads;   // items described at a time
+constexpr int kSlots = 4;         // K steps staged in LDS
+
+// WC waves along the channels, 4 / WC along the rows; RB 32-row blocks a wave.
+template <int WC, int RB>
+struct TileShape {
+  static constexpr int kCB = kNT / 32 / WC;             // 32-channel blocks a wave
+  static constexpr int kMT = 4 / WC * RB * 32;
+  static constexpr int kA = kNT * 64, kB = kMT * 64;    // bytes of a step: weights, rows
+  static constexpr int kStep = kA + kB;
+  static constexpr int kSA = kNT * 16, kSB = kMT * 16;  // bytes of a quad's scales
+  static constexpr int kQuad = kSA + kSB;
+  static constexpr int kScales = kSlots * kStep, kEnds = kScales + 2 * kQuad, kItems = kEnds + 4 * kMaxGroups;
+  static constexpr int kLds = kItems + 16 * kList;
+  static constexpr int kLA = kNT / 64, kLB = kMT / 64;   // direct-to-LDS loads a wave and step (16 rows each)
+  static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
+  static_assert(kMT <= kThreads && kMT % 64 == 0, "rows of an item");
+};
+
+// Keeps the accumulators in accumulation registers across loop edges (left to itself the
+// allocator moves most of them to vector registers and back around each quad, and spills).
+template <int CB, int RB>
+__device__ __forceinline__ void pin(v16f (&acc)[CB][RB]) {
+#pragma unroll
+  for (int i = 0; i < CB; ++i)
+#pragma unroll
+    for (int j = 0; j < RB; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// Waits for the wave's direct-to-LDS loads but the newest N vector memory operations and for
+// its LDS accesses, then for the other waves: what was loaded or written is there for all,
+// and what was read may be written again. (vmcnt counts in order.)
+template <int N>
+__device__ __forceinline__ void slot_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// ends[g] = tiles of groups 0 .. g (all threads; ends has room for kMaxGroups). Returns the
+// number of tiles.
+template <int MT>
+__device__ __forceinline__ int count_tiles(const TileArgs& p, int* ends, int* scratch) {
+  const int t = threadIdx.x, lane = t & 63;
+  int n[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = 4 * t + i;
+    int lo = 0, hi = 0;
+    if (g < p.groups) group_rows(p.off, g, p.rows, &lo, &hi);
+    sum += (hi - lo + MT - 1) / MT;
+    n[i] = sum;
+  }
+  int incl = sum;
+  for (int s = 1; s < 64; s *= 2) {
+    const int v = __shfl_up(incl, s, 64);
+    incl += lane >= s ? v : 0;
+  }
+  if (lane == 63) scratch[t >> 6] = incl;
+  __syncthreads();
+  int base = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    base += w < (t >> 6) ? scratch[w] : 0;
+    total += scratch[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ends[4 * t + i] = base + n[i];
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+struct Item {
+  int group, row0, rows, cb;
+};
+
+// Item `it` of the (tile, channel block) list: four tiles run through the channel blocks
+// together, so that the items in flight on one XCD share weights as well as rows in its L2.
+template <int MT>
+__device__ __forceinline__ int4 describe(const TileArgs& p, const int* ends, int tiles, int ncb, int it) {
+  const int block = it / (4 * ncb), in = it - block * 4 * ncb;
+  const int width = min(4, tiles - 4 * block);
+  const int cb = in / width, t = 4 * block + in - cb * width;
+  int g = 0;   // the first group that ends behind tile t
+  for (int s = kMaxGroups / 2; s > 0; s /= 2)
+    if (g + s <= p.groups - 1 && ends[g + s - 1] <= t) g += s;
+  int lo, hi;
+  group_rows(p.off, g, p.rows, &lo, &hi);
+  const int row0 = lo + (t - (g > 0 ? ends[g - 1] : 0)) * MT;
+  return make_int4(g, row0, min(MT, hi - row0), cb);
+}
+
+// The body gets the LDS area twice, as two restrict pointers: one for the direct-to-LDS
+// loads, one for every other access. The compiler then does not make each LDS read wait for
+// every direct-to-LDS load in flight; slot_barrier orders them.
+template <int WC, int RB, typename O, bool PACKED>
+__device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out, uint8_t* __restrict__ dma,
+                                          uint8_t* __restrict__ lds) {
+  using S = TileShape<WC, RB>;
+  constexpr int CB = S::kCB, MT = S::kMT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wc = wave % WC, wr = wave / WC;
+  const int ks = p.K >> 7, kq = (ks + 3) >> 2, half = p.K >> 1, n16 = p.N >> 4;
+  const int ncb = (p.N + kNT - 1) / kNT;
+  int* const ends = reinterpret_cast<int*>(lds + S::kEnds);
+  int4* const list = reinterpret_cast<int4*>(lds + S::kItems);
+
+  const int tiles = count_tiles<MT>(p, ends, reinterpret_cast<int*>(list));
+  // each XCD takes a contiguous share of the items, dealt to its blocks in turn
+  const int64_t total = (int64_t)tiles * ncb;
+  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
+  const int64_t begin = total * xcd / 8 + (blockIdx.x >> 3), end = total * (xcd + 1) / 8;
+  if (begin >= end) return;   // the whole block
+  const int count = (int)((end - begin + per - 1) / per);
+  auto fill = [&](int first) {   // list[i] = this block's item first + i
+    __syncthreads();
+    if (first + tid < count) list[tid] = describe<MT>(p, ends, tiles, ncb, (int)(begin + (int64_t)(first + tid) * per));
+    __syncthreads();
+  };
+  auto item = [&](int i) {
+    const int4 v = list[i % kList];
+    return Item{__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w)};
+  };
+
+  // code loads: load i of a wave fills 16 rows, lane l place l % 4 of row l / 4
+  const int row_l = lane >> 2, chunk_l = (lane & 3) ^ ((lane >> 3) & 3);
+  int va[S::kLA], vb[S::kLB];
+#pragma unroll
+  for (int i = 0; i < S::kLA; ++i)
+    va[i] = (wave * S::kLA + i) * 16 * half + (PACKED ? chunk_l * 256 + row_l * 16 : row_l * half + chunk_l * 16);
+#pragma unroll
+  for (int i = 0; i < S::kLB; ++i) vb[i] = ((wave * S::kLB + i) * 16 + row_l) * half + chunk_l * 16;
+
+  // The item whose loads are being issued: buffers of exactly its rows (what lies behind
+  // reads as zeros, without memory traffic).
+  const uint8_t *bw, *bx, *bws, *bxs;
+  int wbytes, xbytes;
+  uint32_t vsa, vsb;
+  auto aim = [&](const Item& it) {
+    const int c16 = min(kNT / 16, n16 - it.cb * (kNT / 16));
+    const int64_t wt = (int64_t)it.group * n16 + it.cb * (kNT / 16);   // 16-channel tile of the item
+    bw = p.w + wt * 16 * half;
+    wbytes = c16 * 16 * half;
+    bx = p.x + (int64_t)it.row0 * half;
+    xbytes = it.rows * half;
+    bws = p.ws + wt * (PACKED ? kq * 256 : 64 * ks);
+    bxs = p.xs + (int64_t)it.row0 * (4 * ks);
+    const int ra = min(tid, c16 * 16 - 1), rb = min(tid, it.rows - 1);
+    vsa = PACKED ? (uint32_t)((ra >> 4) * kq * 256 + (ra & 15) * 4) : (uint32_t)(ra * 4 * ks);
+    vsb = (uint32_t)(rb * 4 * ks);
+  };
+  auto issue_step = [&](int slot, int step, bool in) {   // !in: zeros
+    const __amdgpu_buffer_rsrc_t wr_ = buffer_of(bw, in ? wbytes : 0), xr_ = buffer_of(bx, in ? xbytes : 0);
+    uint8_t* base = dma + slot * S::kStep;
+    const int s = in ? step : 0;
+#pragma unroll
+    for (int i = 0; i < S::kLA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr_, (lds_ptr)(base + (wave * S::kLA + i) * 1024), 16, va[i],
+                                               s * (PACKED ? 1024 : 64), 0, 0);
+#pragma unroll
+    for (int i = 0; i < S::kLB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr_, (lds_ptr)(base + S::kA + (wave * S::kLB + i) * 1024), 16, vb[i],
+                                               s * 64, 0, 0);
+  };
+  // The scales of a quad: thread t holds row t's 16 bytes, dword j the four blocks of step j
+  // (the packed weight scales come as dword g = block g of the four steps and are transposed).
+  // The last quad's 16 bytes may reach past the row's end, and of the last rows past the
+  // buffer's: those lanes read up to 12 bytes before their place and shift.
+  u32x4 qa, qx;
+  int early_a = 0, early_x = 0;   // bytes before the place
+  const int64_t ws_bytes = (int64_t)p.groups * p.N * 4 * ks, xs_bytes = (int64_t)p.rows * 4 * ks;
+  typedef u32x4 __attribute__((aligned(4))) u32x4_a4;
+  auto load_scales = [&](int q) {
+    if constexpr (PACKED) {
+      const uint8_t* s = bws + q * 256;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) qa[g] = *reinterpret_cast<const uint32_t*>(s + (vsa + 64 * g));
+    } else {
+      const int room = (int)min((int64_t)INT32_MAX, p.ws + ws_bytes - 16 - bws);   // a read may start here at the latest
+      const int at = (int)vsa + 16 * q;
+      early_a = max(at - room, 0);
+      qa = *reinterpret_cast<const u32x4_a4*>(bws + (uint32_t)(at - early_a));
+    }
+    const int room = (int)min((int64_t)INT32_MAX, p.xs + xs_bytes - 16 - bxs);
+    // (may be negative: the item's first row can lie within the last 16 bytes)
+    const int at = (int)vsb + 16 * q;
+    early_x = max(at - room, 0);
+    qx = *reinterpret_cast<const u32x4_a4*>(bxs + (int64_t)(at - early_x));
+  };
+  // dwords shifted down by `early` bytes (0, 4, 8, 12), zeros behind
+  auto shift_down = [](u32x4 v, int early) {
+    const bool one = early & 4, two = early & 8;
+    v = u32x4{one ? v[1] : v[0], one ? v[2] : v[1], one ? v[3] : v[2], one ? 0u : v[3]};
+    return u32x4{two ? v[2] : v[0], two ? v[3] : v[1], two ? 0u : v[2], two ? 0u : v[3]};
+  };
+  auto store_scales = [&](int area, int q) {
+    u32x4 a, x = shift_down(qx, early_x);
+    if constexpr (PACKED) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        a[j] = ((qa[0] >> (8 * j)) & 0xff) | (((qa[1] >> (8 * j)) & 0xff) << 8) | (((qa[2] >> (8 * j)) & 0xff) << 16) |
+               ((qa[3] >> (8 * j)) << 24);
+    } else {
+      a = shift_down(qa, early_a);
+    }
+    // a step past the last: 2^-127 on both sides, whose products vanish in fp32
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = 4 * q + j < ks ? a[j] : 0;
+      x[j] = 4 * q + j < ks ? x[j] : 0;
+    }
+    uint8_t* base = lds + S::kScales + area * S::kQuad + 16 * tid;
+    *reinterpret_cast<u32x4*>(base) = a;
+    if (MT == kThreads || tid < MT) *reinterpret_cast<u32x4*>(base + S::kSA) = x;
+  };
+
+  // operand reads of a wave: sub-step s of a step (64 elements), lane (h, r) = row r, chunk 2 s + h
+  const int h = lane >> 5;
+  const int read0 = (lane & 31) * 64 + ((h ^ ((lane >> 1) & 3)) * 16);
+  u32x4 a[2][CB], bx_[2][RB];
+  uint32_t sa[CB], sx[RB];
+  auto read_step = [&](int buf, int s) {
+    const uint8_t* base = lds + buf * S::kStep + (read0 ^ (32 * s));
+#pragma unroll
+    for (int i = 0; i < CB; ++i) a[s][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 2048);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) bx_[s][i] = *reinterpret_cast<const u32x4*>(base + S::kA + (wr * RB + i) * 2048);
+  };
+  // the lane's rows' scales of step j of the quad, shifted so that block h of the step is
+  // byte 0 and block 2 + h byte 2 (the MFMA selects a byte)
+  auto read_scales = [&](int area, int j) {
+    const uint8_t* base = lds + S::kScales + area * S::kQuad + 16 * (lane & 31) + 4 * j;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(base + (wc * CB + i) * 512) >> (8 * h);
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+      sx[i] = *reinterpret_cast<const uint32_t*>(base + S::kSA + (wr * RB + i) * 512) >> (8 * h);
+  };
+  v16f acc[CB][RB];
+  auto multiply = [&]<int SUB>(std::integral_constant<int, SUB>) {
+#pragma unroll
+    for (int j = 0; j < RB; ++j)
+#pragma unroll
+      for (int i = 0; i < CB; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            join_operand(a[SUB][i], u32x4{}), join_operand(bx_[SUB][j], u32x4{}), acc[i][j], kFmtFp4, kFmtFp4, 2 * SUB,
+            (int)sa[i], 2 * SUB, (int)sx[j]);
+  };
+  constexpr std::integral_constant<int, 0> k0{};
+  constexpr std::integral_constant<int, 1> k1{};
+  constexpr std::integral_constant<int, 2> k2{};
+  constexpr std::integral_constant<int, 3> k3{};
+
+  constexpr int kCodes = S::kLA + S::kLB, kScaleLoads = PACKED ? 5 : 2;   // loads of a step, of a quad's scales
+
+  fill(0);
+  Item cur = item(0);
+  aim(cur);
+  load_scales(0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) issue_step(j, j, j < ks);
+  store_scales(0, 0);
+  slot_barrier<3 * kCodes>();
+  read_scales(0, 0);
+  read_step(0, 0);
+
+  int area = 0;
+  // Steps 4 q .. 4 q + 3 of the current item; behind them the loads of quad nq of the item
+  // aimed at (none when !more).
+  auto quad = [&](int nq, bool more) {
+    auto step = [&]<int J>(std::integral_constant<int, J>) {
+      read_step(J, 1);
+      if constexpr (J == 3) store_scales(area ^ 1, nq);
+      multiply(k0);
+      // step J + 1 has landed: newer are the codes of the two steps behind it, and the next
+      // quad's scales where they were issued among these
+      slot_barrier<2 * kCodes + (J == 1 || J == 2 ? kScaleLoads : 0)>();
+      if constexpr (J == 0) load_scales(nq);
+      issue_step(J, 4 * nq + J, more && 4 * nq + J < ks);
+      read_step((J + 1) & 3, 0);
+      multiply(k1);
+      read_scales(J == 3 ? area ^ 1 : area, (J + 1) & 3);
+    };
+    step(k0);
+    step(k1);
+    step(k2);
+    step(k3);
+    area ^= 1;
+    pin(acc);
+  };
+  for (int n = 0;;) {
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    pin(acc);
+    for (int q = 1; q < kq; ++q) quad(q, true);
+    // the item's last quad: the next item's first is loaded behind it
+    const bool more = n + 1 < count;
+    if (more && (n + 1) % kList == 0) fill(n + 1);
+    const Item next = more ? item(n + 1) : cur;
+    aim(next);
+    quad(0, more);
+    // lane (h, r) holds row r, channels 8 e + 4 h + 0..3
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const int r = (wr * RB + j) * 32 + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < CB; ++i) {
+        const int c0 = cur.cb * kNT + (wc * CB + i) * 32 + 4 * h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r < cur.rows && c0 + 8 * e < p.N)
+            store4(out + (int64_t)(cur.row0 + r) * p.N + c0 + 8 * e,
+                   v4f{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]});
+      }
+    }
+    if (++n >= count) break;
+    cur = next;
+  }
+  __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (15 << 8));   // no direct-to-LDS load outlives the block
+}
+
+template <int WC, int RB, typename O, bool PACKED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1))) void fp4_tile_kernel(
+    TileArgs p, O* __restrict__ out) {
+  extern __shared__ __align__(16) uint8_t lds_area[];
+  tile_body<WC, RB, O, PACKED>(p, out, lds_area, lds_area);
+}
+
+// The device's compute units, rounded up to whole XCDs' shares; the kernel's LDS size set
+// once for each device.
+hipError_t tile_grid(const void* kernel, int lds, int* grid) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, int> known;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  auto at = known.find({dev, kernel});
+  if (at == known.end()) {
+    int cus = 0;
+    if ((e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds)) != hipSuccess) return e;
+    if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
+    at = known.emplace(std::make_pair(dev, kernel), (cus + 7) / 8 * 8).first;
+  }
+  *grid = at->second;
+  return hipSuccess;
+}
+
+template <int WC, int RB, typename O, bool PACKED>
+hipError_t launch_tiles(const TileArgs& a, void* out, hipStream_t stream) {
+  using S = TileShape<WC, RB>;
+  int grid = 0;
+  const auto kernel = fp4_tile_kernel<WC, RB, O, PACKED>;
+  hipError_t e = tile_grid(reinterpret_cast<const void*>(kernel), S::kLds, &grid);
+  if (e != hipSuccess) return e;
+  kernel<<<grid, kThreads, S::kLds, stream>>>(a, (O*)out);
+  return hipGetLastError();
+}
+
+template <typename O, bool PACKED>
+hipError_t launch_shape(const Fp4MatmulParams& p, const TileArgs& a, hipStream_t stream) {
+  switch (p.mt) {
+    case 256: return launch_tiles<2, 4, O, PACKED>(a, p.out, stream);
+    case 128: return launch_tiles<2, 2, O, PACKED>(a, p.out, stream);
+    default: return launch_tiles<4, 2, O, PACKED>(a, p.out, stream);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_fp4_tiles(const Fp4MatmulParams& p, hipStream_t stream) {
+  TileArgs a{};
+  a.x = (const uint8_t*)p.x; a.xs = p.x_scales; a.w = p.w; a.ws = p.w_scales; a.off = p.off;
+  a.groups = p.groups; a.rows = (int)p.rows; a.K = p.k; a.N = p.n;
+  if (p.x_codes) {
+    const int64_t groups = p.rows * (p.k / 32);
+    const unsigned grid = (unsigned)((groups + 255) / 256);
+    switch (p.x_kind) {
+      case 0: fp4_quantise_kernel<<<grid, 256, 0, stream>>>((const float*)p.x, groups, p.x_codes, p.x_code_scales); break;
+      case 1: fp4_quantise_kernel<<<grid, 256, 0, stream>>>((const _Float16*)p.x, groups, p.x_codes, p.x_code_scales); break;
+      default: fp4_quantise_kernel<<<grid, 256, 0, stream>>>((const uint16_t*)p.x, groups, p.x_codes, p.x_code_scales); break;
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.x = p.x_codes; a.xs = p.x_code_scales;
+  }
+  if (p.packed)
+    return p.out_fp32 ? launch_shape<float, true>(p, a, stream) : launch_shape<uint16_t, true>(p, a, stream);
+  return p.out_fp32 ? launch_shape<float, false>(p, a, stream) : launch_shape<uint16_t, false>(p, a, stream);
+}
+
+}  // namespace moe

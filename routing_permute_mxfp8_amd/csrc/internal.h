@@ -314,7 +314,15 @@ struct Fp4MatmulParams {
   bool packed = false;
   bool out_fp32 = false;           // else bf16
   void* out = nullptr;
+  // rows of an item of the LDS-tiled kernels (fp4_tile.hip), 0: the kernel for few rows
+  int mt = 0;
+  // workspace of the LDS-tiled kernels, unless x holds codes
+  uint8_t* x_codes = nullptr;      // [rows, k/2]
+  uint8_t* x_code_scales = nullptr;  // [rows, k/32]
 };
+// Rows of an item for a call (0: the kernel for few rows).
+int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k);
+hipError_t launch_fp4_tiles(const Fp4MatmulParams& p, hipStream_t stream);
 hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream);
 
 // ---- static scratch of the allocation-free entry point (noalloc.hip) ---------------------

@@ -220,3 +220,24 @@ def test_router_to_expert_product():
     bounds = [int(v) for v in off.cpu()]
     check(out[:order.size], xv, wv, bounds, torch.float32)
     assert bool((out[order.size:] == 3).all())
+
+
+def test_more_items_than_a_block_lists_at_once():
+    """A product of so many tiles that every block of the many-rows kernel computes over 256
+    (it describes 256 at a time): rows from all over it against the oracle."""
+    rows, n, k = 300_000, 16384, 128
+    say(f"mxfp4_matmul rows={rows} n={n} k={k}")
+    rng = np.random.default_rng(0)
+    x, xv, wc, ws, wv = operands(4096, 1, n, k, seed=1)
+    pick = torch.from_numpy(rng.integers(0, 4096, rows))   # rows of x, many times over
+    codes, scales = to_dev(x[0])[pick.to(DEV)], to_dev(x[1])[pick.to(DEV)]
+    got = rp.mxfp4_matmul(codes, to_dev(wc), to_dev(ws), x_scales=scales)
+    some = np.sort(rng.choice(rows, 700, replace=False))
+    some[0], some[-1] = 0, rows - 1
+    check(got[torch.from_numpy(some).to(DEV)], xv[pick.numpy()[some]], wv, [0, some.size], torch.bfloat16)
+    # every row that repeats a row of x repeats its result
+    first = torch.zeros(4096, dtype=torch.int64, device=DEV)
+    first[pick.flip(0).to(DEV)] = torch.arange(rows - 1, -1, -1, device=DEV)
+    for lo in range(0, rows, 50_000):
+        part = pick[lo:lo + 50_000].to(DEV)
+        assert torch.equal(got[lo:lo + 50_000], got[first[part]])
