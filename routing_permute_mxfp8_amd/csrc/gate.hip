@@ -37,8 +37,8 @@ __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(_Float16 v) { return (float)v; }
 __device__ __forceinline__ float to_float(uint16_t v) { return bf16_to_f(v); }   // bf16 bits
 
-// A logit as the operators take it: NaN as -inf, +inf as the largest float.
-__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : fminf(x, FLT_MAX); }
+// A logit as the operators take it: NaN as -inf, +inf as the largest float, -0 as +0.
+__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : fminf(x, FLT_MAX) + 0.0f; }
 
 // The lane's V logits of a row of E; experts past E are -inf. VEC: one wide load (E % V == 0
 // and the address aligned for it, checked on the host).
@@ -291,17 +291,13 @@ __device__ __forceinline__ bool choose(const GateArgs& p, const float (&x)[V], c
   return !close;
 }
 
+// One row by a whole wave.
 template <typename T, int V, bool SOFTMAX>
-__global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __restrict__ logits, GateArgs p) {
-  extern __shared__ double lds_ranks[];   // [waves][E] with groups
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + wave;
-  if (row >= p.rows) return;
-  double* lds = lds_ranks + wave * p.E;
+__device__ __forceinline__ void gate_row(const T* __restrict__ logits, const GateArgs& p, int64_t row, double* lds, int lane,
+                                         bool vec) {
   const T* rp = logits + row * p.E;
   float x[V];
-  load_row<T, V>(rp, p.E, lane, p.vec, x);
+  load_row<T, V>(rp, p.E, lane, vec, x);
   RowNorm<float> norm{0.0f, 0.0f};
   if constexpr (SOFTMAX) norm = softmax_norm<float, V>(x);
   int mine;
@@ -329,6 +325,329 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __res
   if (lane < p.k) {
     p.ids[row * p.k + lane] = mine;
     p.weights[row * p.k + lane] = w * p.scale;
+  }
+}
+
+template <typename T, int V, bool SOFTMAX>
+__global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __restrict__ logits, GateArgs p) {
+  extern __shared__ double lds_ranks[];   // [waves][E] with groups
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + wave;
+  if (row >= p.rows) return;
+  gate_row<T, V, SOFTMAX>(logits, p, row, lds_ranks + wave * p.E, threadIdx.x & 63, p.vec);
+}
+
+// ---- gate, up to 256 experts and K up to 8: four rows a wave ------------------------------
+// 16 lanes a row, lane l holding the V experts [l V, l V + V). A rank becomes one 32-bit key:
+// the upper 24 bits of its fp32 value in unsigned order, then 255 - index, so a comparison
+// is one instruction and equal ranks are in index order. Each lane sorts its keys, and four
+// exchanges between lanes merge the lists of the eight largest: about 60 instructions a
+// row, where a maximum over the wave for each of the K takes about 20 for each.
+// The eight then order themselves by their whole ranks. The lower 8 bits that the keys drop
+// may hide which of two is the K-th, and the rounding of the ranks the order of two
+// neighbours: such rows (about one of a hundred fp32 rows with a bias, none of fp16 or bf16
+// logits without one, which the 24 bits hold exactly) are decided one at a time by the whole wave.
+constexpr int kTop = 8;
+
+__device__ __forceinline__ uint32_t order_key(float r, int e) {
+  const int b = __float_as_int(r);
+  const uint32_t o = (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
+  return (o & 0xffffff00u) | (uint32_t)(255 - e);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {   // the rank, cut to 24 bits
+  const uint32_t o = k & 0xffffff00u;
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o & 0xffffff00u);
+}
+
+__device__ __forceinline__ void larger_first(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b), lo = min(a, b);
+  a = hi;
+  b = lo;
+}
+// Descending order of a bitonic list of eight.
+__device__ __forceinline__ void order_bitonic(uint32_t (&a)[kTop]) {
+#pragma unroll
+  for (int d = kTop / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < kTop; ++i)
+      if (!(i & d)) larger_first(a[i], a[i + d]);
+}
+// Batcher's odd-even merge sort of eight, descending.
+__device__ __forceinline__ void order_eight(uint32_t (&a)[kTop]) {
+#pragma unroll
+  for (int p = 1; p < kTop; p *= 2)
+#pragma unroll
+    for (int k = p; k > 0; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < kTop; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < kTop && (i + j) / (2 * p) == (i + j + k) / (2 * p)) larger_first(a[i + j], a[i + j + k]);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dppu(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dppf(float v) { return __uint_as_float(dppu<CTRL>(__float_as_uint(v))); }
+// Lane exchanges in a row of 16: neighbours, pairs, fours (mirrored), eights (mirrored).
+constexpr int kX1 = 0xB1, kX2 = 0x4E, kX4 = 0x141, kX8 = 0x140;
+template <int CTRL>
+__device__ __forceinline__ void merge_lanes(uint32_t (&a)[kTop]) {
+  uint32_t b[kTop];
+#pragma unroll
+  for (int i = 0; i < kTop; ++i) b[i] = max(a[i], dppu<CTRL>(a[kTop - 1 - i]));
+#pragma unroll
+  for (int i = 0; i < kTop; ++i) a[i] = b[i];
+  order_bitonic(a);
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dppf<kX1>(v));
+  v = fmaxf(v, dppf<kX2>(v));
+  v = fmaxf(v, dppf<kX4>(v));
+  return fmaxf(v, dppf<kX8>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dppf<kX1>(v);
+  v += dppf<kX2>(v);
+  v += dppf<kX4>(v);
+  return v + dppf<kX8>(v);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, dppu<kX1>(v));
+  v = max(v, dppu<kX2>(v));
+  v = max(v, dppu<kX4>(v));
+  return max(v, dppu<kX8>(v));
+}
+
+// The lane's V values of a row of E, by 16-byte loads where they fit (E % V == 0, so that a
+// lane's values are all there or none, and the address aligned); past E some value of the row.
+template <typename T, int V>
+__device__ __forceinline__ void load_part(const T* row, int E, int sub, bool vec, T (&x)[V]) {
+  constexpr int W = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+  typedef T vec_t __attribute__((ext_vector_type(W)));
+  if (vec) {
+    const T* at = row + (sub * V < E ? sub * V : 0);
+#pragma unroll
+    for (int c = 0; c < V; c += W) {
+      const vec_t u = *reinterpret_cast<const vec_t*>(at + c);
+#pragma unroll
+      for (int v = 0; v < W; ++v) x[c + v] = u[v];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = row[min(sub * V + v, E - 1)];
+  }
+}
+
+// The logits of load_part as the operators take them; experts past E are -inf.
+template <typename T, int V>
+__device__ __forceinline__ void clean_part(const T (&raw)[V], int E, int sub, float (&x)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = clean(to_float(raw[v]));
+  if (E < 16 * V) {   // uniform
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = sub * V + v < E ? x[v] : -INFINITY;
+  }
+}
+
+// Where the order of a lane's experts does not matter they are dealt in 16-byte pieces (W
+// values), so that a wave's loads and stores run along the rows: value v of lane `sub` is
+// expert dealt<W>(sub, v). (The gradient of 32768 x 256 fp32 rows with 64 contiguous bytes a
+// lane: 21 us, dealt: see gate16_backward_kernel.)
+template <typename T, int V> constexpr int kPiece = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+template <int W>
+__device__ __forceinline__ int dealt(int sub, int v) { return v / W * 16 * W + sub * W + v % W; }
+
+// VEC: every piece is whole and aligned (E % W == 0); past E some value of the row.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_dealt(const T* row, int E, int sub, bool vec, T (&x)[V]) {
+  constexpr int N = 16 / (int)sizeof(T) < W ? 16 / (int)sizeof(T) : W;
+  typedef T vec_t __attribute__((ext_vector_type(N)));
+  if (vec) {
+#pragma unroll
+    for (int v = 0; v < V; v += N) {
+      const int e = dealt<W>(sub, v);
+      const vec_t u = *reinterpret_cast<const vec_t*>(row + (e < E ? e : 0));
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[v + i] = u[i];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = row[min(dealt<W>(sub, v), E - 1)];
+  }
+}
+template <typename T, int V, int W>
+__device__ __forceinline__ void clean_dealt(const T (&raw)[V], int E, int sub, float (&x)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = clean(to_float(raw[v]));
+  if (E < 16 * V) {   // uniform
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = dealt<W>(sub, v) < E ? x[v] : -INFINITY;
+  }
+}
+
+// softmax_norm of a row held by 16 lanes.
+template <int V>
+__device__ __forceinline__ RowNorm<float> row_norm(const float (&x)[V]) {
+  float m = x[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+  m = fmaxf(row_max(m), -FLT_MAX);   // (a row of -inf only: exp(-inf) = 0 throughout)
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum += exp_of(x[v] - m);
+  sum = row_sum(sum);
+  return RowNorm<float>{m, sum > 0.0f ? 1.0f / sum : 0.0f};
+}
+
+template <typename T, int V, bool SOFTMAX, bool BIAS>
+__global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __restrict__ logits, GateArgs p, bool vec64, bool vec_bias) {
+  extern __shared__ double lds_ranks[];   // [waves][E] with groups
+  const int lane = threadIdx.x & 63, sub = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = ((int64_t)blockIdx.x * kRowsPerBlock + wave) * 4;
+  if (row0 >= p.rows) return;
+  const int64_t row = min(row0 + (lane >> 4), p.rows - 1);
+  const bool there = row0 + (lane >> 4) < p.rows;
+  const T* rp = logits + row * p.E;
+  float x[V];
+  {
+    T raw[V];
+    load_part<T, V>(rp, p.E, sub, p.vec, raw);
+    clean_part<T, V>(raw, p.E, sub, x);
+  }
+  RowNorm<float> norm{0.0f, 0.0f};
+  if constexpr (SOFTMAX) norm = row_norm<V>(x);
+  const float top = SOFTMAX ? norm.inv : 1.0f;
+  float r[V];
+  bool close = false;
+  bool stays = true;
+  const bool groups = p.groups > 1;   // uniform
+  if (BIAS || groups) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v] = score_of<float, SOFTMAX>(x[v], norm);
+    if constexpr (BIAS) {
+      float bias[V];
+      load_part<float, V>(p.bias, p.E, sub, vec_bias, bias);
+#pragma unroll
+      for (int v = 0; v < V; ++v) r[v] += bias[v];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v] = x[v] == -INFINITY ? -INFINITY : r[v];
+  }
+  if (groups) {   // a group is `lanes` whole lanes (a power of two)
+    float a = -INFINITY, b = -INFINITY, big = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      merge_two(a, b, r[v], -INFINITY);
+      big = fmaxf(big, r[v] == -INFINITY ? 0.0f : fabsf(r[v]));
+    }
+    if (p.lanes > 1) merge_two(a, b, dppf<kX1>(a), dppf<kX1>(b));
+    if (p.lanes > 2) merge_two(a, b, dppf<kX2>(a), dppf<kX2>(b));
+    if (p.lanes > 4) merge_two(a, b, dppf<kX4>(a), dppf<kX4>(b));
+    const float score = a + (b == -INFINITY ? 0.0f : b);
+    const float tau = 4 * (top * 0x1p-18f + row_max(big) * 0x1p-21f);
+    const int shift = __builtin_ctz(p.lanes), g = sub >> shift;
+    int better = 0;
+    auto against = [&]<int L>(std::integral_constant<int, L>) {
+      const int h = L >> shift;
+      if ((L & (p.lanes - 1)) == 0 && h < p.groups) {   // uniform
+        const float o = dppf<0x150 + L>(score);   // lane L of each row of 16
+        better += (int)(o > score) | ((int)(o == score) & (int)(h < g));
+        close |= (h != g) & (fabsf(o - score) <= tau);
+      }
+    };
+    [&]<int... L>(std::integer_sequence<int, L...>) { (against(std::integral_constant<int, L>{}), ...); }
+    (std::make_integer_sequence<int, 16>{});
+    stays = better < p.topk_groups && g < p.groups;
+    close = close && p.topk_groups < p.groups;
+  }
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    key[v] = order_key(BIAS ? r[v] : x[v], sub * V + v);   // without a bias the scores rise with the logits
+    key[v] = stays ? key[v] : 0u;
+  }
+  if (p.E < 16 * V) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = sub * V + v < p.E ? key[v] : 0u;
+  }
+  uint32_t best[kTop];
+  if constexpr (V == 16) {
+    uint32_t hi[kTop];
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) best[i] = key[i], hi[i] = key[kTop + i];
+    order_eight(best);
+    order_eight(hi);
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) best[i] = max(best[i], hi[kTop - 1 - i]);
+    order_bitonic(best);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) best[i] = i < V ? key[i < V ? i : 0] : 0u;
+    order_eight(best);
+  }
+  merge_lanes<kX1>(best);
+  merge_lanes<kX2>(best);
+  merge_lanes<kX4>(best);
+  merge_lanes<kX8>(best);
+  // lane j of a row: candidate j of the eight
+  uint32_t mine = best[0];
+#pragma unroll
+  for (int i = 1; i < kTop; ++i) mine = sub == i ? best[i] : mine;
+  const bool held = sub < kTop && mine != 0u;
+  const int id = 255 - (int)(mine & 255u);
+  const float l = held ? clean(to_float(rp[held ? id : 0])) : -INFINITY;
+  const float s = l == -INFINITY ? 0.0f : score_of<float, SOFTMAX>(l, norm);
+  int at = sub;   // its place in the row
+  if constexpr (BIAS || sizeof(T) == 4) {
+    // Certain so far: what the keys put clearly apart. The K-th choice has to be clear of the
+    // first one that is not a candidate any more.
+    const float tau = BIAS ? top * 0x1p-18f : 0.0f;
+    uint32_t kth = best[0], beyond = best[kTop - 1];
+#pragma unroll
+    for (int i = 1; i < kTop; ++i) kth = p.k == i + 1 ? best[i] : kth;
+    if (p.k == kTop) {   // uniform
+      beyond = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) beyond = max(beyond, key[v] < best[kTop - 1] ? key[v] : 0u);
+      beyond = row_max(beyond);
+    }
+    const float u = key_value(kth), w = key_value(beyond);
+    close |= (beyond != 0u) & !(u - w > tau + 0x1p-14f * fmaxf(fabsf(u), fabsf(w)));
+    // The candidates' own order by their whole ranks, and of those by their errors.
+    const float rank = !held ? NAN : BIAS ? (l == -INFINITY ? -INFINITY : s + p.bias[id]) : l;
+    const float reach = tau + (BIAS ? fabsf(rank) * 0x1p-21f : 0.0f);
+    at = 0;
+    auto against = [&]<int L>(std::integral_constant<int, L>) {
+      const float o = dppf<0x150 + L>(rank);
+      const int oid = (int)dppu<0x150 + L>((uint32_t)id);
+      at += (int)(o > rank) | ((int)(o == rank) & (int)(oid < id));
+      if constexpr (BIAS) close |= (L != sub) & (fabsf(o - rank) <= reach);
+    };
+    [&]<int... L>(std::integer_sequence<int, L...>) { (against(std::integral_constant<int, L>{}), ...); }
+    (std::make_integer_sequence<int, kTop>{});
+  }
+  const bool chosen = held && at < p.k;
+  float weight = chosen ? s : 0.0f;
+  if (p.renorm) {
+    const float total = row_sum(weight);
+    weight = total > 0.0f ? weight / total : 0.0f;
+  }
+  uint64_t again = __ballot(close && there);   // any lane of a row
+  const bool redo = (again >> (lane & 48)) & 0xffff;
+  if (chosen && there && !redo) {
+    p.ids[row * p.k + at] = id;
+    p.weights[row * p.k + at] = weight * p.scale;
+  }
+  GateArgs q = p;   // the wave's own lanes a group
+  q.lanes = 64;
+  while (64 / q.lanes < q.groups) q.lanes /= 2;
+  while (again) {
+    const int i = __builtin_ctzll(again) >> 4;
+    again &= ~(0xffffull << (16 * i));
+    gate_row<T, (V + 3) / 4, SOFTMAX>(logits, q, row0 + i, lds_ranks + wave * p.E, lane, vec64);
   }
 }
 
@@ -412,7 +731,99 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
   }
 }
 
-constexpr int kFinishThreads = 1024;
+// The same for up to 256 experts, four rows a wave (16 lanes each, as gate16_kernel), the
+// next rows' logits loaded before these are summed.
+template <typename T, int V, bool SOFTMAX>
+__global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
+    const T* __restrict__ logits, int64_t rows, int E, bool vec, const int32_t* __restrict__ ids, int k,
+    const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, float* __restrict__ sums,
+    int32_t* __restrict__ counts, int32_t* __restrict__ held, unsigned* __restrict__ done) {
+  constexpr int W = kPiece<T, V>;
+  __shared__ float lds_sums[kRowsPerBlock][16 * V];
+  __shared__ int hist[16 * V];
+  __shared__ int rows_seen[kRowsPerBlock];
+  const int lane = threadIdx.x & 63, sub = lane & 15, part = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b = blockIdx.y, splits = gridDim.x, s = blockIdx.x;
+  if (threadIdx.x == 0 && s == 0 && b == 0) *done = 0;
+  for (int e = threadIdx.x; e < 16 * V; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  int64_t lo, hi;
+  seq_rows(off, b, rows, &lo, &hi);
+  const int64_t len = hi - lo, first = lo + len * s / splits, last = lo + len * (s + 1) / splits;
+  float acc[V] = {};
+  int seen = 0;
+  struct Rows {   // four rows, past the end the last one
+    T raw[V];
+    int id[2];
+    uint8_t counted;
+  };
+  auto load = [&](int64_t at, Rows& r) {
+    const int64_t row = min(at + part, last - 1);
+    load_dealt<T, V, W>(logits + row * E, E, sub, vec, r.raw);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.id[i] = sub + 16 * i < k ? ids[row * k + sub + 16 * i] : -1;
+    r.counted = (at + part < last) & ((mask ? mask[row] : 1) != 0);
+  };
+  int64_t at = first + 4 * wave;
+  Rows cur;
+  if (at < last) load(at, cur);
+  for (; at < last; at += 4 * kRowsPerBlock) {
+    Rows next;
+    if (at + 4 * kRowsPerBlock < last) load(at + 4 * kRowsPerBlock, next);
+    const bool counted = cur.counted;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (counted && (unsigned)cur.id[i] < (unsigned)E) atomicAdd(&hist[cur.id[i]], 1);
+    seen += counted && sub == 0;
+    float x[V];
+    clean_dealt<T, V, W>(cur.raw, E, sub, x);
+    if constexpr (SOFTMAX) {
+      RowNorm<float> n = row_norm<V>(x);
+      if (!counted) n.inv = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += score_of<float, true>(x[v], n);
+    } else {
+      float sc[V], z = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        sc[v] = score_of<float, false>(x[v], RowNorm<float>{});
+        z += sc[v];
+      }
+      z = row_sum(z);
+      const float inv = counted && z > 0.0f ? 1.0f / z : 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += sc[v] * inv;
+    }
+    cur = next;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {   // the four rows of the wave
+    acc[v] += __shfl_xor(acc[v], 16, 64);
+    acc[v] += __shfl_xor(acc[v], 32, 64);
+    if (part == 0) lds_sums[wave][dealt<W>(sub, v)] = acc[v];
+  }
+  const int rows_of_wave = __popcll(__ballot(seen & 1)) + 2 * __popcll(__ballot(seen & 2)) + 4 * __popcll(__ballot(seen & 4));
+  int more = seen >> 3;   // (over 7 row quads a wave: long sequences)
+  for (int d = 1; d < 64; d *= 2) more += __shfl_xor(more, d, 64);
+  if (lane == 0) rows_seen[wave] = rows_of_wave + 8 * more;
+  __syncthreads();
+  const int64_t to = (int64_t)b * splits + s;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowsPerBlock; ++w) t += lds_sums[w][e];
+    sums[to * E + e] = t;
+    counts[to * E + e] = hist[e];
+  }
+  if (threadIdx.x == 0) {
+    int t = 0;
+    for (int w = 0; w < kRowsPerBlock; ++w) t += rows_seen[w];
+    held[to] = t;
+  }
+}
+
+constexpr int kFinishThreads = 512, kFinishExperts = 64;   // a block: 64 experts, 8 slices of the partials
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
   v = wave_sum(v);
@@ -424,67 +835,73 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return t;
 }
 
-// Second pass: block b joins its sequence's partials; the last block to end adds the
-// sequences' losses, in order.
+// Second pass: block (c, b) joins the partials of 64 experts of sequence b; the last block
+// to end adds the blocks' shares of the loss, in order.
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
-    int E, int k, int splits, const float* __restrict__ sums, const int32_t* __restrict__ counts_part,
-    const int32_t* __restrict__ held, float alpha, double* __restrict__ seq_loss, unsigned* __restrict__ done,
+    int E, int k, int splits, int seqs, int lanes, const float* __restrict__ sums, const int32_t* __restrict__ counts_part,
+    const int32_t* __restrict__ held, float alpha, double* __restrict__ shares, unsigned* __restrict__ done,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ coef) {
-  __shared__ double lds_p[kFinishThreads];
-  __shared__ int lds_c[kFinishThreads];
+  constexpr int kSlices = kFinishThreads / kFinishExperts;
+  __shared__ double lds_p[kSlices][kFinishExperts];
+  __shared__ int lds_c[kSlices][kFinishExperts];
   __shared__ double lds_w[kFinishThreads / 64];
-  const int b = blockIdx.x, seqs = gridDim.x;
-  // sequences with a counted row, and this one's rows
-  double mine = 0, filled = 0;
-  for (int q = threadIdx.x; q < seqs; q += kFinishThreads) {
+  __shared__ int lds_rows, lds_filled;
+  const int b = blockIdx.y, lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  if (threadIdx.x == 0) lds_rows = lds_filled = 0;
+  // this block's partials first: their loads are under way while the rows are counted
+  const int e = blockIdx.x * kFinishExperts + lane;
+  double p = 0;
+  int c = 0;
+  if (e < E)
+#pragma unroll 4
+    for (int s = slice; s < splits; s += kSlices) {
+      p += sums[((int64_t)b * splits + s) * E + e];
+      c += counts_part[((int64_t)b * splits + s) * E + e];
+    }
+  __syncthreads();
+  // sequences with a counted row, and this one's rows: `lanes` lanes a sequence
+  int filled = 0;
+  for (int q0 = 0; q0 < seqs; q0 += kFinishThreads / lanes) {
+    const int q = q0 + threadIdx.x / lanes;
     int t = 0;
-    for (int s = 0; s < splits; ++s) t += held[(int64_t)q * splits + s];
-    filled += t > 0;
-    if (q == b) mine = t;
+    if (q < seqs)
+      for (int s = threadIdx.x % lanes; s < splits; s += lanes) t += held[(int64_t)q * splits + s];
+    for (int d = 1; d < lanes; d *= 2) t += __shfl_xor(t, d, 64);
+    const bool first = threadIdx.x % lanes == 0 && q < seqs;
+    filled += __popcll(__ballot(first && t > 0));
+    if (first && q == b) lds_rows = t;
   }
-  const double rows = block_sum(mine, lds_w);
-  filled = block_sum(filled, lds_w);
-  const double f = rows > 0 ? (double)alpha * E / ((double)k * rows * rows * filled) : 0.0;
-  double total = 0;
-  // `across` threads an expert where E is small
-  const int width = min((E + 63) / 64 * 64, kFinishThreads), across = kFinishThreads / width;
-  const int slice = threadIdx.x / width, col = threadIdx.x % width;
-  for (int e0 = 0; e0 < E; e0 += width) {
-    const int e = e0 + col;
-    double p = 0;
-    int c = 0;
-    if (e < E && slice < across)
-      for (int s = slice; s < splits; s += across) {
-        p += sums[((int64_t)b * splits + s) * E + e];
-        c += counts_part[((int64_t)b * splits + s) * E + e];
-      }
-    __syncthreads();
-    lds_p[threadIdx.x] = p;
-    lds_c[threadIdx.x] = c;
-    __syncthreads();
-    if (slice == 0 && e < E) {
-      for (int a = 1; a < across; ++a) {
-        p += lds_p[a * width + col];
-        c += lds_c[a * width + col];
+  if (lane == 0) atomicAdd(&lds_filled, filled);
+  lds_p[slice][lane] = p;
+  lds_c[slice][lane] = c;
+  __syncthreads();
+  __shared__ bool last;
+  if (slice == 0) {
+    const double rows = lds_rows;
+    const double f = rows > 0 ? (double)alpha * E / ((double)k * rows * rows * lds_filled) : 0.0;
+    double total = 0;
+    if (e < E) {
+      for (int a = 1; a < kSlices; ++a) {
+        p += lds_p[a][lane];
+        c += lds_c[a][lane];
       }
       counts[(int64_t)b * E + e] = c;
       coef[(int64_t)b * E + e] = (float)(f * c);
-      total += f * c * p;
+      total = f * c * p;
     }
-  }
-  total = block_sum(total, lds_w);
-  __shared__ bool last;
-  if (threadIdx.x == 0) {
-    seq_loss[b] = total;
-    __threadfence();
-    last = atomicAdd(done, 1u) == (unsigned)seqs - 1;
+    total = wave_sum(total);
+    if (lane == 0) {
+      shares[(int64_t)b * gridDim.x + blockIdx.x] = total;
+      __threadfence();
+      last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
+    }
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
   double t = 0;
-  for (int q = threadIdx.x; q < seqs; q += kFinishThreads)
-    t += __hip_atomic_load(&seq_loss[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int64_t q = threadIdx.x; q < (int64_t)seqs * gridDim.x; q += kFinishThreads)
+    t += __hip_atomic_load(&shares[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   t = block_sum(t, lds_w);
   if (threadIdx.x == 0) *loss = (float)t;
 }
@@ -504,9 +921,27 @@ struct GateGradArgs {
   const uint8_t* mask;         // nullable
 };
 
-__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_value(_Float16* p, float v) { *p = (_Float16)v; }
-__device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)bf16x2(v, v); }
+template <typename T>
+__device__ __forceinline__ T value_as(float v) {
+  if constexpr (std::is_same_v<T, uint16_t>)
+    return (uint16_t)bf16x2(v, v);
+  else
+    return (T)v;
+}
+
+// The sequence of a row (-1: none): the last that starts at or before it, if it holds it.
+__device__ __forceinline__ int row_seq(const int32_t* off, int seqs, int64_t row) {
+  if (!off) return 0;
+  int lo = 0, hi = seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return off[lo] <= row && row < off[lo + 1] ? lo : -1;
+}
 
 template <typename T, int V, bool SOFTMAX>
 __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const T* __restrict__ logits, GateGradArgs p,
@@ -554,20 +989,8 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const
 #pragma unroll
   for (int v = 0; v < V; ++v) q[v] = 0.0f;
   if (p.grad_loss && !(p.mask && p.mask[row] == 0)) {
-    int b = 0;
-    bool counted = true;
-    if (p.off) {   // the last sequence that starts at or before the row
-      int hi = p.seqs;
-      while (hi - b > 1) {
-        const int mid = (b + hi) >> 1;
-        if (p.off[mid] <= row)
-          b = mid;
-        else
-          hi = mid;
-      }
-      counted = p.off[b] <= row && row < p.off[b + 1];
-    }
-    if (counted) {
+    const int b = row_seq(p.off, p.seqs, row);
+    if (b >= 0) {
       const float gl = *p.grad_loss;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -606,7 +1029,124 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const
   T* out = grad + row * p.E;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (lane * V + v < p.E) store_value(out + lane * V + v, d[v]);
+    if (lane * V + v < p.E) out[lane * V + v] = value_as<T>(d[v]);
+}
+
+// Up to 256 experts: four rows a wave (16 lanes each, as gate16_kernel).
+template <typename T, int V, bool SOFTMAX>
+__global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(const T* __restrict__ logits, GateGradArgs p,
+                                                                             bool vec_coef, T* __restrict__ grad) {
+  constexpr int W = kPiece<T, V>, N = W < 4 ? W : 4;
+  typedef float part_t __attribute__((ext_vector_type(N)));
+  __shared__ __align__(16) float lds_grad[4 * kRowsPerBlock][16 * V];
+  const int lane = threadIdx.x & 63, sub = lane & 15, part = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = ((int64_t)blockIdx.x * kRowsPerBlock + wave) * 4;
+  if (row0 >= p.rows) return;
+  const int64_t row = min(row0 + part, p.rows - 1);
+  const T* rp = logits + row * p.E;
+  T raw[V];
+  load_dealt<T, V, W>(rp, p.E, sub, p.vec, raw);
+  int id[2] = {-1, -1};
+  float g[2] = {0.0f, 0.0f}, sc[2] = {0.0f, 0.0f}, l[2];
+  if (p.grad_weights) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // choices sub and sub + 16 of the row
+      const int j = sub + 16 * i;
+      if (j < p.k) {
+        id[i] = p.ids[row * p.k + j];
+        if ((unsigned)id[i] >= (unsigned)p.E) id[i] = -1;
+        g[i] = id[i] >= 0 ? p.grad_weights[row * p.k + j] * p.scale : 0.0f;
+      }
+      l[i] = id[i] >= 0 ? clean(to_float(rp[max(id[i], 0)])) : -INFINITY;
+    }
+  }
+  const int seq = p.grad_loss && !(p.mask && p.mask[row] == 0) ? row_seq(p.off, p.seqs, row) : -1;
+  float q[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) q[v] = 0.0f;
+  if (seq >= 0) {
+    const float gl = *p.grad_loss;
+    load_dealt<float, V, W>(p.coef + (int64_t)seq * p.E, p.E, sub, vec_coef, q);
+#pragma unroll
+    for (int v = 0; v < V; ++v) q[v] *= gl;
+  }
+  float x[V], s[V], d[V];
+  clean_dealt<T, V, W>(raw, p.E, sub, x);
+  RowNorm<float> norm{0.0f, 0.0f};
+  if constexpr (SOFTMAX) norm = row_norm<V>(x);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    s[v] = score_of<float, SOFTMAX>(x[v], norm);
+    d[v] = 0.0f;
+  }
+  if (p.grad_weights) {
+    float* area = lds_grad[wave * 4 + part];
+#pragma unroll
+    for (int v = 0; v < V; v += N) *reinterpret_cast<part_t*>(area + dealt<W>(sub, v)) = part_t{};
+    wave_lds_fence();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sc[i] = l[i] == -INFINITY ? 0.0f : score_of<float, SOFTMAX>(l[i], norm);
+    if (p.renorm) {
+      const float total = row_sum(sc[0] + sc[1]);
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      const float mean = row_sum(g[0] * sc[0] + g[1] * sc[1]) * inv;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) g[i] = (g[i] - mean) * inv;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (id[i] >= 0) area[id[i]] = g[i];
+    wave_lds_fence();
+#pragma unroll
+    for (int v = 0; v < V; v += N) {
+      const part_t u = *reinterpret_cast<const part_t*>(area + dealt<W>(sub, v));
+#pragma unroll
+      for (int j = 0; j < N; ++j) d[v + j] = u[j];
+    }
+  }
+  if constexpr (SOFTMAX) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      d[v] += q[v];
+      dot += d[v] * s[v];
+    }
+    dot = row_sum(dot);
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = s[v] * (d[v] - dot);
+  } else {
+    float dot = 0.0f, z = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      dot += q[v] * s[v];
+      z += s[v];
+    }
+    z = row_sum(z);
+    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+    dot = row_sum(dot) * inv;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float t = exp_of(-fabsf(x[v])), r = 1.0f / (1.0f + t);
+      d[v] = (d[v] + (q[v] - dot) * inv) * (t * r * r);
+    }
+  }
+  if (row0 + part >= p.rows) return;
+  T* out = grad + row * p.E;
+  if (p.vec) {
+    typedef T vec_t __attribute__((ext_vector_type(W)));
+#pragma unroll
+    for (int v = 0; v < V; v += W) {
+      vec_t u;
+#pragma unroll
+      for (int j = 0; j < W; ++j) u[j] = value_as<T>(d[v + j]);
+      if (dealt<W>(sub, v) < p.E) *reinterpret_cast<vec_t*>(out + dealt<W>(sub, v)) = u;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (dealt<W>(sub, v) < p.E) out[dealt<W>(sub, v)] = value_as<T>(d[v]);
+  }
 }
 
 // V = experts a lane: the smallest power of two with 64 V >= E.
@@ -616,6 +1156,14 @@ hipError_t with_width(int E, F&& f) {
   if (E <= 128) return f(std::integral_constant<int, 2>{});
   if (E <= 256) return f(std::integral_constant<int, 4>{});
   if (E <= 512) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
+}
+// Experts a lane of the kernels with 16 lanes a row (up to 256 experts).
+constexpr int kMost16 = 256;
+template <typename F>
+hipError_t with_width16(int E, F&& f) {
+  if (E <= 64) return f(std::integral_constant<int, 4>{});
+  if (E <= 128) return f(std::integral_constant<int, 8>{});
   return f(std::integral_constant<int, 16>{});
 }
 template <typename F>
@@ -633,15 +1181,48 @@ bool wide_rows(const void* p, int E, int V) {
 
 }  // namespace
 
+namespace {
+
+template <typename T, int V>
+void launch_gate16(const GateParams& p, GateArgs a, bool vec64, hipStream_t stream) {
+  const unsigned grid = (unsigned)((p.rows + 4 * kRowsPerBlock - 1) / (4 * kRowsPerBlock));
+  const size_t lds = p.groups > 1 ? sizeof(double) * kRowsPerBlock * p.experts : 0;
+  const bool vec_bias = wide_rows<float>(p.bias, p.experts, V);
+  auto go = [&](auto soft, auto bias) {
+    gate16_kernel<T, V, decltype(soft)::value, decltype(bias)::value>
+        <<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a, vec64, vec_bias);
+  };
+  auto with_bias = [&](auto soft) { p.bias ? go(soft, std::true_type{}) : go(soft, std::false_type{}); };
+  p.sigmoid ? with_bias(std::false_type{}) : with_bias(std::true_type{});
+}
+
+}  // namespace
+
 hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   if (p.rows <= 0) return hipSuccess;
   GateArgs a{};
   a.bias = p.bias; a.rows = p.rows; a.E = p.experts; a.k = p.k;
   a.groups = p.groups; a.topk_groups = p.topk_groups; a.group_size = p.experts / p.groups;
   if (a.group_size > 1) a.group_magic = (uint32_t)(((uint64_t(1) << 32) + a.group_size - 1) / a.group_size);
+  a.renorm = p.renorm; a.scale = p.scale; a.ids = p.ids; a.weights = p.weights;
+  // four rows a wave: up to 256 experts, K up to 8, and groups of 1, 2, 4 or 8 whole lanes of it
+  const int V16 = p.experts <= 64 ? 4 : p.experts <= 128 ? 8 : 16;
+  const int lanes = a.group_size / V16;
+  const bool whole = p.groups == 1 || (a.group_size % V16 == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 8);
+  if (p.experts <= kMost16 && p.k <= kTop && whole) {
+    a.lanes = std::max(lanes, 1);
+    return with_type(p.dtype, [&](auto* t) {
+      using T = std::remove_const_t<std::remove_pointer_t<decltype(t)>>;
+      return with_width16(p.experts, [&](auto w) {
+        constexpr int V = decltype(w)::value;
+        a.vec = wide_rows<T>(p.logits, p.experts, V);
+        launch_gate16<T, V>(p, a, wide_rows<T>(p.logits, p.experts, V / 4), stream);
+        return hipGetLastError();
+      });
+    });
+  }
   a.lanes = 64;
   while (64 / a.lanes < a.groups) a.lanes /= 2;
-  a.renorm = p.renorm; a.scale = p.scale; a.ids = p.ids; a.weights = p.weights;
   const unsigned grid = (unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock);
   const size_t lds = p.groups > 1 ? sizeof(double) * kRowsPerBlock * p.experts : 0;
   return with_type(p.dtype, [&](auto* t) {
@@ -665,27 +1246,36 @@ int balance_splits(int64_t rows, int64_t seqs) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((512 + seqs - 1) / seqs, (per + 15) / 16));
 }
 
+int balance_chunks(int experts) { return (experts + kFinishExperts - 1) / kFinishExperts; }
+
 hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
   const dim3 grid((unsigned)p.splits, (unsigned)p.seqs);
-  const size_t lds = sizeof(float) * (kRowsPerBlock + 1) * p.experts;
   hipError_t e = with_type(p.dtype, [&](auto* t) {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(t)>>;
+    auto go = [&](auto kernel, bool vec, size_t lds) {
+      kernel<<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, p.rows, p.experts, vec, p.ids, p.k, p.off, p.mask,
+                                                        p.sums, p.part_counts, p.held, p.done);
+      return hipGetLastError();
+    };
+    if (p.experts <= kMost16)
+      return with_width16(p.experts, [&](auto w) {
+        constexpr int V = decltype(w)::value;
+        const bool vec = wide_rows<T>(p.logits, p.experts, kPiece<T, V>);
+        return p.sigmoid ? go(balance16_sums_kernel<T, V, false>, vec, 0) : go(balance16_sums_kernel<T, V, true>, vec, 0);
+      });
     return with_width(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
       const bool vec = wide_rows<T>(p.logits, p.experts, V);
-      if (p.sigmoid)
-        balance_sums_kernel<T, V, false><<<grid, 64 * kRowsPerBlock, lds, stream>>>(
-            (const T*)p.logits, p.rows, p.experts, vec, p.ids, p.k, p.off, p.mask, p.sums, p.part_counts, p.held, p.done);
-      else
-        balance_sums_kernel<T, V, true><<<grid, 64 * kRowsPerBlock, lds, stream>>>(
-            (const T*)p.logits, p.rows, p.experts, vec, p.ids, p.k, p.off, p.mask, p.sums, p.part_counts, p.held, p.done);
-      return hipGetLastError();
+      const size_t lds = sizeof(float) * (kRowsPerBlock + 1) * p.experts;
+      return p.sigmoid ? go(balance_sums_kernel<T, V, false>, vec, lds) : go(balance_sums_kernel<T, V, true>, vec, lds);
     });
   });
   if (e != hipSuccess) return e;
-  balance_finish_kernel<<<(unsigned)p.seqs, kFinishThreads, 0, stream>>>(p.experts, p.k, p.splits, p.sums, p.part_counts,
-                                                                         p.held, p.alpha, p.seq_loss, p.done, p.loss,
-                                                                         p.counts, p.coef);
+  int lanes = 1;   // a sequence's lanes where its partials are counted
+  while (lanes < 64 && lanes < p.splits) lanes *= 2;
+  balance_finish_kernel<<<dim3((unsigned)balance_chunks(p.experts), (unsigned)p.seqs), kFinishThreads, 0, stream>>>(
+      p.experts, p.k, p.splits, p.seqs, lanes, p.sums, p.part_counts, p.held, p.alpha, p.shares, p.done, p.loss, p.counts,
+      p.coef);
   return hipGetLastError();
 }
 
@@ -695,11 +1285,24 @@ hipError_t launch_gate_backward(const GateGradParams& p, hipStream_t stream) {
   a.rows = p.rows; a.E = p.experts; a.k = p.k; a.renorm = p.renorm; a.scale = p.scale; a.ids = p.ids;
   a.grad_weights = p.grad_weights; a.grad_loss = p.grad_loss; a.coef = p.coef; a.off = p.off; a.seqs = p.seqs;
   a.mask = p.mask;
-  const unsigned grid = (unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock);
   return with_type(p.dtype, [&](auto* t) {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(t)>>;
+    if (p.experts <= kMost16)
+      return with_width16(p.experts, [&](auto w) {
+        constexpr int V = decltype(w)::value;
+        const unsigned grid = (unsigned)((p.rows + 4 * kRowsPerBlock - 1) / (4 * kRowsPerBlock));
+        constexpr int W = kPiece<T, V>;
+        a.vec = wide_rows<T>(p.logits, p.experts, W) && wide_rows<T>(p.grad, p.experts, W);
+        const bool vec_coef = wide_rows<float>(p.coef, p.experts, W);
+        auto go = [&](auto kernel) {
+          kernel<<<grid, 64 * kRowsPerBlock, 0, stream>>>((const T*)p.logits, a, vec_coef, (T*)p.grad);
+          return hipGetLastError();
+        };
+        return p.sigmoid ? go(gate16_backward_kernel<T, V, false>) : go(gate16_backward_kernel<T, V, true>);
+      });
     return with_width(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
+      const unsigned grid = (unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock);
       a.vec = wide_rows<T>(p.logits, p.experts, V);
       const size_t lds = sizeof(float) * kRowsPerBlock * 64 * V;
       if (p.sigmoid)
