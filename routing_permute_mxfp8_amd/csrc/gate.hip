@@ -123,12 +123,14 @@ __device__ __forceinline__ RowNorm<R> softmax_norm(const float (&x)[V]) {
   for (int v = 0; v < V; ++v) sum += exp_of(R(x[v]) - R(mx));
   return RowNorm<R>{R(mx), R(1) / wave_sum(sum)};
 }
+__device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }   // V_RCP_F32, 1 ulp
+__device__ __forceinline__ double reciprocal(double x) { return 1.0 / x; }
 template <typename R, bool SOFTMAX>
 __device__ __forceinline__ R score_of(float x, const RowNorm<R>& n) {
   if constexpr (SOFTMAX)
     return exp_of(R(x) - n.m) * n.inv;
   else
-    return R(1) / (R(1) + exp_of(-R(x)));   // 1 / (1 + inf) = 0 for -inf
+    return reciprocal(R(1) + exp_of(-R(x)));   // 1 / (1 + inf) = 0 for -inf
 }
 
 // ---- gate -----------------------------------------------------------------------------
@@ -343,10 +345,12 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __res
 // is one instruction and equal ranks are in index order. Each lane sorts its keys, and four
 // exchanges between lanes merge the lists of the eight largest: about 60 instructions a
 // row, where a maximum over the wave for each of the K takes about 20 for each.
-// The eight then order themselves by their whole ranks. The lower 8 bits that the keys drop
-// may hide which of two is the K-th, and the rounding of the ranks the order of two
-// neighbours: such rows (about one of a hundred fp32 rows with a bias, none of fp16 or bf16
-// logits without one, which the 24 bits hold exactly) are decided one at a time by the whole wave.
+// The lower 8 bits that the keys drop and the rounding of the ranks may hide the order of two
+// neighbours (not of fp16 or bf16 logits without a bias, which the 24 bits hold exactly): the
+// eight and the ninth order themselves by their whole ranks, and where those are within
+// their errors by ranks in 64 bits. What stays open, a tenth that near to the K-th or two
+// groups that near at the border (about one row of a thousand), is decided row by row by
+// the whole wave: deciding every near row so took 20 of 34 us at 32768 x 256 in groups.
 constexpr int kTop = 8;
 
 __device__ __forceinline__ uint32_t order_key(float r, int e) {
@@ -487,18 +491,23 @@ __device__ __forceinline__ void clean_dealt(const T (&raw)[V], int E, int sub, f
   }
 }
 
+__device__ __forceinline__ double row_sum(double v) {
+  for (int d = 1; d < 16; d *= 2) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
 // softmax_norm of a row held by 16 lanes.
-template <int V>
-__device__ __forceinline__ RowNorm<float> row_norm(const float (&x)[V]) {
+template <typename R, int V>
+__device__ __forceinline__ RowNorm<R> row_norm(const float (&x)[V]) {
   float m = x[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
   m = fmaxf(row_max(m), -FLT_MAX);   // (a row of -inf only: exp(-inf) = 0 throughout)
-  float sum = 0.0f;
+  R sum = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) sum += exp_of(x[v] - m);
+  for (int v = 0; v < V; ++v) sum += exp_of(R(x[v]) - R(m));
   sum = row_sum(sum);
-  return RowNorm<float>{m, sum > 0.0f ? 1.0f / sum : 0.0f};
+  return RowNorm<R>{R(m), sum > R(0) ? R(1) / sum : R(0)};
 }
 
 template <typename T, int V, bool SOFTMAX, bool BIAS>
@@ -518,10 +527,10 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
     clean_part<T, V>(raw, p.E, sub, x);
   }
   RowNorm<float> norm{0.0f, 0.0f};
-  if constexpr (SOFTMAX) norm = row_norm<V>(x);
+  if constexpr (SOFTMAX) norm = row_norm<float, V>(x);
   const float top = SOFTMAX ? norm.inv : 1.0f;
   float r[V];
-  bool close = false;
+  bool redo = false;   // decided by the whole wave
   bool stays = true;
   const bool groups = p.groups > 1;   // uniform
   if (BIAS || groups) {
@@ -555,13 +564,14 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
       if ((L & (p.lanes - 1)) == 0 && h < p.groups) {   // uniform
         const float o = dppf<0x150 + L>(score);   // lane L of each row of 16
         better += (int)(o > score) | ((int)(o == score) & (int)(h < g));
-        close |= (h != g) & (fabsf(o - score) <= tau);
       }
     };
     [&]<int... L>(std::integer_sequence<int, L...>) { (against(std::integral_constant<int, L>{}), ...); }
     (std::make_integer_sequence<int, 16>{});
-    stays = better < p.topk_groups && g < p.groups;
-    close = close && p.topk_groups < p.groups;
+    stays = (better < p.topk_groups) & (g < p.groups);
+    const float lowest = -row_max(stays ? -score : -INFINITY);
+    const float highest = row_max((!stays & (g < p.groups)) ? score : -INFINITY);
+    redo = lowest - highest <= tau;   // (-inf - -inf, NaN: equal groups, in index order)
   }
   uint32_t key[V];
 #pragma unroll
@@ -592,33 +602,45 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
   merge_lanes<kX2>(best);
   merge_lanes<kX4>(best);
   merge_lanes<kX8>(best);
-  // lane j of a row: candidate j of the eight
+  // Lane j of a row: candidate j, the eight best and the one after them.
   uint32_t mine = best[0];
 #pragma unroll
   for (int i = 1; i < kTop; ++i) mine = sub == i ? best[i] : mine;
-  const bool held = sub < kTop && mine != 0u;
+  constexpr bool kCut = BIAS || sizeof(T) == 4;   // keys may hide an order
+  constexpr int kCandidates = kCut ? kTop + 1 : kTop;
+  auto next_key = [&](uint32_t after) {   // the row's largest key below `after`
+    uint32_t k = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) k = max(k, key[v] < after ? key[v] : 0u);
+    return row_max(k);
+  };
+  uint32_t ninth = 0;
+  if constexpr (kCut) {
+    ninth = next_key(best[kTop - 1]);
+    mine = sub == kTop ? ninth : mine;
+  }
+  const bool held = (sub < kCandidates) & (mine != 0u);
   const int id = 255 - (int)(mine & 255u);
   const float l = held ? clean(to_float(rp[held ? id : 0])) : -INFINITY;
   const float s = l == -INFINITY ? 0.0f : score_of<float, SOFTMAX>(l, norm);
   int at = sub;   // its place in the row
-  if constexpr (BIAS || sizeof(T) == 4) {
-    // Certain so far: what the keys put clearly apart. The K-th choice has to be clear of the
-    // first one that is not a candidate any more.
+  if constexpr (kCut) {
     const float tau = BIAS ? top * 0x1p-18f : 0.0f;
-    uint32_t kth = best[0], beyond = best[kTop - 1];
+    // what is no candidate has to be clear of the K-th choice
+    uint32_t kth = best[0];
 #pragma unroll
     for (int i = 1; i < kTop; ++i) kth = p.k == i + 1 ? best[i] : kth;
-    if (p.k == kTop) {   // uniform
-      beyond = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) beyond = max(beyond, key[v] < best[kTop - 1] ? key[v] : 0u);
-      beyond = row_max(beyond);
-    }
-    const float u = key_value(kth), w = key_value(beyond);
-    close |= (beyond != 0u) & !(u - w > tau + 0x1p-14f * fmaxf(fabsf(u), fabsf(w)));
-    // The candidates' own order by their whole ranks, and of those by their errors.
-    const float rank = !held ? NAN : BIAS ? (l == -INFINITY ? -INFINITY : s + p.bias[id]) : l;
-    const float reach = tau + (BIAS ? fabsf(rank) * 0x1p-21f : 0.0f);
+    auto near = [&](uint32_t beyond) {
+      const float u = key_value(kth), w = key_value(beyond);
+      return (beyond != 0u) & !(u - w > tau + 0x1p-14f * fmaxf(fabsf(u), fabsf(w)));
+    };
+    if (__ballot(near(ninth))) redo |= near(next_key(ninth));
+    // the candidates' order by their whole ranks, and where those are within their errors by
+    // ranks in 64 bits
+    const float b = BIAS && held ? p.bias[id] : 0.0f;
+    const float rank = !held ? NAN : BIAS ? (l == -INFINITY ? -INFINITY : s + b) : l;
+    const float reach = tau + fabsf(rank) * 0x1p-21f;
+    bool close = false;
     at = 0;
     auto against = [&]<int L>(std::integral_constant<int, L>) {
       const float o = dppf<0x150 + L>(rank);
@@ -626,18 +648,32 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
       at += (int)(o > rank) | ((int)(o == rank) & (int)(oid < id));
       if constexpr (BIAS) close |= (L != sub) & (fabsf(o - rank) <= reach);
     };
-    [&]<int... L>(std::integer_sequence<int, L...>) { (against(std::integral_constant<int, L>{}), ...); }
-    (std::make_integer_sequence<int, kTop>{});
+    auto against_all = [&]<int... L>(std::integer_sequence<int, L...>) { (against(std::integral_constant<int, L>{}), ...); };
+    against_all(std::make_integer_sequence<int, kCandidates>{});
+    if (BIAS && __ballot(close)) {
+      RowNorm<double> exact{0.0, 0.0};
+      if constexpr (SOFTMAX) exact = row_norm<double, V>(x);
+      const double r64 = rank == rank && l > -INFINITY ? score_of<double, SOFTMAX>(l, exact) + (double)b : (double)rank;
+      const uint64_t bits = __builtin_bit_cast(uint64_t, r64);
+      at = 0;
+      auto against64 = [&]<int L>(std::integral_constant<int, L>) {
+        const uint64_t u = ((uint64_t)dppu<0x150 + L>((uint32_t)(bits >> 32)) << 32) | dppu<0x150 + L>((uint32_t)bits);
+        const double o = __builtin_bit_cast(double, u);
+        const int oid = (int)dppu<0x150 + L>((uint32_t)id);
+        at += (int)(o > r64) | ((int)(o == r64) & (int)(oid < id));
+      };
+      [&]<int... L>(std::integer_sequence<int, L...>) { (against64(std::integral_constant<int, L>{}), ...); }
+      (std::make_integer_sequence<int, kCandidates>{});
+    }
   }
-  const bool chosen = held && at < p.k;
+  const bool chosen = held & (at < p.k);
   float weight = chosen ? s : 0.0f;
   if (p.renorm) {
     const float total = row_sum(weight);
     weight = total > 0.0f ? weight / total : 0.0f;
   }
-  uint64_t again = __ballot(close && there);   // any lane of a row
-  const bool redo = (again >> (lane & 48)) & 0xffff;
-  if (chosen && there && !redo) {
+  uint64_t again = __ballot(redo & there);   // the same for the lanes of a row
+  if (chosen & there & !redo) {
     p.ids[row * p.k + at] = id;
     p.weights[row * p.k + at] = weight * p.scale;
   }
@@ -779,7 +815,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
     float x[V];
     clean_dealt<T, V, W>(cur.raw, E, sub, x);
     if constexpr (SOFTMAX) {
-      RowNorm<float> n = row_norm<V>(x);
+      RowNorm<float> n = row_norm<float, V>(x);
       if (!counted) n.inv = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] += score_of<float, true>(x[v], n);
@@ -1074,7 +1110,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(con
   float x[V], s[V], d[V];
   clean_dealt<T, V, W>(raw, p.E, sub, x);
   RowNorm<float> norm{0.0f, 0.0f};
-  if constexpr (SOFTMAX) norm = row_norm<V>(x);
+  if constexpr (SOFTMAX) norm = row_norm<float, V>(x);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     s[v] = score_of<float, SOFTMAX>(x[v], norm);
