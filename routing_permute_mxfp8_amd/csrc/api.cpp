@@ -426,7 +426,7 @@ moe_status check_fp4_matmul(int64_t rows, int64_t groups, int64_t n, int64_t k, 
 
 moe::Fp4MatmulParams carve_fp4_matmul(Carver& cv, int64_t rows, int64_t groups, int64_t n, int64_t k, int x_dtype) {
   moe::Fp4MatmulParams p;
-  p.mt = moe::fp4_tile_rows(rows, groups, n, k);
+  p.mt = moe::fp4_tile_rows(rows, groups, n, k, x_dtype != MOE_DTYPE_FP4_E2M1);
   if (p.mt != 0 && x_dtype != MOE_DTYPE_FP4_E2M1) {
     p.x_codes = cv.take<uint8_t>((size_t)(rows * (k / 2)));
     p.x_code_scales = cv.take<uint8_t>((size_t)(rows * (k / 32)));

@@ -169,10 +169,33 @@ hipError_t launch_out(const Fp4MatmulParams& p, hipStream_t stream) {
 
 }  // namespace
 
-int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k) {
+// Which kernel, and its tile: 0 for the kernel above, else the rows of the LDS-staged one's.
+//
+// The kernel above splits K over its waves, so it is done soonest where there is little to
+// read, but streams at 3 TB/s at best and reads the weights again for every 16 rows; the other
+// comes to 6, after about half a microsecond for each K step of 128 and three more. (8 groups,
+// 2048 x 1024, 4 rows each: 5.9 and 12 us; 16 groups, 2048 x 2048: 13.4 and 13.8; 32: 24 and
+// 18; 64 groups, 7168 x 4096: 293 and 156; one row, 7168 x 8192: 12.7 and 30, x 32768: 40 and
+// 35.) Values are quantised by a launch of their own there, 3 us more.
+//
+// Tiles a little larger than the average group, because the sizes scatter (64 groups of 7168 x
+// 4096, microseconds with tiles of 32, 64, 128 and 256 rows, us: 16 rows each 163, 174, 207,
+// -; 24: 193, 184, 209, 275; 48: 353, 223, 227, 285; 96: 590, 413, 240, 299; 160: 938, 592,
+// 390, 342; 320: 1854, 1075, 612, 576), but smaller ones where the tiles would not occupy the
+// chip (5 groups of 155 rows, 1408 x 2000: 14.5, 12.0, 16.5, 21.5). With at most a tile of
+// rows a group the weights are read once and non-temporal (40 rows each: 201 us, 212 cached;
+// 160 rows: 592, 478 cached).
+int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool values) {
+  if (rows <= 0) return 0;
+  constexpr int64_t kStart = 9 << 20;   // bytes the kernel above reads in 3 us
   const int64_t per = (rows + groups - 1) / groups;
-  if (per <= 16) return 0;
-  return per <= 64 ? 64 : per <= 128 ? 128 : 256;
+  const double bytes = (double)((per + 15) / 16) * (double)(std::min(groups, rows) * n) * (double)(k / 2);
+  if (bytes < (double)(kStart * (values ? 2 : 1) + k * (kStart / 6 / 128))) return 0;
+  if (per <= 20) return 32;
+  int mt = per <= 48 ? 64 : per <= 112 ? 128 : 256;
+  const auto items = [&](int m) { return groups * ((per + m - 1) / m) * ((n + 255) / 256); };
+  while (mt > 64 && items(mt) < 256) mt /= 2;
+  return mt;
 }
 
 hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream) {

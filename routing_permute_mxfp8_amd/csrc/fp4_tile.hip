@@ -1,23 +1,26 @@
 // MXFP4 x MXFP4 product of expert groups of many rows: both operands staged in LDS.
 //
-// A work item is a tile of MT rows of one group by 256 output channels, computed by four
+// A work item is a tile of MT rows of one group by NT output channels, computed by four
 // waves (one per SIMD), each holding CB x RB accumulators of 32 channels x 32 rows
 // (V_MFMA_SCALE_F32_32X32X64_F8F6F4, weights in the A slot: a lane holds 4 consecutive
 // channels of one row). Blocks are persistent and XCD-aware.
 //
 // FP4 doubles the MFMA's rate against FP8 at the same operand rows, so the LDS reads are
 // what a wave's tile shape decides: 128 x 128 a wave takes 64 of the 128 bytes a clock the
-// CU's LDS delivers, 128 x 64 takes 96, 64 x 64 all of them. One wave a SIMD with 256
-// accumulator registers is therefore better than more, smaller waves.
+// CU's LDS delivers, 128 x 64 takes 96, 64 x 64 all of them. For many rows one wave a SIMD
+// with 256 accumulator registers is therefore better than more, smaller waves. For few rows
+// the weight stream is what takes the time, and two or three blocks a CU keep it going.
 //
-// Per K step of 128 the codes of 256 weight rows and MT rows of x go straight from memory
-// into one of four LDS slots, issued four steps ahead, and are read from there half a step
+// The codes of NT weight rows and MT rows of x go straight from memory into LDS, two K steps
+// of 128 at a time: 128 bytes a row, whole cache lines (64 experts of 4096 x 7168, 4 rows
+// each, single steps: 199 us, pairs: 182). Four steps are staged; a pair is issued as soon as
+// all waves have read the one before it there, and operands are read from LDS half a step
 // ahead of their MFMAs; one barrier a step, between its two halves. The loads go on across
 // items, so an item's first steps are under way while the last ones of the item before are
 // multiplied. The E8M0 scales of four steps (a quad) come through registers, 16 bytes a row.
 //
-// LDS rows hold 64 bytes, four 16-byte chunks (32 K elements each); chunk c of row r sits at
-// place c ^ (r / 2 % 4), so that the eight lanes of a read pass (eight rows, one chunk) touch
+// An LDS row of a pair holds eight 16-byte chunks (32 K elements each); chunk c of row r sits
+// at place c ^ (r % 8), so that the eight lanes of a read pass (eight rows, one chunk) touch
 // all banks once. The direct-to-LDS loads write linearly; their lanes fetch the chunk that
 // belongs at their place, wherever the weight format has it.
 
@@ -63,26 +66,25 @@ struct TileArgs {
   int groups, rows, K, N;
 };
 
-constexpr int kNT = 256;          // channels of an item
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 1024;
-constexpr int kList = kThreads;   // items described at a time
+constexpr int kList = 64;   // items described at a time
 constexpr int kSlots = 4;         // K steps staged in LDS
 
-// WC waves along the channels, 4 / WC along the rows; RB 32-row blocks a wave.
-template <int WC, int RB>
+// WC waves along the channels, 4 / WC along the rows; CB x RB 32 x 32 blocks a wave; BLOCKS
+// blocks a CU.
+template <int WC, int CB, int RB, int BLOCKS>
 struct TileShape {
-  static constexpr int kCB = kNT / 32 / WC;             // 32-channel blocks a wave
-  static constexpr int kMT = 4 / WC * RB * 32;
-  static constexpr int kA = kNT * 64, kB = kMT * 64;    // bytes of a step: weights, rows
-  static constexpr int kStep = kA + kB;
+  static constexpr int kNT = 32 * WC * CB, kMT = 32 * (4 / WC) * RB;
+  static constexpr int kA = kNT * 128, kB = kMT * 128;  // bytes of a pair of steps: weights, rows
+  static constexpr int kPair = kA + kB;
   static constexpr int kSA = kNT * 16, kSB = kMT * 16;  // bytes of a quad's scales
   static constexpr int kQuad = kSA + kSB;
-  static constexpr int kScales = kSlots * kStep, kEnds = kScales + 2 * kQuad, kItems = kEnds + 4 * kMaxGroups;
+  static constexpr int kScales = 2 * kPair, kEnds = kScales + 2 * kQuad, kItems = kEnds + 4 * kMaxGroups;
   static constexpr int kLds = kItems + 16 * kList;
-  static constexpr int kLA = kNT / 64, kLB = kMT / 64;   // direct-to-LDS loads a wave and step (16 rows each)
-  static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
-  static_assert(kMT <= kThreads && kMT % 64 == 0, "rows of an item");
+  static constexpr int kLA = kNT / 32, kLB = kMT / 32;   // direct-to-LDS loads a wave and pair (8 rows each)
+  static_assert(kLds * BLOCKS <= 160 * 1024, "LDS of a compute unit");
+  static_assert(kMT <= kThreads && kNT <= kThreads, "a thread loads a row's scales");
 };
 
 // Keeps the accumulators in accumulation registers across loop edges (left to itself the
@@ -165,11 +167,11 @@ __device__ __forceinline__ int4 describe(const TileArgs& p, const int* ends, int
 // The body gets the LDS area twice, as two restrict pointers: one for the direct-to-LDS
 // loads, one for every other access. The compiler then does not make each LDS read wait for
 // every direct-to-LDS load in flight; slot_barrier orders them.
-template <int WC, int RB, typename O, bool PACKED>
+template <int WC, int CB, int RB, int BLOCKS, bool ONCE, typename O, bool PACKED>
 __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out, uint8_t* __restrict__ dma,
                                           uint8_t* __restrict__ lds) {
-  using S = TileShape<WC, RB>;
-  constexpr int CB = S::kCB, MT = S::kMT;
+  using S = TileShape<WC, CB, RB, BLOCKS>;
+  constexpr int MT = S::kMT, kNT = S::kNT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wc = wave % WC, wr = wave / WC;
   const int ks = p.K >> 7, kq = (ks + 3) >> 2, half = p.K >> 1, n16 = p.N >> 4;
@@ -186,7 +188,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   const int count = (int)((end - begin + per - 1) / per);
   auto fill = [&](int first) {   // list[i] = this block's item first + i
     __syncthreads();
-    if (first + tid < count) list[tid] = describe<MT>(p, ends, tiles, ncb, (int)(begin + (int64_t)(first + tid) * per));
+    if (tid < kList && first + tid < count) list[tid] = describe<MT>(p, ends, tiles, ncb, (int)(begin + (int64_t)(first + tid) * per));
     __syncthreads();
   };
   auto item = [&](int i) {
@@ -195,14 +197,17 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
                 __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w)};
   };
 
-  // code loads: load i of a wave fills 16 rows, lane l place l % 4 of row l / 4
-  const int row_l = lane >> 2, chunk_l = (lane & 3) ^ ((lane >> 3) & 3);
+  // code loads: load i of a wave fills 8 rows, lane l place l % 8 of row l / 8
+  const int row_l = lane >> 3, chunk_l = (lane & 7) ^ row_l;
   int va[S::kLA], vb[S::kLB];
 #pragma unroll
-  for (int i = 0; i < S::kLA; ++i)
-    va[i] = (wave * S::kLA + i) * 16 * half + (PACKED ? chunk_l * 256 + row_l * 16 : row_l * half + chunk_l * 16);
+  for (int i = 0; i < S::kLA; ++i) {
+    const int row = (wave * S::kLA + i) * 8 + row_l;
+    va[i] = PACKED ? (row >> 4) * 16 * half + (chunk_l >> 2) * 1024 + (chunk_l & 3) * 256 + (row & 15) * 16
+                   : row * half + chunk_l * 16;
+  }
 #pragma unroll
-  for (int i = 0; i < S::kLB; ++i) vb[i] = ((wave * S::kLB + i) * 16 + row_l) * half + chunk_l * 16;
+  for (int i = 0; i < S::kLB; ++i) vb[i] = ((wave * S::kLB + i) * 8 + row_l) * half + chunk_l * 16;
 
   // The item whose loads are being issued: buffers of exactly its rows (what lies behind
   // reads as zeros, without memory traffic).
@@ -222,18 +227,23 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
     vsa = PACKED ? (uint32_t)((ra >> 4) * kq * 256 + (ra & 15) * 4) : (uint32_t)(ra * 4 * ks);
     vsb = (uint32_t)(rb * 4 * ks);
   };
-  auto issue_step = [&](int slot, int step, bool in) {   // !in: zeros
+  // Steps `step` and step + 1 (step even) into pair slot `slot`; !in: zeros. Of an odd number
+  // of steps the last pair's second half is whatever follows in the item's buffer, or zeros
+  // behind it; its scales are made to vanish (store_scales). The step is part of the lane's
+  // offset, not of the scalar one, because only that is checked against the buffer's size.
+  // ONCE: the weights are used by this item alone, so they are loaded non-temporal.
+  auto issue_pair = [&](int slot, int step, bool in) {
     const __amdgpu_buffer_rsrc_t wr_ = buffer_of(bw, in ? wbytes : 0), xr_ = buffer_of(bx, in ? xbytes : 0);
-    uint8_t* base = dma + slot * S::kStep;
+    uint8_t* base = dma + slot * S::kPair;
     const int s = in ? step : 0;
 #pragma unroll
     for (int i = 0; i < S::kLA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr_, (lds_ptr)(base + (wave * S::kLA + i) * 1024), 16, va[i],
-                                               s * (PACKED ? 1024 : 64), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr_, (lds_ptr)(base + (wave * S::kLA + i) * 1024), 16,
+                                               va[i] + s * (PACKED ? 1024 : 64), 0, 0, ONCE ? 2 : 0);
 #pragma unroll
     for (int i = 0; i < S::kLB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr_, (lds_ptr)(base + S::kA + (wave * S::kLB + i) * 1024), 16, vb[i],
-                                               s * 64, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr_, (lds_ptr)(base + S::kA + (wave * S::kLB + i) * 1024), 16,
+                                               vb[i] + s * 64, 0, 0, 0);
   };
   // The scales of a quad: thread t holds row t's 16 bytes, dword j the four blocks of step j
   // (the packed weight scales come as dword g = block g of the four steps and are transposed).
@@ -283,21 +293,21 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
       x[j] = 4 * q + j < ks ? x[j] : 0;
     }
     uint8_t* base = lds + S::kScales + area * S::kQuad + 16 * tid;
-    *reinterpret_cast<u32x4*>(base) = a;
+    if (kNT == kThreads || tid < kNT) *reinterpret_cast<u32x4*>(base) = a;
     if (MT == kThreads || tid < MT) *reinterpret_cast<u32x4*>(base + S::kSA) = x;
   };
 
   // operand reads of a wave: sub-step s of a step (64 elements), lane (h, r) = row r, chunk 2 s + h
   const int h = lane >> 5;
-  const int read0 = (lane & 31) * 64 + ((h ^ ((lane >> 1) & 3)) * 16);
+  const int read0 = (lane & 31) * 128 + ((h ^ (lane & 7)) * 16);
   u32x4 a[2][CB], bx_[2][RB];
   uint32_t sa[CB], sx[RB];
-  auto read_step = [&](int buf, int s) {
-    const uint8_t* base = lds + buf * S::kStep + (read0 ^ (32 * s));
+  auto read_step = [&](int j, int s) {   // step j of the quad
+    const uint8_t* base = lds + (j >> 1) * S::kPair + (read0 ^ (32 * s) ^ (64 * (j & 1)));
 #pragma unroll
-    for (int i = 0; i < CB; ++i) a[s][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 2048);
+    for (int i = 0; i < CB; ++i) a[s][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 4096);
 #pragma unroll
-    for (int i = 0; i < RB; ++i) bx_[s][i] = *reinterpret_cast<const u32x4*>(base + S::kA + (wr * RB + i) * 2048);
+    for (int i = 0; i < RB; ++i) bx_[s][i] = *reinterpret_cast<const u32x4*>(base + S::kA + (wr * RB + i) * 4096);
   };
   // the lane's rows' scales of step j of the quad, shifted so that block h of the step is
   // byte 0 and block 2 + h byte 2 (the MFMA selects a byte)
@@ -324,16 +334,16 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   constexpr std::integral_constant<int, 2> k2{};
   constexpr std::integral_constant<int, 3> k3{};
 
-  constexpr int kCodes = S::kLA + S::kLB, kScaleLoads = PACKED ? 5 : 2;   // loads of a step, of a quad's scales
+  constexpr int kCodes = S::kLA + S::kLB, kScaleLoads = PACKED ? 5 : 2;   // loads of a pair, of a quad's scales
 
   fill(0);
   Item cur = item(0);
   aim(cur);
   load_scales(0);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) issue_step(j, j, j < ks);
+  issue_pair(0, 0, true);
+  issue_pair(1, 2, 2 < ks);
   store_scales(0, 0);
-  slot_barrier<3 * kCodes>();
+  slot_barrier<kCodes>();
   read_scales(0, 0);
   read_step(0, 0);
 
@@ -345,11 +355,12 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
       read_step(J, 1);
       if constexpr (J == 3) store_scales(area ^ 1, nq);
       multiply(k0);
-      // step J + 1 has landed: newer are the codes of the two steps behind it, and the next
-      // quad's scales where they were issued among these
-      slot_barrier<2 * kCodes + (J == 1 || J == 2 ? kScaleLoads : 0)>();
+      // Step J + 1 has landed. Newer loads: behind the first pair the second; behind the second
+      // one the next quad's scales (from step 1 on) and its first pair (from step 2 on), behind
+      // which nothing has been issued at step 3.
+      slot_barrier<J == 0 ? kCodes : J == 1 ? kScaleLoads : J == 2 ? kScaleLoads + kCodes : 0>();
       if constexpr (J == 0) load_scales(nq);
-      issue_step(J, 4 * nq + J, more && 4 * nq + J < ks);
+      if constexpr (J == 1 || J == 3) issue_pair(J >> 1, 4 * nq + J - 1, more && 4 * nq + J - 1 < ks);
       read_step((J + 1) & 3, 0);
       multiply(k1);
       read_scales(J == 3 ? area ^ 1 : area, (J + 1) & 3);
@@ -396,11 +407,11 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (15 << 8));   // no direct-to-LDS load outlives the block
 }
 
-template <int WC, int RB, typename O, bool PACKED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1))) void fp4_tile_kernel(
+template <int WC, int CB, int RB, int BLOCKS, bool ONCE, typename O, bool PACKED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BLOCKS))) void fp4_tile_kernel(
     TileArgs p, O* __restrict__ out) {
   extern __shared__ __align__(16) uint8_t lds_area[];
-  tile_body<WC, RB, O, PACKED>(p, out, lds_area, lds_area);
+  tile_body<WC, CB, RB, BLOCKS, ONCE, O, PACKED>(p, out, lds_area, lds_area);
 }
 
 // The device's compute units, rounded up to whole XCDs' shares; the kernel's LDS size set
@@ -423,23 +434,26 @@ hipError_t tile_grid(const void* kernel, int lds, int* grid) {
   return hipSuccess;
 }
 
-template <int WC, int RB, typename O, bool PACKED>
+template <int WC, int CB, int RB, int BLOCKS, bool ONCE, typename O, bool PACKED>
 hipError_t launch_tiles(const TileArgs& a, void* out, hipStream_t stream) {
-  using S = TileShape<WC, RB>;
+  using S = TileShape<WC, CB, RB, BLOCKS>;
   int grid = 0;
-  const auto kernel = fp4_tile_kernel<WC, RB, O, PACKED>;
+  const auto kernel = fp4_tile_kernel<WC, CB, RB, BLOCKS, ONCE, O, PACKED>;
   hipError_t e = tile_grid(reinterpret_cast<const void*>(kernel), S::kLds, &grid);
   if (e != hipSuccess) return e;
-  kernel<<<grid, kThreads, S::kLds, stream>>>(a, (O*)out);
+  kernel<<<grid * BLOCKS, kThreads, S::kLds, stream>>>(a, (O*)out);
   return hipGetLastError();
 }
 
 template <typename O, bool PACKED>
 hipError_t launch_shape(const Fp4MatmulParams& p, const TileArgs& a, hipStream_t stream) {
   switch (p.mt) {
-    case 256: return launch_tiles<2, 4, O, PACKED>(a, p.out, stream);
-    case 128: return launch_tiles<2, 2, O, PACKED>(a, p.out, stream);
-    default: return launch_tiles<4, 2, O, PACKED>(a, p.out, stream);
+    case 256: return launch_tiles<2, 4, 4, 1, false, O, PACKED>(a, p.out, stream);
+    case 128: return launch_tiles<2, 4, 2, 1, false, O, PACKED>(a, p.out, stream);
+    case 64:   // (weights of few rows non-temporal: see fp4_tile_rows)
+      return p.rows <= (int64_t)64 * p.groups ? launch_tiles<4, 1, 2, 2, true, O, PACKED>(a, p.out, stream)
+                                              : launch_tiles<4, 1, 2, 2, false, O, PACKED>(a, p.out, stream);
+    default: return launch_tiles<4, 1, 1, 3, true, O, PACKED>(a, p.out, stream);
   }
 }
 

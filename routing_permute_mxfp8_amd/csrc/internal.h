@@ -322,7 +322,7 @@ struct Fp4MatmulParams {
   uint8_t* x_code_scales = nullptr;  // [rows, k/32]
 };
 // Rows of an item for a call (0: the kernel for few rows).
-int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k);
+int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool values);
 hipError_t launch_fp4_tiles(const Fp4MatmulParams& p, hipStream_t stream);
 hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream);
 

@@ -241,3 +241,51 @@ def test_more_items_than_a_block_lists_at_once():
     for lo in range(0, rows, 50_000):
         part = pick[lo:lo + 50_000].to(DEV)
         assert torch.equal(got[lo:lo + 50_000], got[first[part]])
+
+
+def drawn(groups, n, k, seed):
+    """Random weight codes and scales with their float64 value, made without quantising."""
+    rng = np.random.default_rng(seed)
+    c = rng.integers(0, 256, (groups, n, k // 2), dtype=np.uint8)
+    s = rng.integers(118, 128, (groups, n, k // 32), dtype=np.uint8)
+    table = mxfp.dequantize(np.arange(16, dtype=np.uint8).repeat(32).reshape(16, 32), np.full((16, 1), 127, np.uint8),
+                            "e2m1")[:, 0]
+    v = np.stack([table[c & 15], table[c >> 4]], axis=-1).reshape(groups, n, k)
+    v *= np.repeat(np.exp2(s.astype(np.float64) - 127), 32, axis=-1)
+    return c, s, v
+
+
+def scattered(rows, groups, rng, outside):
+    """Offsets of groups of unequal sizes, some without rows, `outside` rows before and behind."""
+    share = rng.gamma(1.5, size=groups) * (rng.random(groups) > 0.15)
+    sizes = rng.multinomial(rows - 2 * outside, share / share.sum())
+    return [outside, *(outside + np.cumsum(sizes)).tolist()]
+
+
+@pytest.mark.parametrize("groups,per,n,k", [
+    (90, 1, 2064, 128), (90, 9, 2064, 128), (80, 3, 1136, 640), (80, 18, 1136, 640), (300, 1, 528, 512),   # one small tile
+    (40, 30, 1136, 640), (60, 45, 1040, 384),                                                             # a tile of 64
+    (3, 234, 1040, 896), (5, 156, 2000, 1408),                                       # tiles of 64, to occupy the chip
+    (30, 100, 2064, 384), (130, 60, 272, 128),                                                            # of 128
+    (30, 200, 2064, 384), (2, 4100, 2064, 256)])                                                          # of 256
+def test_tiles_of_every_size(groups, per, n, k):
+    wc, ws, wv = drawn(groups, n, k, seed=per)
+    nd = (to_dev(wc), to_dev(ws))
+    pk = rp.pack_weights(*nd, fp4=True)
+    for i, (dtype, out_dtype, packed) in enumerate(KINDS):
+        rng = np.random.default_rng(i)
+        off = scattered(groups * per, groups, rng, outside=i % 2)
+        say(f"mxfp4_matmul tiles groups={groups} per={per} n={n} k={k} x={dtype} out={out_dtype} packed={packed}")
+        x = rng.standard_normal((groups * per, k)) * np.exp(rng.uniform(-2, 2, (groups * per, 1)))
+        if dtype is not None:
+            t = torch.from_numpy(x.astype(np.float32)).to(dtype)
+            x = t.double().numpy()
+        xc, xs, xv = fp4(x)
+        out = torch.full((groups * per, n), 7.0, dtype=out_dtype, device=DEV)
+        w, s = pk if packed else nd
+        got = rp.mxfp4_matmul(to_dev(xc) if dtype is None else t.to(DEV), w, s, group_offsets=torch.tensor(
+            off, dtype=torch.int32, device=DEV), out=out, x_scales=to_dev(xs) if dtype is None else None,
+            weight_format=rp.WEIGHTS_PACKED if packed else rp.WEIGHTS_ND)
+        torch.cuda.synchronize()
+        check(got, xv, wv, off, out_dtype)
+        assert bool((got[:off[0]] == 7).all()) and bool((got[off[-1]:] == 7).all())
