@@ -97,14 +97,11 @@ __device__ __forceinline__ void pin(v16f (&acc)[CB][RB]) {
     for (int j = 0; j < RB; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-// Waits for the wave's direct-to-LDS loads but the newest N vector memory operations and for
-// its LDS accesses, then for the other waves: what was loaded or written is there for all,
-// and what was read may be written again. (vmcnt counts in order.)
-template <int N>
+// Waits for the wave's loads and LDS accesses, then for the other waves: what was loaded or
+// written is there for all, and what was read may be written again.
 __device__ __forceinline__ void slot_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+  __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (0 << 8));
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
@@ -232,18 +229,22 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   // behind it; its scales are made to vanish (store_scales). The step is part of the lane's
   // offset, not of the scalar one, because only that is checked against the buffer's size.
   // ONCE: the weights are used by this item alone, so they are loaded non-temporal.
-  auto issue_pair = [&](int slot, int step, bool in) {
-    const __amdgpu_buffer_rsrc_t wr_ = buffer_of(bw, in ? wbytes : 0), xr_ = buffer_of(bx, in ? xbytes : 0);
+  constexpr int kCodes = S::kLA + S::kLB;   // loads of a pair
+  auto issue = [&](int slot, int step, bool in, int i) {   // load i of the pair
     uint8_t* base = dma + slot * S::kPair;
     const int s = in ? step : 0;
-#pragma unroll
-    for (int i = 0; i < S::kLA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr_, (lds_ptr)(base + (wave * S::kLA + i) * 1024), 16,
+    if (i < S::kLA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(bw, in ? wbytes : 0),
+                                               (lds_ptr)(base + (wave * S::kLA + i) * 1024), 16,
                                                va[i] + s * (PACKED ? 1024 : 64), 0, 0, ONCE ? 2 : 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(bx, in ? xbytes : 0),
+                                               (lds_ptr)(base + S::kA + (wave * S::kLB + i - S::kLA) * 1024), 16,
+                                               vb[i - S::kLA] + s * 64, 0, 0, 0);
+  };
+  auto issue_pair = [&](int slot, int step, bool in) {
 #pragma unroll
-    for (int i = 0; i < S::kLB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr_, (lds_ptr)(base + S::kA + (wave * S::kLB + i) * 1024), 16,
-                                               vb[i] + s * 64, 0, 0, 0);
+    for (int i = 0; i < kCodes; ++i) issue(slot, step, in, i);
   };
   // The scales of a quad: thread t holds row t's 16 bytes, dword j the four blocks of step j
   // (the packed weight scales come as dword g = block g of the four steps and are transposed).
@@ -301,40 +302,50 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   const int h = lane >> 5;
   const int read0 = (lane & 31) * 128 + ((h ^ (lane & 7)) * 16);
   u32x4 a[2][CB], bx_[2][RB];
-  uint32_t sa[CB], sx[RB];
-  auto read_step = [&](int j, int s) {   // step j of the quad
+  uint32_t read_s[CB + RB], sc[CB + RB];
+  auto read_step = [&](int j, int s, int i) {   // operand i of sub-step s of step j
     const uint8_t* base = lds + (j >> 1) * S::kPair + (read0 ^ (32 * s) ^ (64 * (j & 1)));
-#pragma unroll
-    for (int i = 0; i < CB; ++i) a[s][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 4096);
-#pragma unroll
-    for (int i = 0; i < RB; ++i) bx_[s][i] = *reinterpret_cast<const u32x4*>(base + S::kA + (wr * RB + i) * 4096);
+    if (i < CB)
+      a[s][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 4096);
+    else
+      bx_[s][i - CB] = *reinterpret_cast<const u32x4*>(base + S::kA + (wr * RB + i - CB) * 4096);
   };
-  // the lane's rows' scales of step j of the quad, shifted so that block h of the step is
-  // byte 0 and block 2 + h byte 2 (the MFMA selects a byte)
-  auto read_scales = [&](int area, int j) {
+  // the lane's rows' scales of step j of the quad; shifted before their use so that block h of
+  // the step is byte 0 and block 2 + h byte 2 (the MFMA selects a byte)
+  auto read_scale = [&](int area, int j, int i) {
     const uint8_t* base = lds + S::kScales + area * S::kQuad + 16 * (lane & 31) + 4 * j;
-#pragma unroll
-    for (int i = 0; i < CB; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(base + (wc * CB + i) * 512) >> (8 * h);
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-      sx[i] = *reinterpret_cast<const uint32_t*>(base + S::kSA + (wr * RB + i) * 512) >> (8 * h);
+    read_s[i] = *reinterpret_cast<const uint32_t*>(i < CB ? base + (wc * CB + i) * 512 : base + S::kSA + (wr * RB + i - CB) * 512);
   };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < CB + RB; ++i) sc[i] = read_s[i] >> (8 * h);
+  };
+  // Sub-step SUB of step J; behind MFMA m `between(m)`, in the order written (left to itself the
+  // compiler moves the LDS reads to just before their use and the loads into one clump).
   v16f acc[CB][RB];
-  auto multiply = [&]<int SUB>(std::integral_constant<int, SUB>) {
+  constexpr int M = CB * RB;
+  auto multiply = [&]<int SUB>(std::integral_constant<int, SUB>, auto between) {
 #pragma unroll
-    for (int j = 0; j < RB; ++j)
+    for (int m = 0; m < M; ++m) {
+      const int i = m % CB, j = m / CB;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          join_operand(a[SUB][i], u32x4{}), join_operand(bx_[SUB][j], u32x4{}), acc[i][j], kFmtFp4, kFmtFp4, 2 * SUB,
+          (int)sc[i], 2 * SUB, (int)sc[CB + j]);
+      between(m);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // part m of n things dealt over the M places
+  auto dealt = [](int m, int n, auto f) {
+    const int per = (n + M - 1) / M;
 #pragma unroll
-      for (int i = 0; i < CB; ++i)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            join_operand(a[SUB][i], u32x4{}), join_operand(bx_[SUB][j], u32x4{}), acc[i][j], kFmtFp4, kFmtFp4, 2 * SUB,
-            (int)sa[i], 2 * SUB, (int)sx[j]);
+    for (int i = m * per; i < (m + 1) * per; ++i)
+      if (i < n) f(i);
   };
   constexpr std::integral_constant<int, 0> k0{};
   constexpr std::integral_constant<int, 1> k1{};
   constexpr std::integral_constant<int, 2> k2{};
   constexpr std::integral_constant<int, 3> k3{};
-
-  constexpr int kCodes = S::kLA + S::kLB, kScaleLoads = PACKED ? 5 : 2;   // loads of a pair, of a quad's scales
 
   fill(0);
   Item cur = item(0);
@@ -343,27 +354,29 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   issue_pair(0, 0, true);
   issue_pair(1, 2, 2 < ks);
   store_scales(0, 0);
-  slot_barrier<kCodes>();
-  read_scales(0, 0);
-  read_step(0, 0);
+  slot_barrier();
+  for (int i = 0; i < CB + RB; ++i) read_scale(0, 0, i);
+  for (int i = 0; i < CB + RB; ++i) read_step(0, 0, i);
 
   int area = 0;
-  // Steps 4 q .. 4 q + 3 of the current item; behind them the loads of quad nq of the item
-  // aimed at (none when !more).
+  // Steps 4 q .. 4 q + 3 of the current item, and the loads of quad nq of the item aimed at (none
+  // when !more): its scales at the start, its first pair in step 1 and its second in step 3, when
+  // all waves have read the ones before them there. A pair has landed where the next one is
+  // issued, so there is nothing newer to wait past; that is also where the scales are taken from
+  // their registers (the compiler makes that wait for every direct-to-LDS load in flight).
   auto quad = [&](int nq, bool more) {
+    load_scales(nq);
     auto step = [&]<int J>(std::integral_constant<int, J>) {
-      read_step(J, 1);
-      if constexpr (J == 3) store_scales(area ^ 1, nq);
-      multiply(k0);
-      // Step J + 1 has landed. Newer loads: behind the first pair the second; behind the second
-      // one the next quad's scales (from step 1 on) and its first pair (from step 2 on), behind
-      // which nothing has been issued at step 3.
-      slot_barrier<J == 0 ? kCodes : J == 1 ? kScaleLoads : J == 2 ? kScaleLoads + kCodes : 0>();
-      if constexpr (J == 0) load_scales(nq);
-      if constexpr (J == 1 || J == 3) issue_pair(J >> 1, 4 * nq + J - 1, more && 4 * nq + J - 1 < ks);
-      read_step((J + 1) & 3, 0);
-      multiply(k1);
-      read_scales(J == 3 ? area ^ 1 : area, (J + 1) & 3);
+      take_scales();
+      multiply(k0, [&](int m) { dealt(m, CB + RB, [&](int i) { read_step(J, 1, i); }); });
+      if constexpr (J == 1 || J == 3) slot_barrier();
+      if constexpr (J == 1) store_scales(area ^ 1, nq);
+      multiply(k1, [&](int m) {
+        dealt(m, CB + RB, [&](int i) { read_step((J + 1) & 3, 0, i); });
+        dealt(m, CB + RB, [&](int i) { read_scale(J == 3 ? area ^ 1 : area, (J + 1) & 3, i); });
+        if constexpr (J == 1 || J == 3)
+          dealt(m, kCodes, [&](int i) { issue(J >> 1, 4 * nq + J - 1, more && 4 * nq + J - 1 < ks, i); });
+      });
     };
     step(k0);
     step(k1);
