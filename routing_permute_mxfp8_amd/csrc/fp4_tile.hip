@@ -20,8 +20,8 @@
 // multiplied. The E8M0 scales of four steps (a quad) come through registers, 16 bytes a row.
 //
 // An LDS row of a pair holds eight 16-byte chunks (32 K elements each); chunk c of row r sits
-// at place c ^ (r % 8), so that the eight lanes of a read pass (eight rows, one chunk) touch
-// all banks once. The direct-to-LDS loads write linearly; their lanes fetch the chunk that
+// at place c ^ (r / 2 % 8), so that the sixteen lanes of a read pass (sixteen rows, one chunk)
+// touch all 64 banks once (by r % 8 they met in pairs: half of the LDS's time). The direct-to-LDS loads write linearly; their lanes fetch the chunk that
 // belongs at their place, wherever the weight format has it.
 
 #include <algorithm>
@@ -161,6 +161,16 @@ __device__ __forceinline__ int4 describe(const TileArgs& p, const int* ends, int
   return make_int4(g, row0, min(MT, hi - row0), cb);
 }
 
+// Lanes 16 - 31 and 48 - 63 of a change places with lanes 0 - 15 and 32 - 47 of b.
+__device__ __forceinline__ void swap_rows(u32x4& a, u32x4& b) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const auto s = __builtin_amdgcn_permlane16_swap(a[c], b[c], false, false);
+    a[c] = s[0];
+    b[c] = s[1];
+  }
+}
+
 // The body gets the LDS area twice, as two restrict pointers: one for the direct-to-LDS
 // loads, one for every other access. The compiler then does not make each LDS read wait for
 // every direct-to-LDS load in flight; slot_barrier orders them.
@@ -195,30 +205,36 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   };
 
   // code loads: load i of a wave fills 8 rows, lane l place l % 8 of row l / 8
-  const int row_l = lane >> 3, chunk_l = (lane & 7) ^ row_l;
+  const auto chunk_of = [&](int row) { return (lane & 7) ^ ((row >> 1) & 7); };
   int va[S::kLA], vb[S::kLB];
 #pragma unroll
   for (int i = 0; i < S::kLA; ++i) {
-    const int row = (wave * S::kLA + i) * 8 + row_l;
-    va[i] = PACKED ? (row >> 4) * 16 * half + (chunk_l >> 2) * 1024 + (chunk_l & 3) * 256 + (row & 15) * 16
-                   : row * half + chunk_l * 16;
+    const int row = (wave * S::kLA + i) * 8 + (lane >> 3), c = chunk_of(row);
+    va[i] = PACKED ? (row >> 4) * 16 * half + (c >> 2) * 1024 + (c & 3) * 256 + (row & 15) * 16 : row * half + c * 16;
   }
 #pragma unroll
-  for (int i = 0; i < S::kLB; ++i) vb[i] = ((wave * S::kLB + i) * 8 + row_l) * half + chunk_l * 16;
+  for (int i = 0; i < S::kLB; ++i) {
+    const int row = (wave * S::kLB + i) * 8 + (lane >> 3);
+    vb[i] = row * half + chunk_of(row) * 16;
+  }
 
-  // The item whose loads are being issued: buffers of exactly its rows (what lies behind
+  // The item whose codes are being loaded: buffers of exactly its rows (what lies behind
   // reads as zeros, without memory traffic).
-  const uint8_t *bw, *bx, *bws, *bxs;
+  const uint8_t *bw, *bx;
   int wbytes, xbytes;
-  uint32_t vsa, vsb;
-  auto aim = [&](const Item& it) {
+  auto aim_codes = [&](const Item& it) {
     const int c16 = min(kNT / 16, n16 - it.cb * (kNT / 16));
-    const int64_t wt = (int64_t)it.group * n16 + it.cb * (kNT / 16);   // 16-channel tile of the item
-    bw = p.w + wt * 16 * half;
+    bw = p.w + ((int64_t)it.group * n16 + it.cb * (kNT / 16)) * 16 * half;
     wbytes = c16 * 16 * half;
     bx = p.x + (int64_t)it.row0 * half;
     xbytes = it.rows * half;
-    bws = p.ws + wt * (PACKED ? kq * 256 : 64 * ks);
+  };
+  // The item whose scales are being loaded; a row past its end repeats its last row.
+  const uint8_t *bws, *bxs;
+  uint32_t vsa, vsb;
+  auto aim_scales = [&](const Item& it) {
+    const int c16 = min(kNT / 16, n16 - it.cb * (kNT / 16));
+    bws = p.ws + ((int64_t)it.group * n16 + it.cb * (kNT / 16)) * (PACKED ? kq * 256 : 64 * ks);
     bxs = p.xs + (int64_t)it.row0 * (4 * ks);
     const int ra = min(tid, c16 * 16 - 1), rb = min(tid, it.rows - 1);
     vsa = PACKED ? (uint32_t)((ra >> 4) * kq * 256 + (ra & 15) * 4) : (uint32_t)(ra * 4 * ks);
@@ -293,14 +309,17 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
       a[j] = 4 * q + j < ks ? a[j] : 0;
       x[j] = 4 * q + j < ks ? x[j] : 0;
     }
-    uint8_t* base = lds + S::kScales + area * S::kQuad + 16 * tid;
-    if (kNT == kThreads || tid < kNT) *reinterpret_cast<u32x4*>(base) = a;
-    if (MT == kThreads || tid < MT) *reinterpret_cast<u32x4*>(base + S::kSA) = x;
+    uint32_t* base = reinterpret_cast<uint32_t*>(lds + S::kScales + area * S::kQuad) + tid;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // [step][row]
+      if (kNT == kThreads || tid < kNT) base[j * kNT] = a[j];
+      if (MT == kThreads || tid < MT) base[4 * kNT + j * MT] = x[j];
+    }
   };
 
   // operand reads of a wave: sub-step s of a step (64 elements), lane (h, r) = row r, chunk 2 s + h
   const int h = lane >> 5;
-  const int read0 = (lane & 31) * 128 + ((h ^ (lane & 7)) * 16);
+  const int read0 = (lane & 31) * 128 + ((h ^ ((lane >> 1) & 7)) * 16);
   u32x4 a[2][CB], bx_[2][RB];
   uint32_t read_s[CB + RB], sc[CB + RB];
   auto read_step = [&](int j, int s, int i) {   // operand i of sub-step s of step j
@@ -313,8 +332,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   // the lane's rows' scales of step j of the quad; shifted before their use so that block h of
   // the step is byte 0 and block 2 + h byte 2 (the MFMA selects a byte)
   auto read_scale = [&](int area, int j, int i) {
-    const uint8_t* base = lds + S::kScales + area * S::kQuad + 16 * (lane & 31) + 4 * j;
-    read_s[i] = *reinterpret_cast<const uint32_t*>(i < CB ? base + (wc * CB + i) * 512 : base + S::kSA + (wr * RB + i - CB) * 512);
+    const uint32_t* base = reinterpret_cast<const uint32_t*>(lds + S::kScales + area * S::kQuad) + (lane & 31);
+    read_s[i] = base[i < CB ? j * kNT + (wc * CB + i) * 32 : 4 * kNT + j * MT + (wr * RB + i - CB) * 32];
   };
   auto take_scales = [&]() {
 #pragma unroll
@@ -335,12 +354,12 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // part m of n things dealt over the M places
-  auto dealt = [](int m, int n, auto f) {
-    const int per = (n + M - 1) / M;
+  // part m of things lo .. hi - 1 dealt over the M places
+  auto dealt = [](int m, int lo, int hi, auto f) {
+    const int per = (hi - lo + M - 1) / M;
 #pragma unroll
-    for (int i = m * per; i < (m + 1) * per; ++i)
-      if (i < n) f(i);
+    for (int i = lo + m * per; i < lo + (m + 1) * per; ++i)
+      if (i < hi) f(i);
   };
   constexpr std::integral_constant<int, 0> k0{};
   constexpr std::integral_constant<int, 1> k1{};
@@ -349,7 +368,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
 
   fill(0);
   Item cur = item(0);
-  aim(cur);
+  aim_codes(cur);
+  aim_scales(cur);
   load_scales(0);
   issue_pair(0, 0, true);
   issue_pair(1, 2, 2 < ks);
@@ -359,24 +379,49 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   for (int i = 0; i < CB + RB; ++i) read_step(0, 0, i);
 
   int area = 0;
-  // Steps 4 q .. 4 q + 3 of the current item, and the loads of quad nq of the item aimed at (none
-  // when !more): its scales at the start, its first pair in step 1 and its second in step 3, when
-  // all waves have read the ones before them there. A pair has landed where the next one is
-  // issued, so there is nothing newer to wait past; that is also where the scales are taken from
-  // their registers (the compiler makes that wait for every direct-to-LDS load in flight).
-  auto quad = [&](int nq, bool more) {
-    load_scales(nq);
+  // Steps 4 q .. 4 q + 3 of the current item, and the loads of quad nq: the next one, or the
+  // first of item `next` (last; none when !more). Its scales are loaded at the start, its first
+  // pair from step 1 on and its second from step 3 on, when all waves have read the ones before
+  // them there. A pair has landed where the next one's loads begin, so there is nothing newer to
+  // wait past; that is also where the scales are taken from their registers (the compiler makes
+  // that wait for every direct-to-LDS load in flight).
+  // Many MFMAs a step: a burst of a pair's loads meets the L2's rate and stalls the waves (about
+  // 1000 cycles), so half of them go on in the next half step; of the second pair that is the
+  // next quad's first (pending), but for an item's last quad.
+  constexpr int kFirst = M >= 8 ? kCodes / 2 : kCodes;
+  auto quad = [&](int q, bool last, bool more, const Item& next) {
+    const int nq = last ? 0 : q + 1;
+    const bool pending = q > 0;
+    if constexpr (kFirst == kCodes) load_scales(nq);
+    const auto reads = [&](int j, int m) { dealt(m, 0, CB + RB, [&](int i) { read_step(j, 1, i); }); };
     auto step = [&]<int J>(std::integral_constant<int, J>) {
       take_scales();
-      multiply(k0, [&](int m) { dealt(m, CB + RB, [&](int i) { read_step(J, 1, i); }); });
+      if (J == 0 && kFirst < kCodes && pending)
+        multiply(k0, [&](int m) {
+          reads(J, m);
+          dealt(m, kFirst, kCodes, [&](int i) { issue(1, 4 * q + 2, 4 * q + 2 < ks, i); });
+        });
+      else
+        multiply(k0, [&](int m) {
+          reads(J, m);
+          if constexpr (J == 2)
+            dealt(m, kFirst, kCodes, [&](int i) { issue(0, 4 * nq, more, i); });
+        });
+      if constexpr (J == 0)
+        if (last) aim_codes(next);
+      if constexpr (J == 0 && kFirst < kCodes) load_scales(nq);
       if constexpr (J == 1 || J == 3) slot_barrier();
-      if constexpr (J == 1) store_scales(area ^ 1, nq);
       multiply(k1, [&](int m) {
-        dealt(m, CB + RB, [&](int i) { read_step((J + 1) & 3, 0, i); });
-        dealt(m, CB + RB, [&](int i) { read_scale(J == 3 ? area ^ 1 : area, (J + 1) & 3, i); });
-        if constexpr (J == 1 || J == 3)
-          dealt(m, kCodes, [&](int i) { issue(J >> 1, 4 * nq + J - 1, more && 4 * nq + J - 1 < ks, i); });
+        if (J == 1 && m == M / 2) store_scales(area ^ 1, nq);
+        dealt(m, 0, CB + RB, [&](int i) { read_step((J + 1) & 3, 0, i); });
+        dealt(m, 0, CB + RB, [&](int i) { read_scale(J == 3 ? area ^ 1 : area, (J + 1) & 3, i); });
+        if constexpr (J == 1) dealt(m, 0, kFirst, [&](int i) { issue(0, 4 * nq, more, i); });
+        if constexpr (J == 3) dealt(m, 0, kFirst, [&](int i) { issue(1, 4 * nq + 2, more && 4 * nq + 2 < ks, i); });
       });
+      if constexpr (J == 3 && kFirst < kCodes)
+        if (last)
+#pragma unroll
+          for (int i = kFirst; i < kCodes; ++i) issue(1, 4 * nq + 2, more && 4 * nq + 2 < ks, i);
     };
     step(k0);
     step(k1);
@@ -393,25 +438,53 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     pin(acc);
-    for (int q = 1; q < kq; ++q) quad(q, true);
+    for (int q = 0; q < kq - 1; ++q) quad(q, false, true, cur);
     // the item's last quad: the next item's first is loaded behind it
     const bool more = n + 1 < count;
     if (more && (n + 1) % kList == 0) fill(n + 1);
     const Item next = more ? item(n + 1) : cur;
-    aim(next);
-    quad(0, more);
-    // lane (h, r) holds row r, channels 8 e + 4 h + 0..3
+    aim_scales(next);
+    quad(kq - 1, true, more, next);
+    // Lane (h, r) holds row r, channels 8 e + 4 h + 0..3 of a block: pieces of 8 (bf16) or 16
+    // bytes, each a write request of its own to the L2 (8192 a 256 x 256 tile: 18,000 cycles).
+    // Lane halves and quarters change places until a row's 64 bytes are next to one another, in
+    // lanes l, l + 16, l + 32, l + 48.
 #pragma unroll
     for (int j = 0; j < RB; ++j) {
-      const int r = (wr * RB + j) * 32 + (lane & 31);
 #pragma unroll
       for (int i = 0; i < CB; ++i) {
-        const int c0 = cur.cb * kNT + (wc * CB + i) * 32 + 4 * h;
+        const int row = (wr * RB + j) * 32 + (lane & 15), ch = cur.cb * kNT + (wc * CB + i) * 32;
+        if constexpr (sizeof(O) == 2) {
+          u32x4 v[2];   // lane (h, r): channels 16 e + 8 h + 0..7
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r < cur.rows && c0 + 8 * e < p.N)
-            store4(out + (int64_t)(cur.row0 + r) * p.N + c0 + 8 * e,
-                   v4f{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]});
+          for (int e = 0; e < 2; ++e) {
+            const auto at = [&](int c) { return bf16x2(acc[i][j][8 * e + c], acc[i][j][8 * e + c + 1]); };
+            const auto s0 = __builtin_amdgcn_permlane32_swap(at(0), at(4), false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(at(2), at(6), false, false);
+            v[e] = u32x4{s0[0], s1[0], s0[1], s1[1]};
+          }
+          swap_rows(v[0], v[1]);
+          const int c = ch + 16 * ((lane >> 4) & 1) + 8 * h;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (row + 16 * e < cur.rows && c < p.N)
+              *reinterpret_cast<u32x4*>(out + (int64_t)(cur.row0 + row + 16 * e) * p.N + c) = v[e];
+        } else {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            u32x4 v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) v[e][c] = __float_as_uint(acc[i][j][8 * g + 4 * e + c]);
+            swap_rows(v[0], v[1]);
+            const int c = ch + 16 * g + 8 * ((lane >> 4) & 1) + 4 * h;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (row + 16 * e < cur.rows && c < p.N)
+                *reinterpret_cast<u32x4*>(out + (int64_t)(cur.row0 + row + 16 * e) * p.N + c) = v[e];
+          }
+        }
       }
     }
     if (++n >= count) break;
