@@ -14,6 +14,7 @@ inputs may be uint8 or the matching float8 dtype.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -542,6 +543,14 @@ def _device_of(first, **others):
     return first.device.index
 
 
+@functools.lru_cache(maxsize=4096)
+def _sized(query: str, *sizes) -> int:
+    """A workspace size, which depends on the sizes alone."""
+    nbytes = ctypes.c_size_t()
+    _check(getattr(load(), query)(*sizes, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
 def _raw(t):
     return None if t is None else t.data_ptr()
 
@@ -615,13 +624,12 @@ def balance_loss(logits, topk_ids, *, scoring: int = GATE_SOFTMAX, seq_offsets=N
     seqs = _gate_seqs(n, seq_offsets, row_mask)
     index = _device_of(logits, topk_ids=topk_ids, seq_offsets=seq_offsets, row_mask=row_mask)
     dev = logits.device
-    nbytes = ctypes.c_size_t()
-    _check(lib.moe_balance_loss_workspace_size(n, e, seqs, ctypes.byref(nbytes)))
+    nbytes = _sized("moe_balance_loss_workspace_size", n, e, seqs)
     with _on(index):
         loss = torch.empty((1,), dtype=torch.float32, device=dev)
         counts = torch.empty((seqs, e), dtype=torch.int32, device=dev)
         coef = torch.empty((seqs, e), dtype=torch.float32, device=dev)
-        ws = _workspace(nbytes.value, dev)
+        ws = _workspace(nbytes, dev)
         _check(lib.moe_balance_loss(logits.data_ptr(), _DT[logits.dtype], n, e, topk_ids.data_ptr(), topk_ids.shape[1],
                                     scoring, _raw(seq_offsets), seqs, _raw(row_mask), alpha, loss.data_ptr(),
                                     counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(index)))
@@ -703,14 +711,13 @@ def mxfp4_matmul(x, w, w_scales, *, x_scales=None, group_offsets=None, out_dtype
     index = _device_of(x, w=w, w_scales=w_scales, x_scales=x_scales, group_offsets=group_offsets, out=out,
                        workspace=workspace)
     xd = DTYPE_FP4_E2M1 if x_scales is not None else _DT[x.dtype]
-    nbytes = ctypes.c_size_t()
-    _check(lib.moe_mxfp4_matmul_workspace_size(rows, g, n, k, xd, weight_format, ctypes.byref(nbytes)))
+    nbytes = _sized("moe_mxfp4_matmul_workspace_size", rows, g, n, k, xd, weight_format)
     with _on(index):
         if out is None:
             out = torch.empty((rows, n), dtype=out_dtype, device=x.device)
         ws = workspace
-        if nbytes.value and (ws is None or ws.numel() < nbytes.value):
-            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=x.device)
+        if nbytes and (ws is None or ws.numel() < nbytes):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
         _check(lib.moe_mxfp4_matmul(x.data_ptr(), xd, _raw(x_scales), rows, _raw(group_offsets), g, w.data_ptr(),
                                     w_scales.data_ptr(), n, k, weight_format, out.data_ptr(), _DT[out.dtype], _raw(ws),
                                     0 if ws is None else ws.numel(), _raw_stream(index)))

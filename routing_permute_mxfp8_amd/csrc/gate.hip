@@ -349,8 +349,9 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __res
 // neighbours (not of fp16 or bf16 logits without a bias, which the 24 bits hold exactly): the
 // eight and the ninth order themselves by their whole ranks, and where those are within
 // their errors by ranks in 64 bits. What stays open, a tenth that near to the K-th or two
-// groups that near at the border (about one row of a thousand), is decided row by row by
-// the whole wave: deciding every near row so took 20 of 34 us at 32768 x 256 in groups.
+// groups that near at the border (a few rows of ten thousand), is decided row by row by
+// the whole wave: deciding every near row so took 20 of 34 us at 32768 x 256 in groups, a row of
+// a thousand still 9 of 25 (a wave's 8 us at the end of the launch); it is 22 now.
 constexpr int kTop = 8;
 
 __device__ __forceinline__ uint32_t order_key(float r, int e) {
@@ -458,7 +459,7 @@ __device__ __forceinline__ void clean_part(const T (&raw)[V], int E, int sub, fl
 // Where the order of a lane's experts does not matter they are dealt in 16-byte pieces (W
 // values), so that a wave's loads and stores run along the rows: value v of lane `sub` is
 // expert dealt<W>(sub, v). (The gradient of 32768 x 256 fp32 rows with 64 contiguous bytes a
-// lane: 21 us, dealt: see gate16_backward_kernel.)
+// lane: 21 us, dealt: 16.)
 template <typename T, int V> constexpr int kPiece = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
 template <int W>
 __device__ __forceinline__ int dealt(int sub, int v) { return v / W * 16 * W + sub * W + v % W; }
@@ -529,6 +530,11 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
   RowNorm<float> norm{0.0f, 0.0f};
   if constexpr (SOFTMAX) norm = row_norm<float, V>(x);
   const float top = SOFTMAX ? norm.inv : 1.0f;
+  // What two scores can be off together, relative to the largest, with some room. A sigmoid: t = exp(-l)
+  // is off by (1.5 |l| + 2) 2^-24 of itself, which s (1 - s) <= 1/4 and s (1 - s) |l| < 0.23 make
+  // less than 2^-24, 1 + t by another, the reciprocal by 2^-23: 2^-22. A softmax: its sum's
+  // roundings and the exponents' errors, weighted by at most ln E, come to less than 2^-18.6.
+  constexpr float kScoreError = SOFTMAX ? 0x1p-17f : 0x1p-20f;
   float r[V];
   bool redo = false;   // decided by the whole wave
   bool stays = true;
@@ -556,7 +562,8 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
     if (p.lanes > 2) merge_two(a, b, dppf<kX2>(a), dppf<kX2>(b));
     if (p.lanes > 4) merge_two(a, b, dppf<kX4>(a), dppf<kX4>(b));
     const float score = a + (b == -INFINITY ? 0.0f : b);
-    const float tau = 4 * (top * 0x1p-18f + row_max(big) * 0x1p-21f);
+    // two sums of two ranks each: four scores' errors, and 8 roundings of at most `big` 2^-24
+    const float tau = 2 * kScoreError * top + row_max(big) * 0x1p-20f;
     const int shift = __builtin_ctz(p.lanes), g = sub >> shift;
     int better = 0;
     auto against = [&]<int L>(std::integral_constant<int, L>) {
@@ -625,7 +632,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
   const float s = l == -INFINITY ? 0.0f : score_of<float, SOFTMAX>(l, norm);
   int at = sub;   // its place in the row
   if constexpr (kCut) {
-    const float tau = BIAS ? top * 0x1p-18f : 0.0f;
+    const float tau = BIAS ? kScoreError * top : 0.0f;
     // what is no candidate has to be clear of the K-th choice
     uint32_t kth = best[0];
 #pragma unroll
@@ -921,15 +928,22 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
         p += lds_p[a][lane];
         c += lds_c[a][lane];
       }
-      counts[(int64_t)b * E + e] = c;
-      coef[(int64_t)b * E + e] = (float)(f * c);
       total = f * c * p;
     }
-    total = wave_sum(total);
+    const double share = wave_sum(total);
     if (lane == 0) {
-      shares[(int64_t)b * gridDim.x + blockIdx.x] = total;
-      __threadfence();
-      last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
+      if (gridDim.x * gridDim.y == 1) {
+        *loss = (float)share;
+        last = false;
+      } else {   // (before the other stores: the fence would wait for them)
+        shares[(int64_t)b * gridDim.x + blockIdx.x] = share;
+        __threadfence();
+        last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
+      }
+    }
+    if (e < E) {
+      counts[(int64_t)b * E + e] = c;
+      coef[(int64_t)b * E + e] = (float)(f * c);
     }
   }
   __syncthreads();
@@ -1279,7 +1293,7 @@ hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
 // of at least 16 rows on average.
 int balance_splits(int64_t rows, int64_t seqs) {
   const int64_t per = std::max<int64_t>(1, rows / std::max<int64_t>(seqs, 1));
-  return (int)std::max<int64_t>(1, std::min<int64_t>((512 + seqs - 1) / seqs, (per + 15) / 16));
+  return (int)std::max<int64_t>(1, std::min<int64_t>((1024 + seqs - 1) / seqs, (per + 15) / 16));
 }
 
 int balance_chunks(int experts) { return (experts + kFinishExperts - 1) / kFinishExperts; }
