@@ -187,6 +187,7 @@ hipError_t launch_out(const Fp4MatmulParams& p, hipStream_t stream) {
 // 160 rows: 592, 478 cached).
 int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool values) {
   if (rows <= 0) return 0;
+  if (rows * (k / 32) < 16) return 0;   // (it reads x's scales 16 bytes at a time, also at their end)
   constexpr int64_t kStart = 9 << 20;   // bytes the kernel above reads in 3 us
   const int64_t per = (rows + groups - 1) / groups;
   const double bytes = (double)((per + 15) / 16) * (double)(std::min(groups, rows) * n) * (double)(k / 2);

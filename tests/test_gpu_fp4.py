@@ -289,3 +289,23 @@ def test_tiles_of_every_size(groups, per, n, k):
         torch.cuda.synchronize()
         check(got, xv, wv, off, out_dtype)
         assert bool((got[:off[0]] == 7).all()) and bool((got[off[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("rows", [1, 3, 4, 5])
+@pytest.mark.parametrize("values", [False, True])
+def test_few_scales_of_a_wide_product(rows, values):
+    """One K step and so many channels that the size alone asks for tiles: x has 4 to 20 bytes of
+    scales in all, in a tensor of just that size behind others."""
+    n, k = 340_016, 128
+    wc, ws, wv = drawn(1, n, k, seed=rows)
+    rng = np.random.default_rng(rows)
+    x = rng.standard_normal((rows, k))
+    t = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)
+    xc, xs, xv = fp4(t.double().numpy())
+    for packed in (False, True):
+        say(f"mxfp4_matmul wide rows={rows} n={n} k={k} values={values} packed={packed}")
+        w, s = rp.pack_weights(to_dev(wc), to_dev(ws), fp4=True) if packed else (to_dev(wc), to_dev(ws))
+        got = rp.mxfp4_matmul(t.to(DEV) if values else to_dev(xc), w, s, x_scales=None if values else to_dev(xs),
+                              out_dtype=torch.float32, weight_format=rp.WEIGHTS_PACKED if packed else rp.WEIGHTS_ND)
+        torch.cuda.synchronize()
+        check(got, xv, wv, [0, rows], torch.float32)
