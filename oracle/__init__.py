@@ -16,6 +16,9 @@ with it. The oracle is written from the operator pages:
   scatter, histogram, quantized gather, availableIdxNum) and 参数说明
   (active expert range, rowIdxType, expertTokensNumType).
 
+The router (gate.py: top-K gate, load-balance loss, their gradient) is on none of
+these pages; it is written from the formulas in its docstrings. Parity unpinned.
+
 Floating point is float64 throughout unless a step fixes another precision;
 where a reading of the pages had to be chosen it is named in the function's
 docstring. Every function has pins in tests/test_oracle_*.py (worked examples,

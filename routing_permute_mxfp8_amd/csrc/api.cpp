@@ -463,7 +463,7 @@ moe::BalanceParams carve_balance(Carver& cv, int64_t rows, int64_t experts, int6
   p.sums = cv.take<float>(parts * experts);
   p.part_counts = cv.take<int32_t>(parts * experts);
   p.held = cv.take<int32_t>(parts);
-  p.shares = cv.take<double>((size_t)seqs * moe::balance_chunks((int)experts));
+  p.shares = cv.take<double>((size_t)seqs * moe::balance_chunks((int)experts, p.splits));
   p.done = cv.take<unsigned>(1);
   return p;
 }

@@ -13,16 +13,25 @@
 //
 // The codes of NT weight rows and MT rows of x go straight from memory into LDS, two K steps
 // of 128 at a time: 128 bytes a row, whole cache lines (64 experts of 4096 x 7168, 4 rows
-// each, single steps: 199 us, pairs: 182). Four steps are staged; a pair is issued as soon as
-// all waves have read the one before it there, and operands are read from LDS half a step
-// ahead of their MFMAs; one barrier a step, between its two halves. The loads go on across
-// items, so an item's first steps are under way while the last ones of the item before are
-// multiplied. The E8M0 scales of four steps (a quad) come through registers, 16 bytes a row.
+// each, single steps: 199 us, pairs: 182). Two pairs are staged; the next one's loads begin as
+// soon as all waves have read the one before it there, and operands are read from LDS half a
+// step ahead of their MFMAs; one barrier for two steps, between the halves of the second. The
+// loads go on across items, so an item's first steps are under way while the last ones of the
+// item before are multiplied. The E8M0 scales of four steps (a quad) come through registers,
+// 16 bytes a row.
 //
 // An LDS row of a pair holds eight 16-byte chunks (32 K elements each); chunk c of row r sits
 // at place c ^ (r / 2 % 8), so that the sixteen lanes of a read pass (sixteen rows, one chunk)
-// touch all 64 banks once (by r % 8 they met in pairs: half of the LDS's time). The direct-to-LDS loads write linearly; their lanes fetch the chunk that
-// belongs at their place, wherever the weight format has it.
+// touch all 64 banks once (by r % 8 they met in pairs: half of the LDS's time). The
+// direct-to-LDS loads write linearly; their lanes fetch the chunk that belongs at their place,
+// wherever the weight format has it.
+//
+// Measured: 256 rows on 64 experts of 4096 x 7168 (1.0 GB of weights): 155 us, 6.4 TB/s of the
+// 7.1 that a read reaches here. 32768 rows on 16 of them: 530 us, 3.6 PFLOP/s; these MFMAs
+// alone reach 6.5 with random operands, with this kernel's LDS reads and loads dealt between
+// them 5.4 to 5.9, at clocks that power holds at 1.6 to 1.9 GHz; the rest is the stores at an
+// item's end (9,000 cycles of some 75,000), when a compute unit's one block multiplies nothing,
+// and bursts of loads. 8192 rows on 32 of 7168 x 2048: 120 us, a third of it those stores.
 
 #include <algorithm>
 #include <map>
@@ -40,6 +49,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 
 // ---- x given as values: its codes and scales ----------------------------------------------
 // One thread per group of 32; row-major codes [rows, K/2] and scales [rows, K/32].
+// Bound by the stream: 8192 x 2048 bf16 (42 MB) in 8.8 us, 4.8 TB/s.
 template <typename X>
 __global__ __launch_bounds__(256) void fp4_quantise_kernel(const X* __restrict__ x, int64_t groups,
                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {

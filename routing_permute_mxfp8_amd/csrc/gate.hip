@@ -20,6 +20,14 @@
 //
 // One wave per row, lane l holding the V experts [l V, l V + V) (V = 1 .. 16 for up to
 // 1024 experts): the row's reductions are DPP steps in one wave, without LDS or barriers.
+// Up to 256 experts (the gate: and 8 choices, groups of a power of two of lanes) a row takes 16
+// lanes instead, four rows a wave (see there): more of a row's values in one lane, fewer
+// exchanges. Kernel times, one wave per row and 16 lanes, E = 256:
+//   gate 8192 fp32 softmax 10.3, 5.7 us; 32768 bf16 sigmoid in 8 groups 55, 19;
+//   loss 32768 fp32, first pass 60, 13.6 (34 MB); gradient 32768 fp32 23.3, 15.5 (70 MB, 4.5 TB/s).
+// One wave per row at 8192 x 512 fp32: gate 21, in groups 43, loss's first pass 8, gradient 19.
+// Bound: small calls by the launch, the gate by its instructions, the other two by the stream
+// and the latency of few rows a wave.
 
 #include <algorithm>
 #include <cfloat>
@@ -866,7 +874,13 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
   }
 }
 
-constexpr int kFinishThreads = 512, kFinishExperts = 64;   // a block: 64 experts, 8 slices of the partials
+constexpr int kFinishThreads = 512;
+// Experts of a block of the second pass: 16 of many partials, because one compute unit takes no
+// more than about 20 GB/s of them from memory (512 partials of 256 experts: 13.4 us on 4 blocks,
+// 8.7 on 16; 1024 of 512: 21.8, 10.3), else 64, where fewer blocks make the join of the loss
+// cheaper (8 sequences of 128 partials: both passes 21.5 us, with 16 23.4; 63 partials of 60
+// experts, one block: 7.9, 4 blocks 10.3).
+constexpr int finish_experts(int splits) { return splits > 256 ? 16 : 64; }
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
   v = wave_sum(v);
@@ -878,25 +892,26 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return t;
 }
 
-// Second pass: block (c, b) joins the partials of 64 experts of sequence b; the last block
+// Second pass: block (c, b) joins the partials of W experts of sequence b; the last block
 // to end adds the blocks' shares of the loss, in order.
+template <int W>
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     int E, int k, int splits, int seqs, int lanes, const float* __restrict__ sums, const int32_t* __restrict__ counts_part,
     const int32_t* __restrict__ held, float alpha, double* __restrict__ shares, unsigned* __restrict__ done,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ coef) {
-  constexpr int kSlices = kFinishThreads / kFinishExperts;
-  __shared__ double lds_p[kSlices][kFinishExperts];
-  __shared__ int lds_c[kSlices][kFinishExperts];
+  constexpr int kSlices = kFinishThreads / W, kAhead = W == 16 ? 8 : 4;   // (partials in flight a thread)
+  __shared__ double lds_p[kSlices][W];
+  __shared__ int lds_c[kSlices][W];
   __shared__ double lds_w[kFinishThreads / 64];
   __shared__ int lds_rows, lds_filled;
-  const int b = blockIdx.y, lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int b = blockIdx.y, lane = threadIdx.x & 63, slice = threadIdx.x / W, of = threadIdx.x % W;
   if (threadIdx.x == 0) lds_rows = lds_filled = 0;
   // this block's partials first: their loads are under way while the rows are counted
-  const int e = blockIdx.x * kFinishExperts + lane;
+  const int e = blockIdx.x * W + of;
   double p = 0;
   int c = 0;
   if (e < E)
-#pragma unroll 4
+#pragma unroll kAhead
     for (int s = slice; s < splits; s += kSlices) {
       p += sums[((int64_t)b * splits + s) * E + e];
       c += counts_part[((int64_t)b * splits + s) * E + e];
@@ -908,6 +923,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     const int q = q0 + threadIdx.x / lanes;
     int t = 0;
     if (q < seqs)
+#pragma unroll 8
       for (int s = threadIdx.x % lanes; s < splits; s += lanes) t += held[(int64_t)q * splits + s];
     for (int d = 1; d < lanes; d *= 2) t += __shfl_xor(t, d, 64);
     const bool first = threadIdx.x % lanes == 0 && q < seqs;
@@ -915,18 +931,19 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     if (first && q == b) lds_rows = t;
   }
   if (lane == 0) atomicAdd(&lds_filled, filled);
-  lds_p[slice][lane] = p;
-  lds_c[slice][lane] = c;
+  lds_p[slice][of] = p;
+  lds_c[slice][of] = c;
   __syncthreads();
   __shared__ bool last;
-  if (slice == 0) {
+  if (threadIdx.x < 64) {
     const double rows = lds_rows;
     const double f = rows > 0 ? (double)alpha * E / ((double)k * rows * rows * lds_filled) : 0.0;
     double total = 0;
-    if (e < E) {
+    const bool mine = slice == 0 && e < E;
+    if (mine) {
       for (int a = 1; a < kSlices; ++a) {
-        p += lds_p[a][lane];
-        c += lds_c[a][lane];
+        p += lds_p[a][of];
+        c += lds_c[a][of];
       }
       total = f * c * p;
     }
@@ -941,7 +958,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
         last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
       }
     }
-    if (e < E) {
+    if (mine) {
       counts[(int64_t)b * E + e] = c;
       coef[(int64_t)b * E + e] = (float)(f * c);
     }
@@ -1296,7 +1313,7 @@ int balance_splits(int64_t rows, int64_t seqs) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((1024 + seqs - 1) / seqs, (per + 15) / 16));
 }
 
-int balance_chunks(int experts) { return (experts + kFinishExperts - 1) / kFinishExperts; }
+int balance_chunks(int experts, int splits) { return (experts + finish_experts(splits) - 1) / finish_experts(splits); }
 
 hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
   const dim3 grid((unsigned)p.splits, (unsigned)p.seqs);
@@ -1323,9 +1340,15 @@ hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
   if (e != hipSuccess) return e;
   int lanes = 1;   // a sequence's lanes where its partials are counted
   while (lanes < 64 && lanes < p.splits) lanes *= 2;
-  balance_finish_kernel<<<dim3((unsigned)balance_chunks(p.experts), (unsigned)p.seqs), kFinishThreads, 0, stream>>>(
-      p.experts, p.k, p.splits, p.seqs, lanes, p.sums, p.part_counts, p.held, p.alpha, p.shares, p.done, p.loss, p.counts,
-      p.coef);
+  auto finish = [&](auto kernel) {
+    kernel<<<dim3((unsigned)balance_chunks(p.experts, p.splits), (unsigned)p.seqs), kFinishThreads, 0, stream>>>(
+        p.experts, p.k, p.splits, p.seqs, lanes, p.sums, p.part_counts, p.held, p.alpha, p.shares, p.done, p.loss, p.counts,
+        p.coef);
+  };
+  if (finish_experts(p.splits) == 16)
+    finish(balance_finish_kernel<16>);
+  else
+    finish(balance_finish_kernel<64>);
   return hipGetLastError();
 }
 

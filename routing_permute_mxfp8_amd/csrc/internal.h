@@ -257,7 +257,7 @@ struct GateParams {
 hipError_t launch_gate(const GateParams& p, hipStream_t stream);
 
 int balance_splits(int64_t rows, int64_t seqs);
-int balance_chunks(int experts);   // blocks a sequence of the second pass
+int balance_chunks(int experts, int splits);   // blocks a sequence of the second pass
 struct BalanceParams {
   const void* logits = nullptr;
   int dtype = 0;
@@ -273,7 +273,7 @@ struct BalanceParams {
   float* sums = nullptr;           // [seqs, splits, experts]
   int32_t* part_counts = nullptr;  // [seqs, splits, experts]
   int32_t* held = nullptr;         // [seqs, splits]
-  double* shares = nullptr;        // [seqs, balance_chunks(experts)]
+  double* shares = nullptr;        // [seqs, balance_chunks(experts, splits)]
   unsigned* done = nullptr;        // [1]
   // outputs
   float* loss = nullptr;

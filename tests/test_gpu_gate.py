@@ -296,3 +296,32 @@ def test_gate_feeds_the_routing():
     _, counts, _ = rp.balance_loss(logits, ids, scoring=rp.GATE_SIGMOID)
     tokens = rp.init_routing(x, ids, e, quant_mode=rp.QUANT_MXFP4)[2]
     assert torch.equal(tokens, counts[0].long())
+
+
+@pytest.mark.parametrize("n,e,seqs", [(30000, 256, 1), (30000, 100, 2), (20000, 40, 1), (9000, 700, 1)])
+def test_balance_of_many_partials(n, e, seqs):
+    """Long sequences: hundreds of partial sums each, joined on few and on many blocks."""
+    k = 6
+    rng = np.random.default_rng(n + e)
+    x = torch.from_numpy(rng.standard_normal((n, e)).astype(np.float32))
+    ids = torch.from_numpy(np.argsort(rng.random((n, e)), axis=1)[:, :k].astype(np.int32))
+    off = None if seqs == 1 else [0, 3, n]
+    mask = rng.random(n) > 0.1
+    say(f"balance_loss {n}x{e} seqs={seqs}")
+    loss, counts, coef = rp.balance_loss(x.to(DEV), ids.to(DEV), alpha=0.5, row_mask=torch.from_numpy(mask).to(DEV),
+                                         seq_offsets=None if off is None else torch.tensor(off, dtype=torch.int32, device=DEV))
+    p = torch.softmax(x.double(), dim=1).numpy()
+    bounds = off or [0, n]
+    total, filled = 0.0, sum(bool(mask[lo:hi].any()) for lo, hi in zip(bounds[:-1], bounds[1:]))
+    for b, (lo, hi) in enumerate(zip(bounds[:-1], bounds[1:])):
+        m = mask[lo:hi]
+        rows = int(m.sum())
+        c = np.bincount(ids.numpy()[lo:hi][m].reshape(-1), minlength=e)
+        f = 0.5 * e * c / (k * rows * rows * filled)
+        assert np.array_equal(counts[b].cpu().numpy(), c)
+        # one rounding to fp32 of a float64 product of a few factors
+        assert np.all(np.abs(coef[b].cpu().double().numpy() - f) <= 2.0 ** -23 * f)
+        total += float((f * p[lo:hi][m].sum(axis=0)).sum())
+    # a score is off by at most (|l - m| + 12) 2^-23 of itself, |l - m| < 12; a wave's fp32 sums of
+    # at most 64 rows by 64 2^-24; then the rounding of the loss
+    assert abs(float(loss) - total) <= (24 * 2.0 ** -23 + 64 * 2.0 ** -24 + 2.0 ** -24) * total
