@@ -184,12 +184,13 @@ hipError_t launch_out(const Fp4MatmulParams& p, hipStream_t stream) {
 // 35.) Values are quantised by a launch of their own there, 3 us more.
 //
 // Tiles a little larger than the average group, because the sizes scatter (64 groups of 7168 x
-// 4096, microseconds with tiles of 32, 64, 128 and 256 rows, us: 16 rows each 163, 174, 207,
-// -; 24: 193, 184, 209, 275; 48: 353, 223, 227, 285; 96: 590, 413, 240, 299; 160: 938, 592,
-// 390, 342; 320: 1854, 1075, 612, 576), but smaller ones where the tiles would not occupy the
-// chip (5 groups of 155 rows, 1408 x 2000: 14.5, 12.0, 16.5, 21.5). With at most a tile of
-// rows a group the weights are read once and non-temporal (40 rows each: 201 us, 212 cached;
-// 160 rows: 592, 478 cached).
+// 4096, us with tiles of 32, 64, 128 and 256 rows: 16 rows each 172, 176, 206, 228; 24: 204, 188,
+// 215, 236; 48: 376, 219, 223, 245; 96: 641, 318, 214, 234; 112: 700, 379, 251, 236; 320: 1864,
+// 774, 539, 504), but smaller ones where the tiles would not occupy the chip (5 groups of 155
+// rows, 1408 x 2000: 14.4, 10.6, 13.6, 17.6). Where a group is at most four fifths of a tile on
+// average its weights are read about once, non-temporal (tiles of 64, 40 rows each: 201 us, 212
+// cached; of 128, 96 rows: 214, 245; of 256, 160 rows: 253, 281; but of 128, 160 rows: 414, 399,
+// and of 256, 256 rows of 2048 x 7168: 140, 136).
 int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool values) {
   if (rows <= 0) return 0;
   if (rows * (k / 32) < 16) return 0;   // (it reads x's scales 16 bytes at a time, also at their end)
@@ -198,7 +199,7 @@ int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool value
   const double bytes = (double)((per + 15) / 16) * (double)(std::min(groups, rows) * n) * (double)(k / 2);
   if (bytes < (double)(kStart * (values ? 2 : 1) + k * (kStart / 6 / 128))) return 0;
   if (per <= 20) return 32;
-  int mt = per <= 48 ? 64 : per <= 112 ? 128 : 256;
+  int mt = per <= 48 ? 64 : per <= 100 ? 128 : 256;
   const auto items = [&](int m) { return groups * ((per + m - 1) / m) * ((n + 255) / 256); };
   while (mt > 64 && items(mt) < 256) mt /= 2;
   return mt;

@@ -254,7 +254,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   // of steps the last pair's second half is whatever follows in the item's buffer, or zeros
   // behind it; its scales are made to vanish (store_scales). The step is part of the lane's
   // offset, not of the scalar one, because only that is checked against the buffer's size.
-  // ONCE: the weights are used by this item alone, so they are loaded non-temporal.
+  // ONCE: a weight is used by about one item, so weights are loaded non-temporal.
   constexpr int kCodes = S::kLA + S::kLB;   // loads of a pair
   auto issue = [&](int slot, int step, bool in, int i) {   // load i of the pair
     uint8_t* base = dma + slot * S::kPair;
@@ -543,12 +543,15 @@ hipError_t launch_tiles(const TileArgs& a, void* out, hipStream_t stream) {
 
 template <typename O, bool PACKED>
 hipError_t launch_shape(const Fp4MatmulParams& p, const TileArgs& a, hipStream_t stream) {
+  // weights of groups that mostly fit into one tile are read about once: see fp4_tile_rows
+  const bool once = 5 * p.rows <= (int64_t)4 * p.mt * p.groups;
   switch (p.mt) {
-    case 256: return launch_tiles<2, 4, 4, 1, false, O, PACKED>(a, p.out, stream);
-    case 128: return launch_tiles<2, 4, 2, 1, false, O, PACKED>(a, p.out, stream);
-    case 64:   // (weights of few rows non-temporal: see fp4_tile_rows)
-      return p.rows <= (int64_t)64 * p.groups ? launch_tiles<4, 1, 2, 2, true, O, PACKED>(a, p.out, stream)
-                                              : launch_tiles<4, 1, 2, 2, false, O, PACKED>(a, p.out, stream);
+    case 256: return once ? launch_tiles<2, 4, 4, 1, true, O, PACKED>(a, p.out, stream)
+                          : launch_tiles<2, 4, 4, 1, false, O, PACKED>(a, p.out, stream);
+    case 128: return once ? launch_tiles<2, 4, 2, 1, true, O, PACKED>(a, p.out, stream)
+                          : launch_tiles<2, 4, 2, 1, false, O, PACKED>(a, p.out, stream);
+    case 64: return once ? launch_tiles<4, 1, 2, 2, true, O, PACKED>(a, p.out, stream)
+                         : launch_tiles<4, 1, 2, 2, false, O, PACKED>(a, p.out, stream);
     default: return launch_tiles<4, 1, 1, 3, true, O, PACKED>(a, p.out, stream);
   }
 }

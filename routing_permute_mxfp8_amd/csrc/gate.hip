@@ -257,10 +257,12 @@ __device__ __forceinline__ int pick(const GateArgs& p, R (&r)[V], int lane, R ta
 template <typename R, typename T, int V, bool SOFTMAX, bool CHECK>
 __device__ __forceinline__ bool choose(const GateArgs& p, const float (&x)[V], const RowNorm<R>& norm, R* lds, int lane,
                                        int* mine) {
-  // Errors of the fp32 ranks (CHECK): a score is off by at most 2^-20 of the row's largest
-  // (the exponent's argument, V_EXP_F32, the sum of up to 1024 terms, the reciprocal), a
-  // rank by its own rounding on top; two ranks closer than twice that, and a group's sums
-  // of two closer than four times that, are decided in 64 bits.
+  // Errors of the fp32 ranks (CHECK). A softmax's sum and its reciprocal: less than 45 2^-24
+  // (22 additions, the exponents' errors weighted by at most ln 1024), the same factor for all
+  // scores of the row; a score's own exponential: less than 4 2^-24 of the largest. A sigmoid:
+  // 2^-22. So two scores are off by less than 2^-18 of the largest together, their ranks by
+  // their roundings on top; ranks closer than that, and groups' sums of two closer than four
+  // times that, are decided in 64 bits.
   const R top = SOFTMAX ? norm.inv : R(1);
   const R tau = CHECK ? top * R(0x1p-18) : R(0), tau_rel = CHECK ? R(0x1p-21) : R(0);
   bool close = false;

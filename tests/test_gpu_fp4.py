@@ -224,7 +224,7 @@ def test_router_to_expert_product():
 
 def test_more_items_than_a_block_lists_at_once():
     """A product of so many tiles that every block of the many-rows kernel computes over 256
-    (it describes 256 at a time): rows from all over it against the oracle."""
+    (it describes 64 at a time): rows from all over it against the oracle."""
     rows, n, k = 300_000, 16384, 128
     say(f"mxfp4_matmul rows={rows} n={n} k={k}")
     rng = np.random.default_rng(0)
