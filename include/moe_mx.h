@@ -412,10 +412,12 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
 /*   row_mask     device, uint8 [rows] or NULL: rows with 0 (padding) do not count. */
 /* moe_gate_topk                                                                 */
 /*   Rank of an expert: r_e = s_e + bias_e (bias fp32 [E] or NULL; it takes part   */
-/*   in the choice only). num_groups G > 1 (E % G == 0, G <= 64): of the G groups   */
-/*   of E / G neighbouring experts only the topk_groups with the largest sums of    */
-/*   their two best ranks take part (k <= topk_groups E / G; an expert taken out    */
-/*   adds 0, a group without any other expert comes last). topk_ids: the k best     */
+/*   in the choice only; NaN in it counts as -inf, and an expert of rank -inf comes */
+/*   last with the experts taken out, but keeps its score). num_groups G > 1        */
+/*   (E % G == 0, G <= 64): of the G groups of E / G neighbouring experts only the   */
+/*   topk_groups with the largest sums of their two best ranks take part            */
+/*   (k <= topk_groups E / G; an expert taken out or of rank -inf adds 0, a group    */
+/*   without any other comes last). topk_ids: the k best                             */
 /*   ranks, largest first, equal ranks (and equal groups) by ascending index, so     */
 /*   they are distinct; the order is that of the exact ranks (ranks too close for    */
 /*   fp32 are compared in 64 bits). topk_weights[j] = scale s_j, or with             */

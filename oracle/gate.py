@@ -40,7 +40,8 @@ def topk(logits, k, scoring, bias=None, groups=1, topk_groups=1, renorm=True, sc
     x = clean(logits)
     n, e = x.shape
     s = scores(logits, scoring)
-    rank = x.copy() if bias is None else np.where(np.isfinite(x), s + np.asarray(bias, np.float64), -np.inf)
+    rank = x.copy() if bias is None else s + np.asarray(bias, np.float64)
+    rank = np.where(np.isfinite(x) & ~np.isnan(rank), rank, -np.inf)
     ids = np.zeros((n, k), dtype=np.int32)
     w = np.zeros((n, k))
     for t in range(n):
@@ -49,8 +50,8 @@ def topk(logits, k, scoring, bias=None, groups=1, topk_groups=1, renorm=True, sc
             size = e // groups
             best = []
             for g in range(groups):
-                live = [s[t, i] + (0.0 if bias is None else float(bias[i])) for i in range(g * size, (g + 1) * size)
-                        if np.isfinite(x[t, i])]
+                live = [s[t, i] if bias is None else rank[t, i] for i in range(g * size, (g + 1) * size)
+                        if rank[t, i] > -np.inf]
                 best.append(sum(sorted(live, reverse=True)[:2]) if live else -np.inf)
             keep = sorted(range(groups), key=lambda g: (-best[g], g))[:topk_groups]
             allowed = [i for i in range(e) if i // size in keep]

@@ -588,11 +588,11 @@ def gate_topk(logits, k: int, *, scoring: int = GATE_SOFTMAX, bias=None, num_gro
     (fp32, fp16 or bf16), as init_routing and mega_moe take them.
 
     scoring: GATE_SOFTMAX (over all E) or GATE_SIGMOID. bias: fp32 [E] added to the scores for
-    the choice only. num_groups / topk_groups: only the topk_groups best of num_groups equal
-    groups of neighbouring experts (by the sum of their two best ranks) take part. The ids come
-    in descending order of rank, ties by the lowest index. renormalize: the weights of a row
-    sum to `scale` (else they are scale * score). A logit of -inf or NaN takes its expert out
-    (score 0, chosen last)."""
+    the choice only (NaN counts as -inf: chosen last). num_groups / topk_groups: only the
+    topk_groups best of num_groups equal groups of neighbouring experts (by the sum of their two
+    best ranks) take part. The ids come in descending order of rank, ties by the lowest index.
+    renormalize: the weights of a row sum to `scale` (else they are scale * score). A logit of
+    -inf or NaN takes its expert out (score 0, chosen last)."""
     lib = load()
     n, e = _gate_logits(logits)
     index = _device_of(logits, bias=bias)

@@ -16,7 +16,8 @@
 //            with Z = sum s, dl_e = s_e (1 - s_e) d_e
 //
 // A logit of -inf or NaN takes its expert out: score 0, ranked behind every other expert
-// of the allowed groups, gradient 0. +inf counts as the largest finite float.
+// of the allowed groups, gradient 0. +inf counts as the largest finite float. A rank of NaN
+// (a bias of NaN) is -inf; an expert of rank -inf is ranked like one taken out, by its index.
 //
 // One wave per row, lane l holding the V experts [l V, l V + V) (V = 1 .. 16 for up to
 // 1024 experts): the row's reductions are DPP steps in one wave, without LDS or barriers.
@@ -161,6 +162,10 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A rank; NaN as -inf (the maximum of a NaN and a number is the number).
+__device__ __forceinline__ float rank_of(float s, float bias) { return fmaxf(s + bias, -INFINITY); }
+__device__ __forceinline__ double rank_of(double s, float bias) { return fmax(s + (double)bias, -(double)INFINITY); }
+
 // (a, b) = the two largest of (a, b) and (c, d), a >= b, c >= d; -inf = none.
 template <typename R>
 __device__ __forceinline__ void merge_two(R& a, R& b, R c, R d) {
@@ -271,7 +276,7 @@ __device__ __forceinline__ bool choose(const GateArgs& p, const float (&x)[V], c
   for (int v = 0; v < V; ++v) {
     const int e = lane * V + v;
     r[v] = e < p.E ? score_of<R, SOFTMAX>(x[v], norm) : R(0);
-    if (p.bias) r[v] += e < p.E ? R(p.bias[e]) : R(0);
+    if (p.bias) r[v] = rank_of(r[v], e < p.E ? p.bias[e] : 0.0f);
     r[v] = x[v] == -INFINITY ? R(-INFINITY) : r[v];
   }
   uint64_t stay = ~0ull;
@@ -556,7 +561,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
       float bias[V];
       load_part<float, V>(p.bias, p.E, sub, vec_bias, bias);
 #pragma unroll
-      for (int v = 0; v < V; ++v) r[v] += bias[v];
+      for (int v = 0; v < V; ++v) r[v] = rank_of(r[v], bias[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = x[v] == -INFINITY ? -INFINITY : r[v];
@@ -655,7 +660,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
     // the candidates' order by their whole ranks, and where those are within their errors by
     // ranks in 64 bits
     const float b = BIAS && held ? p.bias[id] : 0.0f;
-    const float rank = !held ? NAN : BIAS ? (l == -INFINITY ? -INFINITY : s + b) : l;
+    const float rank = !held ? NAN : BIAS ? (l == -INFINITY ? -INFINITY : rank_of(s, b)) : l;
     const float reach = tau + fabsf(rank) * 0x1p-21f;
     bool close = false;
     at = 0;
@@ -670,7 +675,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
     if (BIAS && __ballot(close)) {
       RowNorm<double> exact{0.0, 0.0};
       if constexpr (SOFTMAX) exact = row_norm<double, V>(x);
-      const double r64 = rank == rank && l > -INFINITY ? score_of<double, SOFTMAX>(l, exact) + (double)b : (double)rank;
+      const double r64 = rank == rank && l > -INFINITY ? rank_of(score_of<double, SOFTMAX>(l, exact), b) : (double)rank;
       const uint64_t bits = __builtin_bit_cast(uint64_t, r64);
       at = 0;
       auto against64 = [&]<int L>(std::integral_constant<int, L>) {

@@ -325,3 +325,30 @@ def test_balance_of_many_partials(n, e, seqs):
     # a score is off by at most (|l - m| + 12) 2^-23 of itself, |l - m| < 12; a wave's fp32 sums of
     # at most 64 rows by 64 2^-24; then the rounding of the loss
     assert abs(float(loss) - total) <= (24 * 2.0 ** -23 + 64 * 2.0 ** -24 + 2.0 ** -24) * total
+
+
+BIASES = {
+    "one NaN": lambda e: {e // 3: np.nan},
+    "NaN": lambda e: {i: np.nan for i in range(0, e, 3)},
+    "all NaN": lambda e: {i: np.nan for i in range(e)},
+    "-inf": lambda e: {i: -np.inf for i in range(1, e, 2)},
+    "+inf": lambda e: {1: np.inf, e - 1: np.inf},
+    "all of them": lambda e: {0: np.nan, 1: -np.inf, 2: np.inf, e // 2: np.inf, e - 2: np.nan, e - 1: -np.inf},
+    "largest": lambda e: {i: float(np.finfo(np.float32).max) * (-1) ** i for i in range(0, e, 5)},
+}
+
+
+@pytest.mark.parametrize("e,k,groups,topk_groups", [(7, 5, 1, 1), (60, 8, 1, 1), (128, 8, 4, 2), (256, 8, 1, 1),
+                                                    (256, 8, 8, 4), (60, 9, 1, 1), (160, 6, 8, 3), (300, 12, 1, 1)])
+@pytest.mark.parametrize("kind", list(BIASES))
+def test_gate_bias_without_a_value(e, k, groups, topk_groups, kind):
+    """NaN in the bias is -inf: such experts come last, in index order, whether 16 lanes or the
+    whole wave choose; the ids stay distinct and every place is written."""
+    bias = torch.randn(e, generator=torch.Generator().manual_seed(e)) * 0.1
+    for i, v in BIASES[kind](e).items():
+        bias[i] = v
+    for scoring in ("softmax", "sigmoid"):
+        for dtype, dead in [(torch.float32, 0.0), (torch.bfloat16, 0.3)]:
+            x = logits_of(9, e, dtype, seed=e + k, dead=dead)
+            ids, w = check_gate(x, k, scoring, bias, groups, topk_groups)
+            assert all(len(set(row)) == k for row in ids.tolist()) and bool(torch.isfinite(w).all())

@@ -67,3 +67,15 @@ def test_gradient_against_differences(scoring, renorm):
             z[t, i] -= h
             # central difference: truncation h^2 |f'''| / 6 < 1e-11, rounding 2^-53 |f| / h < 1e-9
             assert abs((total(y) - total(z)) / (2 * h) - got[t, i]) < 1e-7
+
+
+def test_biases_without_a_value():
+    """NaN and -inf in the bias rank an expert last and add nothing to its group; it keeps its score."""
+    x = np.log(np.array([[4.0, 2.0, 1.0, 1.0]]))
+    ids, w = gate.topk(x, 3, "softmax", bias=[np.nan, 0.0, -np.inf, 0.0], renorm=False)
+    assert ids.tolist() == [[1, 3, 0]] and np.allclose(w, [[0.25, 0.125, 0.5]])
+    ids, _ = gate.topk(x, 2, "softmax", bias=[0.0, 0.0, np.inf, np.nan])
+    assert ids.tolist() == [[2, 0]]
+    # group {0, 1} has the sum 0.25, {2, 3} of 0.125
+    ids, _ = gate.topk(x, 2, "softmax", bias=[np.nan, 0.0, -np.inf, 0.0], groups=2, topk_groups=1)
+    assert ids.tolist() == [[1, 0]]
