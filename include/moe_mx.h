@@ -432,7 +432,8 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
 /*   counts int32 [num_seqs, E] = c_be;                                             */
 /*   coef fp32 [num_seqs, E] = alpha E c_be / (k T_b^2 B'): the derivative of the    */
 /*   loss by p_te of each counted row t of b.                                        */
-/*   Sums over rows are fp32 over a few rows and 64 bits beyond, in a fixed order.   */
+/*   Sums over rows are fp32 over at most 64 rows and 64 bits beyond, in a fixed       */
+/*   order; a block's share of a sequence is rounded to fp32 once.                     */
 /* moe_gate_backward: d / d logits, [rows, E] of dtype, of                         */
 /*     sum_tj grad_weights[t, j] topk_weights[t, j] + grad_loss[0] loss             */
 /*   grad_weights fp32 [rows, k] or NULL (no gradient of the weights): the choice     */

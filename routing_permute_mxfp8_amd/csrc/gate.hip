@@ -723,13 +723,18 @@ __device__ __forceinline__ void seq_rows(const int32_t* off, int b, int64_t rows
 
 // ---- balance loss ---------------------------------------------------------------------
 // First pass: block (s, b) sums the scores and counts the choices of its share of sequence
-// b's rows: one partial row each, in the same order on every call.
+// b's rows: one partial row each, in the same order on every call. A share has no upper limit
+// (one sequence may hold all rows of many), so a lane adds only kSumRows rows in fp32 and then
+// joins them to a sum in 64 bits in LDS: fp32 throughout was off by 2^-15 after 2048 equal rows.
+// The partial row is rounded to fp32 once.
+constexpr int kSumRows = 16;
+
 template <typename T, int V, bool SOFTMAX>
 __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
     const T* __restrict__ logits, int64_t rows, int E, bool vec, const int32_t* __restrict__ ids, int k,
     const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, float* __restrict__ sums,
     int32_t* __restrict__ counts, int32_t* __restrict__ held, unsigned* __restrict__ done) {
-  extern __shared__ float lds_sums[];   // [waves][E] sums, then [E] counts
+  extern __shared__ double lds_sums[];   // [waves][E] sums, then [E] counts
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int* hist = reinterpret_cast<int*>(lds_sums + kRowsPerBlock * E);
@@ -742,8 +747,21 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
   const int64_t len = hi - lo, first = lo + len * s / splits, last = lo + len * (s + 1) / splits;
   float acc[V] = {};
   int seen = 0;
+  bool joined = false;
+  auto join = [&]() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (lane * V + v < E) {
+        double& sum = lds_sums[wave * E + lane * V + v];
+        sum = (joined ? sum : 0.0) + (double)acc[v];
+      }
+      acc[v] = 0.0f;
+    }
+    joined = true;
+  };
   for (int64_t row = first + wave; row < last; row += kRowsPerBlock) {
     if (mask && mask[row] == 0) continue;   // uniform per wave
+    if (seen > 0 && seen % kSumRows == 0) join();
     ++seen;
     float x[V];
     load_row<T, V>(logits + row * E, E, lane, vec, x);
@@ -768,18 +786,16 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
       for (int v = 0; v < V; ++v) acc[v] += sc[v] * inv;
     }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (lane * V + v < E) lds_sums[wave * E + lane * V + v] = acc[v];
+  join();
   __shared__ int rows_seen[kRowsPerBlock];
   if (lane == 0) rows_seen[wave] = seen;
   __syncthreads();
   const int64_t part = (int64_t)b * splits + s;
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    float t = 0.0f;
+    double t = 0.0;
 #pragma unroll
     for (int w = 0; w < kRowsPerBlock; ++w) t += lds_sums[w * E + e];
-    sums[part * E + e] = t;
+    sums[part * E + e] = (float)t;
     counts[part * E + e] = hist[e];
   }
   if (threadIdx.x == 0) {
@@ -797,7 +813,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
     const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, float* __restrict__ sums,
     int32_t* __restrict__ counts, int32_t* __restrict__ held, unsigned* __restrict__ done) {
   constexpr int W = kPiece<T, V>;
-  __shared__ float lds_sums[kRowsPerBlock][16 * V];
+  __shared__ double lds_sums[kRowsPerBlock][16 * V];
   __shared__ int hist[16 * V];
   __shared__ int rows_seen[kRowsPerBlock];
   const int lane = threadIdx.x & 63, sub = lane & 15, part = lane >> 4;
@@ -823,10 +839,26 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
     for (int i = 0; i < 2; ++i) r.id[i] = sub + 16 * i < k ? ids[row * k + sub + 16 * i] : -1;
     r.counted = (at + part < last) & ((mask ? mask[row] : 1) != 0);
   };
+  int rounds = 0;
+  auto join = [&]() {   // the wave's sums, of its four rows at a time
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float t = acc[v];
+      t += __shfl_xor(t, 16, 64);
+      t += __shfl_xor(t, 32, 64);
+      if (part == 0) {
+        double& sum = lds_sums[wave][dealt<W>(sub, v)];
+        sum = (rounds > kSumRows ? sum : 0.0) + (double)t;
+      }
+      acc[v] = 0.0f;
+    }
+  };
   int64_t at = first + 4 * wave;
   Rows cur;
   if (at < last) load(at, cur);
   for (; at < last; at += 4 * kRowsPerBlock) {
+    if (rounds > 0 && rounds % kSumRows == 0) join();
+    ++rounds;
     Rows next;
     if (at + 4 * kRowsPerBlock < last) load(at + 4 * kRowsPerBlock, next);
     const bool counted = cur.counted;
@@ -855,12 +887,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
     }
     cur = next;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {   // the four rows of the wave
-    acc[v] += __shfl_xor(acc[v], 16, 64);
-    acc[v] += __shfl_xor(acc[v], 32, 64);
-    if (part == 0) lds_sums[wave][dealt<W>(sub, v)] = acc[v];
-  }
+  join();
   const int rows_of_wave = __popcll(__ballot(seen & 1)) + 2 * __popcll(__ballot(seen & 2)) + 4 * __popcll(__ballot(seen & 4));
   int more = seen >> 3;   // (over 7 row quads a wave: long sequences)
   for (int d = 1; d < 64; d *= 2) more += __shfl_xor(more, d, 64);
@@ -868,10 +895,10 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance16_sums_kernel(
   __syncthreads();
   const int64_t to = (int64_t)b * splits + s;
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    float t = 0.0f;
+    double t = 0.0;
 #pragma unroll
     for (int w = 0; w < kRowsPerBlock; ++w) t += lds_sums[w][e];
-    sums[to * E + e] = t;
+    sums[to * E + e] = (float)t;
     counts[to * E + e] = hist[e];
   }
   if (threadIdx.x == 0) {
@@ -1340,7 +1367,7 @@ hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
     return with_width(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
       const bool vec = wide_rows<T>(p.logits, p.experts, V);
-      const size_t lds = sizeof(float) * (kRowsPerBlock + 1) * p.experts;
+      const size_t lds = (sizeof(double) * kRowsPerBlock + sizeof(int)) * p.experts;
       return p.sigmoid ? go(balance_sums_kernel<T, V, false>, vec, lds) : go(balance_sums_kernel<T, V, true>, vec, lds);
     });
   });

@@ -352,3 +352,34 @@ def test_gate_bias_without_a_value(e, k, groups, topk_groups, kind):
             x = logits_of(9, e, dtype, seed=e + k, dead=dead)
             ids, w = check_gate(x, k, scoring, bias, groups, topk_groups)
             assert all(len(set(row)) == k for row in ids.tolist()) and bool(torch.isfinite(w).all())
+
+
+@pytest.mark.parametrize("e", [256, 512])
+@pytest.mark.parametrize("equal", [True, False])
+def test_balance_of_one_long_sequence_among_many(e, equal):
+    """1023 sequences of three rows and one of 32768, where a block may get a whole sequence:
+    what its lanes add in fp32 must not grow with the sequence. The loss of rows that all chose
+    one expert is a single expert's sum. With equal rows every addition rounds the same way:
+    2048 of them (8192 above 256 experts) are off by up to 2^-15 (2^-13).
+    Bound: a score by 2^-17.5 (|l - m| < 12: (24 + 22 + 8) 2^-24; the same for equal rows), at
+    most 64 rows added in fp32 by 2^-18, roundings of the partial sum and of the loss 2^-23."""
+    rng = np.random.default_rng(e)
+    long, short = 32768, 1023
+    n = long + 3 * short
+    rows = rng.standard_normal((n, e)).astype(np.float32) * 1.5
+    if equal:
+        rows[:] = rows[0]
+    off = np.array([0, *(3 * np.arange(1, 513)), 3 * 512 + long,
+                    *(3 * 512 + long + 3 * np.arange(1, 512))], dtype=np.int32)
+    assert off[-1] == n and off.size == 1025
+    mask = np.zeros(n, dtype=np.uint8)
+    mask[3 * 512:3 * 512 + long] = 1   # only the long one counts
+    p = torch.softmax(torch.from_numpy(rows[3 * 512:3 * 512 + long]).double(), 1).mean(0).numpy()
+    x = torch.from_numpy(rows).to(DEV)
+    for expert in (0, 7, e // 3, e // 2 + 1, e - 60, e - 37, e - 2, e - 1):
+        say(f"balance_loss long sequence e={e} equal={equal} expert={expert}")
+        ids = torch.full((n, 1), expert, dtype=torch.int32, device=DEV)
+        loss, counts, _ = rp.balance_loss(x, ids, seq_offsets=dev(off), row_mask=dev(mask))
+        assert int(counts[512, expert]) == long and int(counts.sum()) == long
+        want = e * float(p[expert])
+        assert abs(float(loss) - want) <= (2.0 ** -17.5 + 2.0 ** -18 + 2.0 ** -23) * want
