@@ -145,7 +145,7 @@ __device__ __forceinline__ R score_of(float x, const RowNorm<R>& n) {
 // ---- gate -----------------------------------------------------------------------------
 struct GateArgs {
   const float* bias;      // nullable [E]
-  int64_t rows;
+  int64_t first, rows;    // the launch's rows: [first, rows)
   int E, k;
   int groups, topk_groups, group_size;
   uint32_t group_magic;   // e / group_size = umulhi(e, group_magic) for e < 1024 (group_size > 1)
@@ -349,7 +349,7 @@ template <typename T, int V, bool SOFTMAX>
 __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __restrict__ logits, GateArgs p) {
   extern __shared__ double lds_ranks[];   // [waves][E] with groups
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + wave;
+  const int64_t row = p.first + (int64_t)blockIdx.x * kRowsPerBlock + wave;
   if (row >= p.rows) return;
   gate_row<T, V, SOFTMAX>(logits, p, row, lds_ranks + wave * p.E, threadIdx.x & 63, p.vec);
 }
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_kernel(const T* __r
   extern __shared__ double lds_ranks[];   // [waves][E] with groups
   const int lane = threadIdx.x & 63, sub = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row0 = ((int64_t)blockIdx.x * kRowsPerBlock + wave) * 4;
+  const int64_t row0 = p.first + ((int64_t)blockIdx.x * kRowsPerBlock + wave) * 4;
   if (row0 >= p.rows) return;
   const int64_t row = min(row0 + (lane >> 4), p.rows - 1);
   const bool there = row0 + (lane >> 4) < p.rows;
@@ -1009,7 +1009,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
 
 // ---- gradient -------------------------------------------------------------------------
 struct GateGradArgs {
-  int64_t rows;
+  int64_t first, rows;         // the launch's rows: [first, rows)
   int E, k;
   bool renorm, vec;
   float scale;
@@ -1050,7 +1050,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const
   extern __shared__ float lds_grad[];   // [waves][64 V]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + wave;
+  const int64_t row = p.first + (int64_t)blockIdx.x * kRowsPerBlock + wave;
   if (row >= p.rows) return;
   const T* rp = logits + row * p.E;
   float x[V], s[V], d[V];
@@ -1142,7 +1142,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(con
   __shared__ __align__(16) float lds_grad[4 * kRowsPerBlock][16 * V];
   const int lane = threadIdx.x & 63, sub = lane & 15, part = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row0 = ((int64_t)blockIdx.x * kRowsPerBlock + wave) * 4;
+  const int64_t row0 = p.first + ((int64_t)blockIdx.x * kRowsPerBlock + wave) * 4;
   if (row0 >= p.rows) return;
   const int64_t row = min(row0 + part, p.rows - 1);
   const T* rp = logits + row * p.E;
@@ -1275,6 +1275,22 @@ hipError_t with_type(int dtype, F&& f) {
     default: return f((const uint16_t*)nullptr);
   }
 }
+// A launch has at most 2^32 - 1 threads along x (the runtime takes more without an error and
+// leaves the rows past them undone), and a row takes up to 64: calls of more than kLaunchRows
+// rows are several launches. `launch` gets the first row and the end of each.
+constexpr int64_t kLaunchRows = 1 << 25;
+template <typename F>
+hipError_t in_launches(int64_t rows, F&& launch) {
+  for (int64_t first = 0; first < rows; first += kLaunchRows) {
+    launch(first, std::min(rows, first + kLaunchRows));
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+// Blocks of `per` rows each for the rows [first, end).
+unsigned blocks_of(int64_t first, int64_t end, int per) { return (unsigned)((end - first + per - 1) / per); }
+
 template <typename T>
 bool wide_rows(const void* p, int E, int V) {
   return E % V == 0 && reinterpret_cast<uintptr_t>(p) % std::min<size_t>(16, V * sizeof(T)) == 0;
@@ -1286,7 +1302,7 @@ namespace {
 
 template <typename T, int V>
 void launch_gate16(const GateParams& p, GateArgs a, bool vec64, hipStream_t stream) {
-  const unsigned grid = (unsigned)((p.rows + 4 * kRowsPerBlock - 1) / (4 * kRowsPerBlock));
+  const unsigned grid = blocks_of(a.first, a.rows, 4 * kRowsPerBlock);
   const size_t lds = p.groups > 1 ? sizeof(double) * kRowsPerBlock * p.experts : 0;
   const bool vec_bias = wide_rows<float>(p.bias, p.experts, V);
   auto go = [&](auto soft, auto bias) {
@@ -1302,7 +1318,7 @@ void launch_gate16(const GateParams& p, GateArgs a, bool vec64, hipStream_t stre
 hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   if (p.rows <= 0) return hipSuccess;
   GateArgs a{};
-  a.bias = p.bias; a.rows = p.rows; a.E = p.experts; a.k = p.k;
+  a.bias = p.bias; a.E = p.experts; a.k = p.k;
   a.groups = p.groups; a.topk_groups = p.topk_groups; a.group_size = p.experts / p.groups;
   if (a.group_size > 1) a.group_magic = (uint32_t)(((uint64_t(1) << 32) + a.group_size - 1) / a.group_size);
   a.renorm = p.renorm; a.scale = p.scale; a.ids = p.ids; a.weights = p.weights;
@@ -1317,25 +1333,29 @@ hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
       return with_width16(p.experts, [&](auto w) {
         constexpr int V = decltype(w)::value;
         a.vec = wide_rows<T>(p.logits, p.experts, V);
-        launch_gate16<T, V>(p, a, wide_rows<T>(p.logits, p.experts, V / 4), stream);
-        return hipGetLastError();
+        return in_launches(p.rows, [&](int64_t first, int64_t end) {
+          a.first = first; a.rows = end;
+          launch_gate16<T, V>(p, a, wide_rows<T>(p.logits, p.experts, V / 4), stream);
+        });
       });
     });
   }
   a.lanes = 64;
   while (64 / a.lanes < a.groups) a.lanes /= 2;
-  const unsigned grid = (unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock);
   const size_t lds = p.groups > 1 ? sizeof(double) * kRowsPerBlock * p.experts : 0;
   return with_type(p.dtype, [&](auto* t) {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(t)>>;
     return with_width(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
       a.vec = wide_rows<T>(p.logits, p.experts, V);
-      if (p.sigmoid)
-        gate_kernel<T, V, false><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a);
-      else
-        gate_kernel<T, V, true><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a);
-      return hipGetLastError();
+      return in_launches(p.rows, [&](int64_t first, int64_t end) {
+        a.first = first; a.rows = end;
+        const unsigned grid = blocks_of(first, end, kRowsPerBlock);
+        if (p.sigmoid)
+          gate_kernel<T, V, false><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a);
+        else
+          gate_kernel<T, V, true><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a);
+      });
     });
   });
 }
@@ -1389,7 +1409,7 @@ hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
 hipError_t launch_gate_backward(const GateGradParams& p, hipStream_t stream) {
   if (p.rows <= 0) return hipSuccess;
   GateGradArgs a{};
-  a.rows = p.rows; a.E = p.experts; a.k = p.k; a.renorm = p.renorm; a.scale = p.scale; a.ids = p.ids;
+  a.E = p.experts; a.k = p.k; a.renorm = p.renorm; a.scale = p.scale; a.ids = p.ids;
   a.grad_weights = p.grad_weights; a.grad_loss = p.grad_loss; a.coef = p.coef; a.off = p.off; a.seqs = p.seqs;
   a.mask = p.mask;
   return with_type(p.dtype, [&](auto* t) {
@@ -1397,26 +1417,30 @@ hipError_t launch_gate_backward(const GateGradParams& p, hipStream_t stream) {
     if (p.experts <= kMost16)
       return with_width16(p.experts, [&](auto w) {
         constexpr int V = decltype(w)::value;
-        const unsigned grid = (unsigned)((p.rows + 4 * kRowsPerBlock - 1) / (4 * kRowsPerBlock));
         constexpr int W = kPiece<T, V>;
         a.vec = wide_rows<T>(p.logits, p.experts, W) && wide_rows<T>(p.grad, p.experts, W);
         const bool vec_coef = wide_rows<float>(p.coef, p.experts, W);
         auto go = [&](auto kernel) {
-          kernel<<<grid, 64 * kRowsPerBlock, 0, stream>>>((const T*)p.logits, a, vec_coef, (T*)p.grad);
-          return hipGetLastError();
+          return in_launches(p.rows, [&](int64_t first, int64_t end) {
+            a.first = first; a.rows = end;
+            kernel<<<blocks_of(first, end, 4 * kRowsPerBlock), 64 * kRowsPerBlock, 0, stream>>>((const T*)p.logits, a,
+                                                                                                vec_coef, (T*)p.grad);
+          });
         };
         return p.sigmoid ? go(gate16_backward_kernel<T, V, false>) : go(gate16_backward_kernel<T, V, true>);
       });
     return with_width(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
-      const unsigned grid = (unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock);
       a.vec = wide_rows<T>(p.logits, p.experts, V);
       const size_t lds = sizeof(float) * kRowsPerBlock * 64 * V;
-      if (p.sigmoid)
-        gate_backward_kernel<T, V, false><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a, (T*)p.grad);
-      else
-        gate_backward_kernel<T, V, true><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a, (T*)p.grad);
-      return hipGetLastError();
+      return in_launches(p.rows, [&](int64_t first, int64_t end) {
+        a.first = first; a.rows = end;
+        const unsigned grid = blocks_of(first, end, kRowsPerBlock);
+        if (p.sigmoid)
+          gate_backward_kernel<T, V, false><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a, (T*)p.grad);
+        else
+          gate_backward_kernel<T, V, true><<<grid, 64 * kRowsPerBlock, lds, stream>>>((const T*)p.logits, a, (T*)p.grad);
+      });
     });
   });
 }

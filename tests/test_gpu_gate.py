@@ -383,3 +383,59 @@ def test_balance_of_one_long_sequence_among_many(e, equal):
         assert int(counts[512, expert]) == long and int(counts.sum()) == long
         want = e * float(p[expert])
         assert abs(float(loss) - want) <= (2.0 ** -17.5 + 2.0 ** -18 + 2.0 ** -23) * want
+
+
+def repeated(base, rows):
+    """`rows` rows: those of base over and over."""
+    x = base.repeat(-(-rows // base.shape[0]), 1)
+    return x[:rows]
+
+
+def assert_repeats(got, want):
+    """got's rows are want's rows over and over."""
+    n = want.shape[0]
+    whole = got.shape[0] // n * n
+    assert bool((got[:whole].view(-1, *want.shape) == want).all()) and torch.equal(got[whole:], want[:got.shape[0] - whole])
+
+
+def test_gate_of_more_rows_than_a_launch_takes():
+    """2^26 rows at 64 lanes each and 2^28 at 16 are more threads than one launch has."""
+    n, e, k = (1 << 26) + 5, 10, 9
+    base = logits_of(1 << 12, e, torch.bfloat16, seed=1).to(DEV)
+    say(f"gate_topk {n}x{e} k={k}")
+    ids, w = rp.gate_topk(repeated(base, n), k)
+    want = rp.gate_topk(base, k)
+    assert_repeats(ids, want[0])
+    assert_repeats(w, want[1])
+    del ids, w
+    n, e, k = (1 << 28) + 7, 2, 1
+    base = logits_of(1 << 12, e, torch.bfloat16, seed=2).to(DEV)
+    x = repeated(base, n)
+    say(f"gate_topk {n}x{e} k={k}")
+    ids, w = rp.gate_topk(x, k, renormalize=False)
+    want = rp.gate_topk(base, k, renormalize=False)
+    assert_repeats(ids, want[0])
+    assert_repeats(w, want[1])
+
+
+def test_backward_of_more_rows_than_a_launch_takes():
+    """The same for the gradient, with sequences that begin and end behind the first launch's rows
+    and a mask."""
+    n, e, k = (1 << 28) + 7, 2, 1
+    base = logits_of(1 << 12, e, torch.bfloat16, seed=2).to(DEV)
+    x = repeated(base, n)
+    ids = rp.gate_topk(base, k)[0]
+    gl = torch.ones(1, device=DEV)
+    cut = [0, 1 << 27, (1 << 28) - 4096, 1 << 28]   # multiples of the period; the last 7 rows belong to none
+    off = torch.tensor(cut, dtype=torch.int32, device=DEV)
+    coef = torch.tensor([[0.25, 0.5], [1.0, -1.0], [2.0, 0.125]], device=DEV)
+    mask = (torch.arange(1 << 12, device=DEV) % 5 != 0).to(torch.uint8)
+    gw = torch.randn((1 << 12, k), generator=torch.Generator().manual_seed(0)).to(DEV)
+    say(f"gate_backward {n}x{e} k={k}")
+    got = rp.gate_backward(x, repeated(ids, n), repeated(gw, n), renormalize=False, grad_loss=gl, coef=coef,
+                           seq_offsets=off, row_mask=repeated(mask[:, None], n)[:, 0].contiguous())
+    del x
+    for b in range(3):
+        want = rp.gate_backward(base, ids, gw, renormalize=False, grad_loss=gl, coef=coef[b:b + 1], row_mask=mask)
+        assert_repeats(got[cut[b]:cut[b + 1]], want)
+    assert torch.equal(got[1 << 28:], rp.gate_backward(base, ids, gw, renormalize=False)[:7])
