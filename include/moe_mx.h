@@ -404,7 +404,8 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
 /*                largest finite fp32 value.                                       */
 /*   num_experts  E in [1, 1024]; k in [1, min(32, E)]; rows < 2^31                */
 /*   scoring      MOE_GATE_SOFTMAX: s_e = exp(l_e) / sum_i exp(l_i) over all E;     */
-/*                MOE_GATE_SIGMOID: s_e = 1 / (1 + exp(-l_e)). Held in fp32.       */
+/*                MOE_GATE_SIGMOID: s_e = 1 / (1 + exp(-l_e)). Held in fp32; a      */
+/*                sigmoid below 2^-126 (l < -87.3) may come as 0.                   */
 /*   seq_offsets  device, int32 [num_seqs + 1], non-decreasing: the rows of         */
 /*                sequence b are [off[b], off[b + 1]); rows outside [off[0],        */
 /*                off[num_seqs]) belong to none. NULL: all rows are one sequence    */
@@ -440,7 +441,8 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
 /*   topk_ids is held fixed, scoring / renormalize / scale as in moe_gate_topk;       */
 /*   grad_loss fp32 [1] or NULL (no gradient of the loss): with the coef, seq_offsets */
 /*   and row_mask of moe_balance_loss (the counts are held fixed). Both are added in  */
-/*   one pass over the logits. An id outside [0, E) adds nothing.                     */
+/*   one pass over the logits. An id outside [0, E) adds nothing. Sums of scores       */
+/*   below 2^-126, the smallest normal fp32, count as 0 and their gradient is 0.        */
 /* ------------------------------------------------------------------------ */
 enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 };
 #define MOE_GATE_MAX_EXPERTS 1024

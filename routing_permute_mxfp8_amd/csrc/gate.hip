@@ -1030,6 +1030,18 @@ __device__ __forceinline__ T value_as(float v) {
     return (T)v;
 }
 
+// Every term of the gradient is a gradient times a score, or times a quotient of a score by a
+// sum of them: c_j = g_j s_j (renormalised: (scale dw_j - sum_i scale dw_i w_i) w_j with w_j =
+// s_j / S), q_e p_e, and 1 - s for a sigmoid. A sigmoid's sums may lie near fp32's smallest, so
+// that a gradient over them, the other way to write this, would overflow. A sum below 2^-126
+// (its reciprocal overflows) counts as 0, like its scores.
+__device__ __forceinline__ float inverse_sum(float sum) { return sum >= FLT_MIN ? 1.0f / sum : 0.0f; }
+// 1 - s of a sigmoid, also of a score near 1, with t = exp(-|l|).
+__device__ __forceinline__ float sigmoid_rest(float l) {
+  const float t = exp_of(-fabsf(l)), r = 1.0f / (1.0f + t);
+  return l > 0.0f ? t * r : r;
+}
+
 // The sequence of a row (-1: none): the last that starts at or before it, if it holds it.
 __device__ __forceinline__ int row_seq(const int32_t* off, int seqs, int64_t row) {
   if (!off) return 0;
@@ -1077,11 +1089,10 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const
       sc = l == -INFINITY ? 0.0f : score_of<float, SOFTMAX>(l, norm);
     }
     if (p.renorm) {
-      const float total = wave_sum(sc);
-      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-      g = (g - wave_sum(g * sc) * inv) * inv;
+      sc *= inverse_sum(wave_sum(sc));
+      g -= wave_sum(g * sc);
     }
-    if (id >= 0) area[id] = g;
+    if (id >= 0) area[id] = g * sc;
     wave_lds_fence();
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = area[lane * V + v];
@@ -1104,28 +1115,25 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      d[v] += q[v];
-      dot += d[v] * s[v];
+      d[v] += q[v] * s[v];
+      dot += d[v];
     }
     dot = wave_sum(dot);
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = s[v] * (d[v] - dot);
+    for (int v = 0; v < V; ++v) d[v] -= s[v] * dot;
   } else {
     float dot = 0.0f, z = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      dot += q[v] * s[v];
-      z += s[v];
-    }
-    z = wave_sum(z);
-    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
-    dot = wave_sum(dot) * inv;
+    for (int v = 0; v < V; ++v) z += s[v];
+    const float inv = inverse_sum(wave_sum(z));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      // s (1 - s) = t / (1 + t)^2 with t = exp(-|l|): 1 - s would lose the digits of a score near 1
-      const float t = exp_of(-fabsf(x[v])), r = 1.0f / (1.0f + t);
-      d[v] = (d[v] + (q[v] - dot) * inv) * (t * r * r);
+      s[v] *= inv;
+      dot += q[v] * s[v];
     }
+    dot = wave_sum(dot);
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = (d[v] + (q[v] - dot) * s[v]) * sigmoid_rest(x[v]);
   }
   T* out = grad + row * p.E;
 #pragma unroll
@@ -1189,15 +1197,16 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(con
 #pragma unroll
     for (int i = 0; i < 2; ++i) sc[i] = l[i] == -INFINITY ? 0.0f : score_of<float, SOFTMAX>(l[i], norm);
     if (p.renorm) {
-      const float total = row_sum(sc[0] + sc[1]);
-      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-      const float mean = row_sum(g[0] * sc[0] + g[1] * sc[1]) * inv;
+      const float inv = inverse_sum(row_sum(sc[0] + sc[1]));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) g[i] = (g[i] - mean) * inv;
+      for (int i = 0; i < 2; ++i) sc[i] *= inv;
+      const float mean = row_sum(g[0] * sc[0] + g[1] * sc[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) g[i] -= mean;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (id[i] >= 0) area[id[i]] = g[i];
+      if (id[i] >= 0) area[id[i]] = g[i] * sc[i];
     wave_lds_fence();
 #pragma unroll
     for (int v = 0; v < V; v += N) {
@@ -1210,27 +1219,25 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(con
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      d[v] += q[v];
-      dot += d[v] * s[v];
+      d[v] += q[v] * s[v];
+      dot += d[v];
     }
     dot = row_sum(dot);
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = s[v] * (d[v] - dot);
+    for (int v = 0; v < V; ++v) d[v] -= s[v] * dot;
   } else {
     float dot = 0.0f, z = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      dot += q[v] * s[v];
-      z += s[v];
-    }
-    z = row_sum(z);
-    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
-    dot = row_sum(dot) * inv;
+    for (int v = 0; v < V; ++v) z += s[v];
+    const float inv = inverse_sum(row_sum(z));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float t = exp_of(-fabsf(x[v])), r = 1.0f / (1.0f + t);
-      d[v] = (d[v] + (q[v] - dot) * inv) * (t * r * r);
+      s[v] *= inv;
+      dot += q[v] * s[v];
     }
+    dot = row_sum(dot);
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = (d[v] + (q[v] - dot) * s[v]) * sigmoid_rest(x[v]);
   }
   if (row0 + part >= p.rows) return;
   T* out = grad + row * p.E;

@@ -439,3 +439,34 @@ def test_backward_of_more_rows_than_a_launch_takes():
         want = rp.gate_backward(base, ids, gw, renormalize=False, grad_loss=gl, coef=coef[b:b + 1], row_mask=mask)
         assert_repeats(got[cut[b]:cut[b + 1]], want)
     assert torch.equal(got[1 << 28:], rp.gate_backward(base, ids, gw, renormalize=False)[:7])
+
+
+@pytest.mark.parametrize("e,k", [(60, 4), (256, 8), (300, 4)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_backward_where_the_scores_are_tiny(e, k, renorm):
+    """Sigmoid scores near fp32's smallest (2^-126 = exp(-87.3)) under large gradients: the
+    quotients by their sums are of ordinary size, the reciprocals of these sums are not.
+    A score's exponent is off by 87 log2 e (2^-24 + 2^-25) and so the score by under 2^-16.8, a
+    quotient of two by 2^-15.8, the differences of at most k + 1 such terms by no more of the sum of
+    their magnitudes: within GRAD. A score below 2^-126 is 0 in fp32 (here exp(-120) = 2^-173): every
+    term of its own element has it as a factor, so that element may be off by all of its magnitude
+    (some 2^-46 of the others'); in the row's sums, over 2^-126 each, it is missing by under 2^-40."""
+    n = 33
+    rng = np.random.default_rng(e)
+    x = torch.from_numpy(rng.uniform(-87.2, -84.0, (n, e)).astype(np.float32))
+    x[1] = -87.25
+    x[2, ::2] = -120.0   # scores of 0
+    ids = gate.topk(x.double().numpy(), k, "sigmoid")[0]
+    gw = (rng.standard_normal((n, k)) * 1000).astype(np.float32)
+    coef = torch.from_numpy(rng.random((1, e)).astype(np.float32) * 1000)
+    for parts in ("w", "l", "wl"):
+        say(f"gate_backward tiny scores e={e} k={k} renorm={renorm} {parts}")
+        gl = np.array([3.0], dtype=np.float32) if "l" in parts else None
+        got = rp.gate_backward(x.to(DEV), dev(ids), dev(gw) if "w" in parts else None, scoring=rp.GATE_SIGMOID,
+                               renormalize=renorm, grad_loss=dev(gl), coef=coef.to(DEV) if gl is not None else None)
+        want, mag = gate.backward(x.double().numpy(), ids, "sigmoid", gw if "w" in parts else None, renorm, 1.0, gl,
+                                  coef.double().numpy())
+        got = got.cpu().double().numpy()
+        assert np.all(np.isfinite(got))
+        own = np.where(gate.scores(x.double().numpy(), "sigmoid") < 2.0 ** -126, 1.0, GRAD)
+        assert np.all(np.abs(got - want) <= own * mag + 2.0 ** -24 * (np.abs(want) + GRAD * mag) + 2.0 ** -120)
