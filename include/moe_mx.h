@@ -441,8 +441,9 @@ moe_status moe_combine_finalize(const float* y_accum, int64_t num_tokens, int64_
 /*   topk_ids is held fixed, scoring / renormalize / scale as in moe_gate_topk;       */
 /*   grad_loss fp32 [1] or NULL (no gradient of the loss): with the coef, seq_offsets */
 /*   and row_mask of moe_balance_loss (the counts are held fixed). Both are added in  */
-/*   one pass over the logits. An id outside [0, E) adds nothing. Sums of scores       */
-/*   below 2^-126, the smallest normal fp32, count as 0 and their gradient is 0.        */
+/*   one pass over the logits. An id outside [0, E) adds nothing, one that stands   */
+/*   in several places of a row all of their gradients. Sums of scores below 2^-126,     */
+/*   the smallest normal fp32, count as 0 and their gradient is 0.                       */
 /* ------------------------------------------------------------------------ */
 enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 };
 #define MOE_GATE_MAX_EXPERTS 1024

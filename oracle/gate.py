@@ -123,8 +123,9 @@ def backward(logits, ids, scoring, grad_weights=None, renorm=True, scale=1.0, gr
             inv = np.where(total > 0, 1.0 / np.where(total > 0, total, 1.0), 0.0)
             gm = (gm + (gm * sel).sum(axis=1, keepdims=True) * inv) * inv
             g = (g - (g * sel).sum(axis=1, keepdims=True) * inv) * inv
-        np.put_along_axis(d, ids, g, axis=1)
-        np.put_along_axis(dm, ids, gm, axis=1)
+        rows = np.arange(n)[:, None]
+        np.add.at(d, (rows, ids), g)   # an id may stand in several places
+        np.add.at(dm, (rows, ids), gm)
     q = np.zeros((n, e))
     if grad_loss is not None:
         seq, _ = sequences(n, offsets, mask)

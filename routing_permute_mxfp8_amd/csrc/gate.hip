@@ -1092,7 +1092,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_backward_kernel(const
       sc *= inverse_sum(wave_sum(sc));
       g -= wave_sum(g * sc);
     }
-    if (id >= 0) area[id] = g * sc;
+    if (id >= 0) atomicAdd(&area[id], g * sc);   // (an id may stand in several places; one wave: a fixed order)
     wave_lds_fence();
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = area[lane * V + v];
@@ -1206,7 +1206,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(con
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (id[i] >= 0) area[id[i]] = g[i] * sc[i];
+      if (id[i] >= 0) atomicAdd(&area[id[i]], g[i] * sc[i]);   // (an id may stand in several places)
     wave_lds_fence();
 #pragma unroll
     for (int v = 0; v < V; v += N) {

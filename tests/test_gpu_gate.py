@@ -470,3 +470,25 @@ def test_backward_where_the_scores_are_tiny(e, k, renorm):
         assert np.all(np.isfinite(got))
         own = np.where(gate.scores(x.double().numpy(), "sigmoid") < 2.0 ** -126, 1.0, GRAD)
         assert np.all(np.abs(got - want) <= own * mag + 2.0 ** -24 * (np.abs(want) + GRAD * mag) + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("e,k", [(8, 4), (60, 8), (256, 32), (300, 6)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_backward_of_an_expert_chosen_twice(e, k, scoring, renorm):
+    """An id that stands in several places of a row gets the sum of their gradients."""
+    n = 21
+    rng = np.random.default_rng(e + k)
+    x = logits_of(n, e, torch.float32, seed=e)
+    ids = rng.integers(0, e, (n, k)).astype(np.int32)
+    ids[0] = 3
+    ids[1, 1] = ids[1, 0]
+    ids[2, -1] = ids[2, 0]
+    gw = rng.standard_normal((n, k)).astype(np.float32)
+    say(f"gate_backward repeated ids e={e} k={k} {scoring} renorm={renorm}")
+    call = lambda: rp.gate_backward(x.to(DEV), dev(ids), dev(gw), scoring=SCORING[scoring], renormalize=renorm)
+    got = call()
+    want, mag = gate.backward(x.double().numpy(), ids, scoring, gw, renorm)
+    assert np.all(np.abs(got.cpu().double().numpy() - want) <= GRAD * mag + 2.0 ** -24 * (np.abs(want) + GRAD * mag) + 2.0 ** -120)
+    for _ in range(3):
+        assert torch.equal(got, call())

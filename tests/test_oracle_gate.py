@@ -79,3 +79,23 @@ def test_biases_without_a_value():
     # group {0, 1} has the sum 0.25, {2, 3} of 0.125
     ids, _ = gate.topk(x, 2, "softmax", bias=[np.nan, 0.0, -np.inf, 0.0], groups=2, topk_groups=1)
     assert ids.tolist() == [[1, 0]]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_gradient_of_an_expert_chosen_twice(scoring):
+    """An id that stands twice in a row gets both gradients (differences of the weights)."""
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((2, 5))
+    ids, gw = np.array([[1, 1, 3], [2, 2, 2]]), rng.standard_normal((2, 3))
+
+    def total(y):
+        w = np.take_along_axis(gate.scores(y, scoring), ids, axis=1)
+        return float((w / w.sum(axis=1, keepdims=True) * gw).sum())
+
+    got, h = gate.backward(x, ids, scoring, gw)[0], 1e-6
+    for t in range(2):
+        for i in range(5):
+            y, z = x.copy(), x.copy()
+            y[t, i] += h
+            z[t, i] -= h
+            assert abs((total(y) - total(z)) / (2 * h) - got[t, i]) < 1e-7
