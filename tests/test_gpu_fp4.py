@@ -5,6 +5,8 @@ Bound: the FP4 products are exact, a K step of 128 adds its products and the acc
 fp32; a wave's partial sums (up to 8) are added in fp32. Allowing one unit 2^-23 of the sum
 of the products' magnitudes per K step and per partial sum: (K / 128 + 8) 2^-23 sum |x| |w|;
 then the rounding to the output type, eps / 2 relative."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -309,3 +311,33 @@ def test_few_scales_of_a_wide_product(rows, values):
                               out_dtype=torch.float32, weight_format=rp.WEIGHTS_PACKED if packed else rp.WEIGHTS_ND)
         torch.cuda.synchronize()
         check(got, xv, wv, [0, rows], torch.float32)
+
+
+def uses_tiles(rows, groups, n, k, packed=False):
+    """The many-rows kernel is what keeps x's codes in a workspace. (Codes take it from half the size on.)"""
+    b = ctypes.c_size_t()
+    assert rp.load().moe_mxfp4_matmul_workspace_size(rows, groups, n, k, 2, int(packed), ctypes.byref(b)) == 0
+    return b.value > 0
+
+
+def test_rows_outside_the_groups_are_not_quantised():
+    """Rows before the first group and behind the last take no part: x holds NaN there and the
+    workspace keeps, but for the codes and scales of the rows inside, what was in it."""
+    rows, groups, n, k = 5000, 6, 2048, 512
+    lo, hi = 700, 1500
+    assert uses_tiles(rows, groups, n, k)
+    wc, ws, wv = drawn(groups, n, k, seed=3)
+    off = [lo, 800, 800, 1100, 1101, 1300, hi]
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        say(f"mxfp4_matmul rows outside {dtype}")
+        x = torch.randn((rows, k), generator=torch.Generator().manual_seed(1)).to(dtype)
+        xv = fp4(x[lo:hi].double().numpy())[2]
+        x[:lo] = float("nan")
+        x[hi:] = float("nan")
+        area = torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device=DEV)
+        out = torch.full((rows, n), 7.0, device=DEV)
+        rp.mxfp4_matmul(x.to(DEV), to_dev(wc), to_dev(ws), group_offsets=torch.tensor(off, dtype=torch.int32, device=DEV),
+                        out=out, workspace=area)
+        check(out[lo:hi], xv, wv, [o - lo for o in off], torch.float32)
+        assert bool((out[:lo] == 7).all()) and bool((out[hi:] == 7).all())
+        assert int((area != 0xA5).sum()) <= (hi - lo) * (k // 2 + k // 32)
