@@ -341,3 +341,107 @@ def test_rows_outside_the_groups_are_not_quantised():
         check(out[lo:hi], xv, wv, [o - lo for o in off], torch.float32)
         assert bool((out[:lo] == 7).all()) and bool((out[hi:] == 7).all())
         assert int((area != 0xA5).sum()) <= (hi - lo) * (k // 2 + k // 32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_tiles_quantisation_of_every_16_bit_value(dtype):
+    """x against identity weights on the many-rows kernel, as test_quantisation_of_every_bf16_value:
+    every finite value of a 16-bit type, also given as fp32, in random groups and in groups of
+    neighbouring magnitudes; and against the codes of mx_quantize, bit for bit."""
+    k, n = 256, 8192
+    bits = np.arange(65536, dtype=np.uint32).astype(np.uint16)
+    value = torch.from_numpy(bits.astype(np.int16)).view(dtype)
+    bits = bits[torch.isfinite(value.float()).numpy()]
+    w = np.zeros((1, n, k), dtype=np.uint8)
+    w[0, np.arange(n), np.arange(n) % k] = 2
+    wc, ws = to_dev(mxfp.pack_fp4(w)), torch.full((1, n, k // 32), 127, dtype=torch.uint8, device=DEV)
+    for order in ("random", "sorted"):
+        b = np.random.default_rng(1).permutation(bits)
+        if order == "sorted":
+            b = bits[np.argsort(bits & 0x7fff, kind="stable")]
+        b = np.concatenate([b, np.zeros((-b.size) % k, np.uint16)]).reshape(-1, k)
+        x = torch.from_numpy(b.astype(np.int16)).view(dtype)
+        x = torch.cat([x, x])   # rows enough for tiles
+        assert uses_tiles(x.shape[0], 1, n, k)
+        c, s = mxfp.quantize(x.double().numpy(), "e2m1")
+        want = mxfp.dequantize(c, s, "e2m1")
+        normal = np.abs(want) >= 2.0 ** -126
+        for given in (dtype, torch.float32):
+            say(f"mxfp4_matmul tiles, every {dtype} value as {given}, {order}")
+            xd = x.to(given).to(DEV)
+            got = rp.mxfp4_matmul(xd, wc, ws, out_dtype=torch.float32)
+            codes, scales = rp.mx_quantize(xd, rp.QUANT_MXFP4)
+            same = rp.mxfp4_matmul(codes, wc, ws, x_scales=scales, out_dtype=torch.float32)
+            assert torch.equal(got, same)
+            for part in (got[:, :k], got[:, -k:]):
+                part = part.cpu().double().numpy()
+                assert np.array_equal(part[normal], want[normal])
+                assert np.all(np.abs(part[~normal]) <= 2.0 ** -126)
+
+
+@pytest.mark.parametrize("rows,groups,n,k", [(520, 1, 8192, 640), (900, 40, 2064, 512), (2100, 3, 2064, 1408)])
+def test_tiles_same_result_as_codes(rows, groups, n, k):
+    """x quantised in the call gives the bits of the product of mx_quantize's codes (tiles of more
+    than one size), with the workspace of the call or a given one, whatever that holds."""
+    assert uses_tiles(rows, groups, n, k) and uses_tiles(rows, groups, n, k, packed=True)
+    wc, ws, _ = drawn(groups, n, k, seed=rows)
+    w, s = to_dev(wc), to_dev(ws)
+    off = [0, rows] if groups == 1 else scattered(rows, groups, np.random.default_rng(0), 0)
+    off = torch.tensor(off, dtype=torch.int32, device=DEV)
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        say(f"mxfp4_matmul tiles against codes rows={rows} groups={groups} {dtype}")
+        x = torch.randn((rows, k), generator=torch.Generator().manual_seed(rows)).to(dtype).to(DEV)
+        codes, scales = rp.mx_quantize(x, rp.QUANT_MXFP4)
+        want = rp.mxfp4_matmul(codes, w, s, x_scales=scales, group_offsets=off, out_dtype=torch.float32)
+        assert bool((want != 0).any(dim=1).all())
+        area = torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device=DEV)
+        for kw in (dict(), dict(workspace=area), dict(workspace=area)):
+            assert torch.equal(want, rp.mxfp4_matmul(x, w, s, group_offsets=off, out_dtype=torch.float32, **kw))
+
+
+def test_tiles_captured_and_replayed_on_two_streams():
+    """Two captured graphs whose calls quantise into workspaces of their own, replayed in turn on
+    changed inputs with eager calls between, and calls on another stream at the same time."""
+    n, k = 2064, 640
+    held = []
+    for rows, dtype, packed in [(700, torch.float32, False), (1500, torch.bfloat16, True)]:
+        assert uses_tiles(rows, 3, n, k, packed)
+        wc, ws, _ = drawn(3, n, k, seed=rows)
+        w, s = to_dev(wc), to_dev(ws)
+        if packed:
+            w, s = rp.pack_weights(w, s, fp4=True)
+        kw = dict(group_offsets=torch.tensor([0, rows // 4, rows // 4, rows], dtype=torch.int32, device=DEV),
+                  weight_format=rp.WEIGHTS_PACKED if packed else rp.WEIGHTS_ND)
+        x = torch.randn((rows, k), device=DEV).to(dtype)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            first = [rp.mxfp4_matmul(x, w, s, **kw) for _ in range(3)]
+        second = [rp.mxfp4_matmul(x, w, s, **kw) for _ in range(3)]
+        torch.cuda.current_stream().wait_stream(side)
+        for a in first + second:
+            assert torch.equal(a, first[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = rp.mxfp4_matmul(x, w, s, **kw)
+        held.append((graph, x, w, s, kw, out))
+    for _ in range(4):
+        for graph, x, *_ in held:
+            x.copy_(torch.randn_like(x))
+            graph.replay()
+        eager = [rp.mxfp4_matmul(x, w, s, **kw) for _, x, w, s, kw, _ in held]
+        torch.cuda.synchronize()
+        for (*_, out), want in zip(held, eager):
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows,groups,n,k", [
+    (2048, 8, 4096, 384), (2000, 8, 4096, 128),   # tiles of 128 rows, groups of more: weights read more than once
+    (4096, 1, 3600, 256),                         # one dense group, the last channel block partly filled
+    (70, 1, 16384, 1024), (190, 3, 16400, 512)])    # dense and grouped, tiles of 64
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+def test_tiles_with_weights_read_more_than_once(rows, groups, n, k, kind):
+    dtype, out_dtype, packed = KINDS[kind]
+    assert uses_tiles(rows, groups, n, k, packed)
+    off = None if groups == 1 else scattered(rows, groups, np.random.default_rng(kind), 0)
+    product(rows, groups, n, k, off, dtype, out_dtype, packed, seed=kind)
