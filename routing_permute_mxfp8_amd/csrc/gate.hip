@@ -1257,14 +1257,19 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate16_backward_kernel(con
   }
 }
 
-// V = experts a lane: the smallest power of two with 64 V >= E.
+// V = experts a lane: the smallest power of two with 64 V >= E. The loss and the gradient come
+// here above 256 experts only (with_wide), the gate also for what its 16 lanes cannot do.
+template <typename F>
+hipError_t with_wide(int E, F&& f) {
+  if (E <= 512) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
+}
 template <typename F>
 hipError_t with_width(int E, F&& f) {
   if (E <= 64) return f(std::integral_constant<int, 1>{});
   if (E <= 128) return f(std::integral_constant<int, 2>{});
   if (E <= 256) return f(std::integral_constant<int, 4>{});
-  if (E <= 512) return f(std::integral_constant<int, 8>{});
-  return f(std::integral_constant<int, 16>{});
+  return with_wide(E, f);
 }
 // Experts a lane of the kernels with 16 lanes a row (up to 256 experts).
 constexpr int kMost16 = 256;
@@ -1391,7 +1396,7 @@ hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
         const bool vec = wide_rows<T>(p.logits, p.experts, kPiece<T, V>);
         return p.sigmoid ? go(balance16_sums_kernel<T, V, false>, vec, 0) : go(balance16_sums_kernel<T, V, true>, vec, 0);
       });
-    return with_width(p.experts, [&](auto w) {
+    return with_wide(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
       const bool vec = wide_rows<T>(p.logits, p.experts, V);
       const size_t lds = (sizeof(double) * kRowsPerBlock + sizeof(int)) * p.experts;
@@ -1436,7 +1441,7 @@ hipError_t launch_gate_backward(const GateGradParams& p, hipStream_t stream) {
         };
         return p.sigmoid ? go(gate16_backward_kernel<T, V, false>) : go(gate16_backward_kernel<T, V, true>);
       });
-    return with_width(p.experts, [&](auto w) {
+    return with_wide(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
       a.vec = wide_rows<T>(p.logits, p.experts, V);
       const size_t lds = sizeof(float) * kRowsPerBlock * 64 * V;
