@@ -83,7 +83,6 @@ struct TileArgs {
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 1024;
 constexpr int kList = 64;   // items described at a time
-constexpr int kSlots = 4;         // K steps staged in LDS
 
 // WC waves along the channels, 4 / WC along the rows; CB x RB 32 x 32 blocks a wave; BLOCKS
 // blocks a CU.
@@ -94,8 +93,9 @@ struct TileShape {
   static constexpr int kPair = kA + kB;
   static constexpr int kSA = kNT * 16, kSB = kMT * 16;  // bytes of a quad's scales
   static constexpr int kQuad = kSA + kSB;
-  static constexpr int kScales = 2 * kPair, kEnds = kScales + 2 * kQuad, kItems = kEnds + 4 * kMaxGroups;
-  static constexpr int kLds = kItems + 16 * kList;
+  // the area behind the two pairs: scales, tile ends of the groups, item list
+  static constexpr int kScales = 0, kEnds = kScales + 2 * kQuad, kItems = kEnds + 4 * kMaxGroups;
+  static constexpr int kLds = 2 * kPair + kItems + 16 * kList;
   static constexpr int kLA = kNT / 32, kLB = kMT / 32;   // direct-to-LDS loads a wave and pair (8 rows each)
   static_assert(kLds * BLOCKS <= 160 * 1024, "LDS of a compute unit");
   static_assert(kMT <= kThreads && kNT <= kThreads, "a thread loads a row's scales");
@@ -185,12 +185,13 @@ __device__ __forceinline__ void swap_rows(u32x4& a, u32x4& b) {
   }
 }
 
-// The body gets the LDS area twice, as two restrict pointers: one for the direct-to-LDS
-// loads, one for every other access. The compiler then does not make each LDS read wait for
-// every direct-to-LDS load in flight; slot_barrier orders them.
+// The body gets the two pairs of steps staged in LDS and the rest of it as three restrict
+// pointers, which is what they are: apart. A pair is never read while loads into it are in
+// flight (slot_barrier lies between), and so the compiler, which makes an LDS read wait for the
+// direct-to-LDS loads that may write there, has nothing to wait for.
 template <int WC, int CB, int RB, int BLOCKS, bool ONCE, typename O, bool PACKED>
-__device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out, uint8_t* __restrict__ dma,
-                                          uint8_t* __restrict__ lds) {
+__device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out, uint8_t* __restrict__ pair0,
+                                          uint8_t* __restrict__ pair1, uint8_t* __restrict__ lds) {
   using S = TileShape<WC, CB, RB, BLOCKS>;
   constexpr int MT = S::kMT, kNT = S::kNT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -260,8 +261,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   // offset, not of the scalar one, because only that is checked against the buffer's size.
   // ONCE: a weight is used by about one item, so weights are loaded non-temporal.
   constexpr int kCodes = S::kLA + S::kLB;   // loads of a pair
-  auto issue = [&](int slot, int step, bool in, int i) {   // load i of the pair
-    uint8_t* base = dma + slot * S::kPair;
+  auto issue = [&](int slot, int step, bool in, int i) {   // load i of the pair (slot: a constant)
+    uint8_t* base = slot ? pair1 : pair0;
     const int s = in ? step : 0;
     if (i < S::kLA)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(bw, in ? wbytes : 0),
@@ -336,8 +337,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, O* __restrict__ out
   const int read0 = (lane & 31) * 128 + ((h ^ ((lane >> 1) & 7)) * 16);
   u32x4 a[2][CB], bx_[2][RB];
   uint32_t read_s[CB + RB], sc[CB + RB];
-  auto read_step = [&](int j, int s, int i) {   // operand i of sub-step s of step j
-    const uint8_t* base = lds + (j >> 1) * S::kPair + (read0 ^ (32 * s) ^ (64 * (j & 1)));
+  auto read_step = [&](int j, int s, int i) {   // operand i of sub-step s of step j (a constant)
+    const uint8_t* base = (j >> 1 ? pair1 : pair0) + (read0 ^ (32 * s) ^ (64 * (j & 1)));
     if (i < CB)
       a[s][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 4096);
     else
@@ -511,7 +512,8 @@ template <int WC, int CB, int RB, int BLOCKS, bool ONCE, typename O, bool PACKED
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BLOCKS))) void fp4_tile_kernel(
     TileArgs p, O* __restrict__ out) {
   extern __shared__ __align__(16) uint8_t lds_area[];
-  tile_body<WC, CB, RB, BLOCKS, ONCE, O, PACKED>(p, out, lds_area, lds_area);
+  constexpr int kPair = TileShape<WC, CB, RB, BLOCKS>::kPair;
+  tile_body<WC, CB, RB, BLOCKS, ONCE, O, PACKED>(p, out, lds_area, lds_area + kPair, lds_area + 2 * kPair);
 }
 
 // The device's compute units, rounded up to whole XCDs' shares; the kernel's LDS size set
