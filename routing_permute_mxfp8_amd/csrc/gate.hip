@@ -734,10 +734,14 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
     const T* __restrict__ logits, int64_t rows, int E, bool vec, const int32_t* __restrict__ ids, int k,
     const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, float* __restrict__ sums,
     int32_t* __restrict__ counts, int32_t* __restrict__ held, unsigned* __restrict__ done) {
-  extern __shared__ double lds_sums[];   // [waves][E] sums, then [E] counts
+  // [waves] sums, then [E] counts; a lane's V sums lie V + 1 apart from the next lane's, so that
+  // the lanes meet different banks (8192 x 1024, with V: 23.5 us, with V + 1: 21.3)
+  extern __shared__ double lds_sums[];
+  constexpr int kSums = 64 * (V + 1);
+  const auto place = [](int e) { return e / V * (V + 1) + e % V; };
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int* hist = reinterpret_cast<int*>(lds_sums + kRowsPerBlock * E);
+  int* hist = reinterpret_cast<int*>(lds_sums + kRowsPerBlock * kSums);
   const int b = blockIdx.y, splits = gridDim.x, s = blockIdx.x;
   if (threadIdx.x == 0 && s == 0 && b == 0) *done = 0;
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
@@ -752,7 +756,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (lane * V + v < E) {
-        double& sum = lds_sums[wave * E + lane * V + v];
+        double& sum = lds_sums[wave * kSums + lane * (V + 1) + v];
         sum = (joined ? sum : 0.0) + (double)acc[v];
       }
       acc[v] = 0.0f;
@@ -794,7 +798,7 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void balance_sums_kernel(
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     double t = 0.0;
 #pragma unroll
-    for (int w = 0; w < kRowsPerBlock; ++w) t += lds_sums[w * E + e];
+    for (int w = 0; w < kRowsPerBlock; ++w) t += lds_sums[w * kSums + place(e)];
     sums[part * E + e] = (float)t;
     counts[part * E + e] = hist[e];
   }
@@ -1399,7 +1403,7 @@ hipError_t launch_balance(const BalanceParams& p, hipStream_t stream) {
     return with_wide(p.experts, [&](auto w) {
       constexpr int V = decltype(w)::value;
       const bool vec = wide_rows<T>(p.logits, p.experts, V);
-      const size_t lds = (sizeof(double) * kRowsPerBlock + sizeof(int)) * p.experts;
+      const size_t lds = sizeof(double) * kRowsPerBlock * 64 * (V + 1) + sizeof(int) * p.experts;
       return p.sigmoid ? go(balance_sums_kernel<T, V, false>, vec, lds) : go(balance_sums_kernel<T, V, true>, vec, lds);
     });
   });
