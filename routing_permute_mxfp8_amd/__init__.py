@@ -592,7 +592,8 @@ def gate_topk(logits, k: int, *, scoring: int = GATE_SOFTMAX, bias=None, num_gro
     topk_groups best of num_groups equal groups of neighbouring experts (by the sum of their two
     best ranks) take part. The ids come in descending order of rank, ties by the lowest index.
     renormalize: the weights of a row sum to `scale` (else they are scale * score). A logit of
-    -inf or NaN takes its expert out (score 0, chosen last)."""
+    -inf or NaN takes its expert out (score 0, chosen last). The weights carry no autograd
+    history: gate_backward gives the logits' gradient."""
     lib = load()
     n, e = _gate_logits(logits)
     index = _device_of(logits, bias=bias)

@@ -23,8 +23,10 @@ namespace {
 // K steps (a pair is one 128-byte line of a weight row) and add their sums in LDS at the
 // end, so that a dense layer of a few thousand channels still fills the chip. Loads behind
 // the last K step or the group's rows fall outside their buffers: zeros, no traffic.
-// Measured: one bf16 row, 7168 x 4096: 7.7 us (15.6 MB, 2 TB/s: the launch and two or three
-// memory latencies); at 59 MB 22 us, 2.7 TB/s. Beyond that the LDS-tiled kernel takes over.
+// Measured: one bf16 row, 7168 x 4096: 8.0 us (15.6 MB, 2 TB/s: the launch and the rounds of a
+// wave's loop, which loads its four K steps, waits for them and multiplies with nothing in flight);
+// x 16384 24.7 us (62 MB, 2.5 TB/s; packed weights 18.1). Beyond that the LDS-tiled kernel takes
+// over.
 struct RowsArgs {
   const void* x;            // codes [rows, K/2], or values [rows, K]
   const uint8_t* xs;        // codes: scales [rows, K/32]
@@ -191,6 +193,14 @@ hipError_t launch_out(const Fp4MatmulParams& p, hipStream_t stream) {
 // average its weights are read about once, non-temporal (tiles of 64, 40 rows each: 201 us, 212
 // cached; of 128, 96 rows: 214, 245; of 256, 160 rows: 253, 281; but of 128, 160 rows: 414, 399,
 // and of 256, 256 rows of 2048 x 7168: 140, 136).
+//
+// Limits of the rule: it was fitted on dense calls and groups of about even sizes of 7168 x 4096,
+// 2048 x 7168 and 1408 x 2000, and sees `rows`, not the offsets (these are on the device): where
+// rows outside the groups or a few large groups make the average a poor guide, the tile is larger
+// or smaller than it should be, and tiles of 32 are non-temporal also for a group that needs many.
+// The kernel above takes 16 rows after one another on a block of 16 or 64 channels, which the
+// bytes do not show: many rows by few channels are slow (32768 rows, 128 to 64: 1170 us; 1024,
+// 8192 to 64: 522; 4096, 1024 to 128: 342).
 int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool values) {
   if (rows <= 0) return 0;
   if (rows * (k / 32) < 16) return 0;   // (it reads x's scales 16 bytes at a time, also at their end)

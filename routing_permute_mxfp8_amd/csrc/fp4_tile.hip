@@ -26,12 +26,16 @@
 // direct-to-LDS loads write linearly; their lanes fetch the chunk that belongs at their place,
 // wherever the weight format has it.
 //
-// Measured: 256 rows on 64 experts of 4096 x 7168 (1.0 GB of weights): 155 us, 6.4 TB/s of the
-// 7.1 that a read reaches here. 32768 rows on 16 of them: 530 us, 3.6 PFLOP/s; these MFMAs
-// alone reach 6.5 with random operands, with this kernel's LDS reads and loads dealt between
-// them 5.4 to 5.9, at clocks that power holds at 1.6 to 1.9 GHz; the rest is the stores at an
-// item's end (9,000 cycles of some 75,000), when a compute unit's one block multiplies nothing,
-// and bursts of loads. 8192 rows on 32 of 7168 x 2048: 120 us, a third of it those stores.
+// Measured: 256 rows on 64 experts of 4096 x 7168 (1.0 GB of weights): 154 us, 6.4 TB/s of the
+// 7.1 that a read reaches here. 32768 rows on 16 of them: 530 to 550 us, 3.5 to 3.6 PFLOP/s; these
+// MFMAs alone reach 6.5 with random operands, with this kernel's LDS reads and loads dealt between
+// them 5.4 to 5.9, at clocks that power holds at 1.6 to 1.9 GHz. That is nine rounds of some 2170
+// items over 256 blocks, 94,000 to 112,000 cycles each: 57,000 of MFMAs (busy 42 to 45 % of all
+// cycles by the counters), some 9,000 issuing an item's stores, when a compute unit's one block
+// multiplies nothing. The rest is not accounted for stamp by stamp; known parts are the last round,
+// half full, bursts of loads, and the first barrier of an item, which waits for every store of the
+// item before (vmcnt counts stores too). 8192 rows on 32 of 7168 x 2048: 118 us; groups of about a
+// tile leave half of the second tiles nearly empty, and its stores take a third.
 
 #include <algorithm>
 #include <map>
@@ -51,7 +55,8 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // One thread per group of 32 of the rows that belong to an expert group, [off[0], off[groups])
 // (the others' are not read, and no tile uses their codes); row-major codes [rows, K/2] and
 // scales [rows, K/32].
-// Bound by the stream: 8192 x 2048 bf16 (42 MB) in 8.8 us, 4.8 TB/s.
+// Bound by the stream and, before it, the offsets' load: 8192 x 2048 bf16 (42 MB) in 10.3 us
+// (8.7 for all rows without offsets; the call takes the same 132 us with either).
 template <typename X>
 __global__ __launch_bounds__(256) void fp4_quantise_kernel(const X* __restrict__ x, int64_t rows, int per_row,
                                                            const int32_t* __restrict__ off, int groups,

@@ -25,8 +25,9 @@
 // lanes instead, four rows a wave (see there): more of a row's values in one lane, fewer
 // exchanges. Kernel times, one wave per row and 16 lanes, E = 256:
 //   gate 8192 fp32 softmax 10.3, 5.7 us; 32768 bf16 sigmoid in 8 groups 55, 19;
-//   loss 32768 fp32, first pass 60, 13.6 (34 MB); gradient 32768 fp32 23.3, 15.5 (70 MB, 4.5 TB/s).
-// One wave per row at 8192 x 512 fp32: gate 21, in groups 43, loss's first pass 8, gradient 19.
+//   loss 32768 fp32, first pass 60, 12.6 (34 MB); gradient 32768 fp32 23.3, 15.6 (70 MB, 4.5 TB/s).
+// One wave per row at 8192 x 512 fp32: gate 21, with bias and groups 42, loss 17 (both passes),
+// gradient 21.
 // Bound: small calls by the launch, the gate by its instructions, the other two by the stream
 // and the latency of few rows a wave.
 
@@ -366,7 +367,9 @@ __global__ __launch_bounds__(64 * kRowsPerBlock) void gate_kernel(const T* __res
 // their errors by ranks in 64 bits. What stays open, a tenth that near to the K-th or two
 // groups that near at the border (a few rows of ten thousand), is decided row by row by
 // the whole wave: deciding every near row so took 20 of 34 us at 32768 x 256 in groups, a row of
-// a thousand still 9 of 25 (a wave's 8 us at the end of the launch); it is 22 now.
+// a thousand still 9 of 25 (a wave's 8 us at the end of the launch); it is 22 now. So is, although
+// its order is plain, a row of fp32 logits or with a bias that has eight live experts or fewer of
+// more (8192 such rows of 256: 18 us, others 6).
 constexpr int kTop = 8;
 
 __device__ __forceinline__ uint32_t order_key(float r, int e) {
@@ -1376,8 +1379,11 @@ hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   });
 }
 
-// Shares of a sequence's rows: enough blocks over all sequences to fill the chip twice,
-// of at least 16 rows on average.
+// Shares of a sequence's rows, the same number for every sequence: enough blocks over all
+// sequences for four a compute unit, of 16 rows and more of an average sequence (17 rows are two
+// shares). (So a long sequence among many short ones is read by few blocks, and the second pass counts the rows
+// of all sequences in every block: one of 30,000 rows among 512, 256 experts, 820 us; among 1024
+// 1,630; 4096 sequences of 8 rows 383; the same rows as one sequence 21.)
 int balance_splits(int64_t rows, int64_t seqs) {
   const int64_t per = std::max<int64_t>(1, rows / std::max<int64_t>(seqs, 1));
   return (int)std::max<int64_t>(1, std::min<int64_t>((1024 + seqs - 1) / seqs, (per + 15) / 16));
