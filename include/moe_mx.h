@@ -491,6 +491,71 @@ moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales,
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* moe_rms_norm: the root-mean-square norm in front of a layer, of the sum of a    */
+/* row and its residual, with the normed row's MX codes:                            */
+/*   h = T(x + residual)      T: dtype (FP32, FP16 or BF16); residual NULL: h = x     */
+/*   rstd = (sum_c h_c^2 / cols + eps)^(-1/2)      (the squares summed in 64 bits)     */
+/*   y = T(h rstd weight)     in fp32, rounded once                                    */
+/*   codes, scales = what moe_mx_quantize(y, quant_mode) makes of it, byte for byte     */
+/*   x, residual, y, h  device, [rows, cols] of dtype. y may be NULL where quant_mode     */
+/*                asks for codes; h is written with a residual and may be NULL without one  */
+/*   weight       device, [cols] of weight_dtype: dtype or FP32                             */
+/*   eps          positive and finite                                                        */
+/*   rstd         device, fp32 [rows]                                                         */
+/*   quant_mode   -1 (codes, scales unused), 2, 3 or 9, the MOE_QUANT_* values: codes             */
+/*                uint8 [rows, cols] ([rows, cols / 2] for MXFP4), scales uint8 [rows,           */
+/*                moe_mx_scale_cols(cols)], cols % 32 == 0 (finite y, as there)                   */
+/* moe_rms_norm_backward: with a = grad_y weight and xh = h rstd (h, rstd of that call)            */
+/*   grad_x = T(rstd (a - xh sum_c(a_c xh_c) / cols) + grad_h)                                      */
+/*   grad_weight = sum over the rows of grad_y xh, in fp32, in a fixed order                         */
+/*   grad_y, h, grad_h, grad_x  device, [rows, cols] of dtype; grad_h, the gradient of h from          */
+/*                elsewhere (the residual stream), may be NULL. grad_x is the gradient of x and of      */
+/*                the residual alike. It may be the same buffer as grad_y or grad_h.                     */
+/*   grad_weight  device, fp32 [cols]; zeros for rows = 0                                                 */
+/* Limits: rows in [0, MOE_MAX_FLAT_ROWS), cols in [1, MOE_NORM_MAX_COLS]; codes 8-byte aligned, the other   */
+/* tensors as their elements.                                                                               */
+/* ------------------------------------------------------------------------ */
+#define MOE_NORM_MAX_COLS 16384
+moe_status moe_rms_norm(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const void* weight,
+                        int weight_dtype, float eps, int quant_mode, void* y, void* h, float* rstd, uint8_t* codes,
+                        uint8_t* scales, void* stream);
+moe_status moe_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes /* host out */);
+moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* grad_h, int dtype, int64_t rows,
+                                 int64_t cols, const void* weight, int weight_dtype, const float* rstd, void* grad_x,
+                                 float* grad_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_grouped_matmul: the product of the 16-bit rows of each group with its weights    */
+/*   transpose_w 0: out[r, j] = sum_i x[r, i] w[g][j, i]    w device, [num_groups, n, k]  */
+/*   transpose_w 1: out[r, j] = sum_i x[r, i] w[g][i, j]    w device, [num_groups, k, n]   */
+/*   for the rows r of group g. With out = x w^T forward, the gradient by x is the call     */
+/*   of the gradient by out with the same w and transpose_w 1.                               */
+/* moe_grouped_matmul_wgrad: the gradient by w of that forward product                        */
+/*   out[g][j, i] = sum over the rows r of group g of grad_out[r, j] x[r, i]                   */
+/*   out device, [num_groups, n, k]; zeros for a group without rows                             */
+/*   x            device, [rows, k] of dtype; grad_out device, [rows, n] of dtype                */
+/*   dtype        FP16 or BF16, of both operands; out_dtype: the same or FP32. The products        */
+/*                are exact, added in fp32, and rounded to out_dtype once.                          */
+/*   group_offsets device, int32 [num_groups + 1], non-decreasing: the rows of group g are            */
+/*                [off[g], off[g+1]); empty groups are allowed; rows outside [off[0],                  */
+/*                off[num_groups]) take no part and their out rows are left as they were.               */
+/*                NULL: all rows are one group (num_groups must be 1).                                   */
+/* Limits: n and k in [1, 1048576]; num_groups in [1, 1024]; rows in [0, MOE_MAX_FLAT_ROWS). Any          */
+/* sizes and element-aligned addresses are taken; n and k that are multiples of 8 and 16-byte              */
+/* aligned tensors are much faster. out must not overlap an operand.                                        */
+/* ------------------------------------------------------------------------ */
+moe_status moe_grouped_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int transpose_w,
+                                             size_t* bytes /* host out */);
+moe_status moe_grouped_matmul(const void* x, int dtype, int64_t rows, const int32_t* group_offsets, int64_t num_groups,
+                              const void* w, int transpose_w, int64_t n, int64_t k, void* out, int out_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+moe_status moe_grouped_matmul_wgrad_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k,
+                                                   size_t* bytes /* host out */);
+moe_status moe_grouped_matmul_wgrad(const void* grad_out, const void* x, int dtype, int64_t rows,
+                                    const int32_t* group_offsets, int64_t num_groups, int64_t n, int64_t k, void* out,
+                                    int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Measured peaks for the roofline report (one launch each; the caller times   */
 /* it with events on `stream`).                                                */
 /* moe_probe_stream: mode 0 reads `bytes` from src (dst receives nothing      */

@@ -17,7 +17,8 @@ with it. The oracle is written from the operator pages:
   (active expert range, rowIdxType, expertTokensNumType).
 
 The router (gate.py: top-K gate, load-balance loss, their gradient) is on none of
-these pages; it is written from the formulas in its docstrings. Parity unpinned.
+these pages; it is written from the formulas in its docstrings. Parity unpinned. The
+same holds for the norm and the 16-bit products of expert groups (dense.py).
 
 Floating point is float64 throughout unless a step fixes another precision;
 where a reading of the pages had to be chosen it is named in the function's

@@ -28,6 +28,7 @@ __all__ = [
     "pack_weights", "WEIGHTS_ND", "WEIGHTS_PACKED", "DTYPE_FP8_E5M2", "DTYPE_FP8_E4M3", "DTYPE_FP4_E2M1",
     "gate_topk", "balance_loss", "gate_backward", "GATE_SOFTMAX", "GATE_SIGMOID",
     "mxfp4_matmul",
+    "rms_norm", "rms_norm_backward", "grouped_matmul", "grouped_matmul_wgrad",
 ]
 
 QUANT_NONE, QUANT_E5M2, QUANT_E4M3, QUANT_MXFP4 = -1, 2, 3, 9
@@ -112,6 +113,13 @@ _SIGS = {
                            _VP, _VP, _VP], _INT),
     "moe_mxfp4_matmul_workspace_size": ([_I64, _I64, _I64, _I64, _INT, _INT, ctypes.POINTER(_SZ)], _INT),
     "moe_mxfp4_matmul": ([_VP, _INT, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _I64, _INT, _VP, _INT, _VP, _SZ, _VP], _INT),
+    "moe_rms_norm": ([_VP, _VP, _INT, _I64, _I64, _VP, _INT, ctypes.c_float, _INT, _VP, _VP, _VP, _VP, _VP, _VP], _INT),
+    "moe_rms_norm_backward_workspace_size": ([_I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "moe_rms_norm_backward": ([_VP, _VP, _VP, _INT, _I64, _I64, _VP, _INT, _VP, _VP, _VP, _VP, _SZ, _VP], _INT),
+    "moe_grouped_matmul_workspace_size": ([_I64, _I64, _I64, _I64, _INT, ctypes.POINTER(_SZ)], _INT),
+    "moe_grouped_matmul": ([_VP, _INT, _I64, _VP, _I64, _VP, _INT, _I64, _I64, _VP, _INT, _VP, _SZ, _VP], _INT),
+    "moe_grouped_matmul_wgrad_workspace_size": ([_I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "moe_grouped_matmul_wgrad": ([_VP, _VP, _INT, _I64, _VP, _I64, _I64, _I64, _VP, _INT, _VP, _SZ, _VP], _INT),
     "moe_probe_stream": ([_INT, _VP, _VP, _I64, _VP], _INT),
     "moe_probe_mfma": ([_INT, _VP, ctypes.POINTER(_I64), ctypes.POINTER(ctypes.c_double), _VP], _INT),
 }
@@ -722,6 +730,167 @@ def mxfp4_matmul(x, w, w_scales, *, x_scales=None, group_offsets=None, out_dtype
         _check(lib.moe_mxfp4_matmul(x.data_ptr(), xd, _raw(x_scales), rows, _raw(group_offsets), g, w.data_ptr(),
                                     w_scales.data_ptr(), n, k, weight_format, out.data_ptr(), _DT[out.dtype], _raw(ws),
                                     0 if ws is None else ws.numel(), _raw_stream(index)))
+    return out
+
+
+def _norm_rows(x, weight, **others):
+    """[rows, cols] of a norm's rows, after the checks of them, of the weight and of the other row matrices."""
+    if x.dim() != 2 or x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"rows must be float32, float16 or bfloat16 [rows, cols] (got {x.dtype} {tuple(x.shape)})")
+    if weight.dtype not in (x.dtype, torch.float32) or tuple(weight.shape) != (x.shape[1],):
+        raise ValueError(f"weight must be {x.dtype} or float32 [{x.shape[1]}] (got {weight.dtype} "
+                         f"{tuple(weight.shape)})")
+    for name, t in others.items():
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"{name} must be {x.dtype} {tuple(x.shape)} (got {t.dtype} {tuple(t.shape)})")
+    return x.shape
+
+
+def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant_mode: int = QUANT_NONE, want_y: bool = True):
+    """The norm in front of a layer: (y, h, rstd fp32 [N], codes, scales) of x [N, C] (fp32, fp16 or bf16).
+
+    h = x + residual in x's type, the residual of the next layer (x itself without a residual);
+    rstd = 1 / sqrt(mean(h^2) + eps); y = h rstd weight in x's type, what the router's product
+    reads. weight: [C] of x's type or fp32. codes, scales: with quant_mode QUANT_E4M3, QUANT_E5M2
+    or QUANT_MXFP4 the bytes that mx_quantize makes of y (uint8 [N, C], or [N, C/2] for MXFP4, and
+    [N, mx_scale_cols(C)]), as mega_moe, init_routing and mxfp4_matmul take them, else None.
+    want_y=False: y is not written (None), for a quantised layer whose router reads something
+    else. C <= 16384. The results carry no autograd history: rms_norm_backward takes h and rstd."""
+    lib = load()
+    n, c = _norm_rows(x, weight, residual=residual)
+    quant = quant_mode != QUANT_NONE
+    if not want_y and not quant:
+        raise ValueError("want_y=False needs a quant_mode")
+    index = _device_of(x, weight=weight, residual=residual)
+    dev = x.device
+    with _on(index):
+        y = torch.empty_like(x) if want_y else None
+        h = x if residual is None else torch.empty_like(x)
+        rstd = torch.empty((n,), dtype=torch.float32, device=dev)
+        codes = scales = None
+        if quant:
+            codes = torch.empty((n, c // 2 if quant_mode == QUANT_MXFP4 else c), dtype=torch.uint8, device=dev)
+            scales = torch.empty((n, (c + 63) // 64 * 2), dtype=torch.uint8, device=dev)
+        _check(lib.moe_rms_norm(x.data_ptr(), _raw(residual), _DT[x.dtype], n, c, weight.data_ptr(), _DT[weight.dtype],
+                                eps, quant_mode, _raw(y), h.data_ptr(), rstd.data_ptr(), _raw(codes), _raw(scales),
+                                _raw_stream(index)))
+    return y, h, rstd, codes, scales
+
+
+def rms_norm_backward(grad_y, h, weight, rstd, *, grad_h=None):
+    """The gradients of rms_norm: (grad_x [N, C] of h's type, grad_weight fp32 [C]) from grad_y
+    [N, C] and that call's h and rstd. grad_h: the gradient of h from elsewhere (the residual
+    stream), added to grad_x, which is the gradient of x and of the residual alike."""
+    lib = load()
+    n, c = _norm_rows(h, weight, grad_y=grad_y, grad_h=grad_h)
+    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (n,):
+        raise ValueError(f"rstd must be float32 [{n}] (got {rstd.dtype} {tuple(rstd.shape)})")
+    index = _device_of(h, grad_y=grad_y, weight=weight, rstd=rstd, grad_h=grad_h)
+    nbytes = _sized("moe_rms_norm_backward_workspace_size", n, c)
+    with _on(index):
+        grad_x = torch.empty_like(h)
+        grad_weight = torch.empty((c,), dtype=torch.float32, device=h.device)
+        ws = _workspace(nbytes, h.device)
+        _check(lib.moe_rms_norm_backward(grad_y.data_ptr(), h.data_ptr(), _raw(grad_h), _DT[h.dtype], n, c,
+                                         weight.data_ptr(), _DT[weight.dtype], rstd.data_ptr(), grad_x.data_ptr(),
+                                         grad_weight.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(index)))
+    return grad_x, grad_weight
+
+
+def _group_count(group_offsets):
+    if group_offsets is None:
+        return 1
+    if group_offsets.dtype != torch.int32 or group_offsets.dim() != 1 or group_offsets.numel() < 2:
+        raise ValueError(f"group_offsets must be int32 [groups + 1] (got {group_offsets.dtype} "
+                         f"{tuple(group_offsets.shape)})")
+    return group_offsets.numel() - 1
+
+
+def _gmm16_out(out, shape, dtype, out_dtype):
+    """The output's type, after the checks of `out` or of out_dtype."""
+    if out is None:
+        od = dtype if out_dtype is None else out_dtype
+        if od not in (dtype, torch.float32):
+            raise ValueError(f"out_dtype must be {dtype} or float32 (got {out_dtype})")
+        return od
+    if out.dtype not in (dtype, torch.float32) or tuple(out.shape) != shape or out_dtype not in (None, out.dtype):
+        raise ValueError(f"out must be {dtype if out_dtype is None else out_dtype} or float32 {list(shape)} "
+                         f"(got {out.dtype} {tuple(out.shape)})")
+    return out.dtype
+
+
+def grouped_matmul(x, w, group_offsets=None, *, transpose_w: bool = False, out_dtype=None, out=None, workspace=None):
+    """16-bit product of expert groups: out [R, N], out[r] = x[r] w[g]^T for the rows r of group g.
+
+    x: bf16 or fp16 [R, K]. w: [G, N, K] of x's type; with transpose_w [G, K, N], out[r] = x[r] w[g]:
+    grad_x of a forward call is grouped_matmul(grad_out, w, group_offsets, transpose_w=True) with
+    the same w. Without group_offsets (one group) w may be 2-D. group_offsets: int32 [G + 1], the
+    rows of group g are [off[g], off[g + 1]); rows outside all groups are left as they were in
+    `out` (uninitialised when out is None). out_dtype: x's (the default) or fp32; the sums are
+    fp32. workspace: optional preallocated uint8 device tensor. The result carries no autograd
+    history."""
+    lib = load()
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x must be float16 or bfloat16 [rows, k] (got {x.dtype} {tuple(x.shape)})")
+    if w.dim() == 2 and group_offsets is None:
+        w = w.unsqueeze(0)
+    if w.dim() != 3 or w.dtype != x.dtype:
+        raise ValueError(f"w must be {x.dtype} [groups, n, k] (got {w.dtype} {tuple(w.shape)})")
+    rows, k = x.shape
+    g = w.shape[0]
+    n, wk = (w.shape[2], w.shape[1]) if transpose_w else (w.shape[1], w.shape[2])
+    if wk != k:
+        raise ValueError(f"x has k = {k}, w has k = {wk}")
+    if group_offsets is None and g != 1:
+        raise ValueError(f"{g} groups need group_offsets")
+    if group_offsets is not None and _group_count(group_offsets) != g:
+        raise ValueError(f"group_offsets must be int32 [{g + 1}] (got {tuple(group_offsets.shape)})")
+    od = _gmm16_out(out, (rows, n), x.dtype, out_dtype)
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be uint8 (got {workspace.dtype})")
+    index = _device_of(x, w=w, group_offsets=group_offsets, out=out, workspace=workspace)
+    nbytes = _sized("moe_grouped_matmul_workspace_size", rows, g, n, k, int(bool(transpose_w)))
+    with _on(index):
+        if out is None:
+            out = torch.empty((rows, n), dtype=od, device=x.device)
+        ws = workspace
+        if nbytes and (ws is None or ws.numel() < nbytes):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        _check(lib.moe_grouped_matmul(x.data_ptr(), _DT[x.dtype], rows, _raw(group_offsets), g, w.data_ptr(),
+                                      int(bool(transpose_w)), n, k, out.data_ptr(), _DT[od], _raw(ws),
+                                      0 if ws is None else ws.numel(), _raw_stream(index)))
+    return out
+
+
+def grouped_matmul_wgrad(grad_out, x, group_offsets=None, *, out_dtype=None, out=None, workspace=None):
+    """The gradient of grouped_matmul's w: [G, N, K], the sum over the rows r of group g of
+    grad_out[r]^T x[r], from grad_out [R, N] and x [R, K] (bf16 or fp16, both the same); zeros for
+    a group without rows. Without group_offsets: all rows, [N, K]. out_dtype: x's (the default) or
+    fp32. out, workspace: as in grouped_matmul."""
+    lib = load()
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x must be float16 or bfloat16 [rows, k] (got {x.dtype} {tuple(x.shape)})")
+    if grad_out.dim() != 2 or grad_out.dtype != x.dtype or grad_out.shape[0] != x.shape[0]:
+        raise ValueError(f"grad_out must be {x.dtype} [{x.shape[0]}, n] (got {grad_out.dtype} "
+                         f"{tuple(grad_out.shape)})")
+    g = _group_count(group_offsets)
+    rows, k = x.shape
+    n = grad_out.shape[1]
+    shape = (n, k) if group_offsets is None else (g, n, k)
+    od = _gmm16_out(out, shape, x.dtype, out_dtype)
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be uint8 (got {workspace.dtype})")
+    index = _device_of(x, grad_out=grad_out, group_offsets=group_offsets, out=out, workspace=workspace)
+    nbytes = _sized("moe_grouped_matmul_wgrad_workspace_size", rows, g, n, k)
+    with _on(index):
+        if out is None:
+            out = torch.empty(shape, dtype=od, device=x.device)
+        ws = workspace
+        if nbytes and (ws is None or ws.numel() < nbytes):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        _check(lib.moe_grouped_matmul_wgrad(grad_out.data_ptr(), x.data_ptr(), _DT[x.dtype], rows, _raw(group_offsets),
+                                            g, n, k, out.data_ptr(), _DT[od], _raw(ws), 0 if ws is None else ws.numel(),
+                                            _raw_stream(index)))
     return out
 
 

@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <string>
 
 #include "moe_mx.h"
@@ -466,6 +467,62 @@ moe::BalanceParams carve_balance(Carver& cv, int64_t rows, int64_t experts, int6
   p.shares = cv.take<double>((size_t)seqs * moe::balance_chunks((int)experts, p.splits));
   p.done = cv.take<unsigned>(1);
   return p;
+}
+
+bool misaligned(size_t to, std::initializer_list<const void*> ps) {
+  for (const void* q : ps)
+    if (reinterpret_cast<uintptr_t>(q) % to) return true;
+  return false;
+}
+
+moe_status check_norm(const char* who, int dtype, int64_t rows, int64_t cols, int weight_dtype) {
+  if (rows < 0 || rows >= MOE_MAX_FLAT_ROWS)
+    return fail(MOE_ERR_SHAPE, "%s: rows %lld outside [0, %d)", who, (long long)rows, MOE_MAX_FLAT_ROWS);
+  if (cols < 1 || cols > MOE_NORM_MAX_COLS)
+    return fail(MOE_ERR_SHAPE, "%s: cols %lld outside [1, %d]", who, (long long)cols, MOE_NORM_MAX_COLS);
+  if (!valid_x_dtype(dtype)) return fail(MOE_ERR_DTYPE, "%s: dtype %d not FP32/FP16/BF16", who, dtype);
+  if (weight_dtype != dtype && weight_dtype != MOE_DTYPE_FP32)
+    return fail(MOE_ERR_DTYPE, "%s: weight_dtype %d neither the rows' %d nor FP32", who, weight_dtype, dtype);
+  return MOE_OK;
+}
+
+moe_status check_gmm16(const char* who, int dtype, int out_dtype, int64_t rows, int64_t groups, int64_t n, int64_t k) {
+  if (rows < 0 || rows >= MOE_MAX_FLAT_ROWS)
+    return fail(MOE_ERR_SHAPE, "%s: rows %lld outside [0, %d)", who, (long long)rows, MOE_MAX_FLAT_ROWS);
+  if (groups < 1 || groups > 1024) return fail(MOE_ERR_SHAPE, "%s: num_groups %lld outside [1, 1024]", who, (long long)groups);
+  if (n < 1 || n > 1048576 || k < 1 || k > 1048576)
+    return fail(MOE_ERR_SHAPE, "%s: n %lld or k %lld outside [1, 1048576]", who, (long long)n, (long long)k);
+  if (dtype != MOE_DTYPE_FP16 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_DTYPE, "%s: dtype %d not FP16 or BF16", who, dtype);
+  if (out_dtype != dtype && out_dtype != MOE_DTYPE_FP32)
+    return fail(MOE_ERR_DTYPE, "%s: out_dtype %d neither the operands' %d nor FP32", who, out_dtype, dtype);
+  return MOE_OK;
+}
+
+moe::Gmm16Params gmm16_params(int dtype, int out_dtype, int64_t rows, const int32_t* off, int64_t groups, int64_t n,
+                              int64_t k) {
+  moe::Gmm16Params p;
+  p.half = dtype == MOE_DTYPE_FP16; p.out_fp32 = out_dtype == MOE_DTYPE_FP32; p.rows = rows; p.off = off;
+  p.groups = (int)groups; p.n = (int)n; p.k = (int)k;
+  return p;
+}
+
+void carve_gmm16(Carver&, moe::Gmm16Params&) {}
+
+moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!p.out || (p.rows > 0 && (!p.a || !p.b)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: both operands and out must be non-NULL", who);
+  if (misaligned(2, {p.a, p.b}) || misaligned(p.out_fp32 ? 4 : 2, {p.out}) || misaligned(4, {p.off}))
+    return fail(MOE_ERR_INVALID_ARG, "%s: tensors must be aligned to their elements", who);
+  Carver cv(nullptr);
+  carve_gmm16(cv, p);
+  if (cv.off > 0) {
+    if (moe_status s = check_ws(who, cv.off, workspace, workspace_bytes)) return s;
+    Carver wc(workspace);
+    carve_gmm16(wc, p);
+  }
+  hipError_t e = moe::launch_gmm16(p, stream);
+  if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s launch: %s", who, hipGetErrorString(e));
+  return ok();
 }
 
 }  // namespace
@@ -1113,6 +1170,118 @@ moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales,
   hipError_t e = moe::launch_fp4_matmul(p, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "moe_mxfp4_matmul launch");
   return ok();
+}
+
+// ---- root-mean-square norm -------------------------------------------------------------
+moe_status moe_rms_norm(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const void* weight,
+                        int weight_dtype, float eps, int quant_mode, void* y, void* h, float* rstd, uint8_t* codes,
+                        uint8_t* scales, void* stream) {
+  if (moe_status s = check_norm("moe_rms_norm", dtype, rows, cols, weight_dtype)) return s;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm: eps must be positive and finite");
+  if (quant_mode != MOE_QUANT_NONE && quant_mode != MOE_QUANT_MXFP8_E5M2 && quant_mode != MOE_QUANT_MXFP8_E4M3 &&
+      quant_mode != MOE_QUANT_MXFP4_E2M1)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_rms_norm: quant_mode %d not -1, 2, 3 or 9", quant_mode);
+  const bool quant = quant_mode != MOE_QUANT_NONE;
+  if (quant && cols % 32 != 0)
+    return fail(MOE_ERR_SHAPE, "moe_rms_norm: cols %lld must be a multiple of 32 to be quantised", (long long)cols);
+  if (rows == 0) return ok();
+  if (!x || !weight || !rstd || (!y && !quant) || (residual && !h) || (quant && (!codes || !scales)))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm: x, weight, rstd, y (or codes and scales) and, with a residual, h must be non-NULL");
+  const size_t sz = dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (misaligned(sz, {x, residual, y, h}) || misaligned(weight_dtype == MOE_DTYPE_FP32 ? 4 : 2, {weight}) ||
+      misaligned(4, {rstd}) || (quant && misaligned(8, {codes})))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm: tensors must be aligned to their elements, codes to 8 bytes");
+  moe::NormParams p;
+  p.x = x; p.residual = residual; p.weight = weight; p.dtype = dtype; p.weight_dtype = weight_dtype; p.rows = rows;
+  p.cols = (int)cols; p.eps = eps; p.y = y; p.h = h; p.rstd = rstd; p.codes = codes; p.scales = scales;
+  p.quant = !quant ? 0 : quant_mode == MOE_QUANT_MXFP8_E4M3 ? 1 : quant_mode == MOE_QUANT_MXFP8_E5M2 ? 2 : 3;
+  p.scale_cols = (int)scale_cols(cols);
+  hipError_t e = moe::launch_norm(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_rms_norm launch");
+  return ok();
+}
+
+moe_status moe_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm_backward_workspace_size: bytes is NULL");
+  if (moe_status s = check_norm("moe_rms_norm_backward", MOE_DTYPE_FP32, rows, cols, MOE_DTYPE_FP32)) return s;
+  Carver cv(nullptr);
+  cv.take<float>((size_t)moe::norm_parts(rows) * cols);
+  *bytes = cv.off;
+  return ok();
+}
+
+moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* grad_h, int dtype, int64_t rows,
+                                 int64_t cols, const void* weight, int weight_dtype, const float* rstd, void* grad_x,
+                                 float* grad_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  if (moe_status s = check_norm("moe_rms_norm_backward", dtype, rows, cols, weight_dtype)) return s;
+  if (!weight || !grad_weight || (rows > 0 && (!grad_y || !h || !rstd || !grad_x)))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm_backward: grad_y, h, weight, rstd, grad_x and grad_weight must be non-NULL");
+  const size_t sz = dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (misaligned(sz, {grad_y, h, grad_h, grad_x}) || misaligned(weight_dtype == MOE_DTYPE_FP32 ? 4 : 2, {weight}) ||
+      misaligned(4, {rstd, grad_weight}))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm_backward: tensors must be aligned to their elements");
+  moe::NormGradParams p;
+  p.parts = moe::norm_parts(rows);
+  Carver need(nullptr);
+  need.take<float>((size_t)p.parts * cols);
+  if (moe_status s = check_ws("moe_rms_norm_backward", need.off, workspace, workspace_bytes)) return s;
+  Carver cv(workspace);
+  p.part = cv.take<float>((size_t)p.parts * cols);
+  p.grad_y = grad_y; p.h = h; p.grad_h = grad_h; p.weight = weight; p.rstd = rstd; p.dtype = dtype;
+  p.weight_dtype = weight_dtype; p.rows = rows; p.cols = (int)cols; p.grad_x = grad_x; p.grad_w = grad_weight;
+  hipError_t e = moe::launch_norm_backward(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_rms_norm_backward launch");
+  return ok();
+}
+
+// ---- 16-bit grouped products -----------------------------------------------------------
+moe_status moe_grouped_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int transpose_w,
+                                             size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul_workspace_size: bytes is NULL");
+  if (moe_status s = check_gmm16("moe_grouped_matmul", MOE_DTYPE_BF16, MOE_DTYPE_BF16, rows, num_groups, n, k)) return s;
+  if (transpose_w != 0 && transpose_w != 1) return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul: transpose_w must be 0 or 1");
+  Carver cv(nullptr);
+  moe::Gmm16Params p = gmm16_params(MOE_DTYPE_BF16, MOE_DTYPE_FP32, rows, nullptr, num_groups, n, k);
+  p.trans = transpose_w != 0;
+  carve_gmm16(cv, p);
+  *bytes = cv.off;
+  return ok();
+}
+
+moe_status moe_grouped_matmul(const void* x, int dtype, int64_t rows, const int32_t* group_offsets, int64_t num_groups,
+                              const void* w, int transpose_w, int64_t n, int64_t k, void* out, int out_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (moe_status s = check_gmm16("moe_grouped_matmul", dtype, out_dtype, rows, num_groups, n, k)) return s;
+  if (transpose_w != 0 && transpose_w != 1) return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul: transpose_w must be 0 or 1");
+  if (!group_offsets && num_groups != 1)
+    return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul: num_groups %lld needs group_offsets", (long long)num_groups);
+  if (rows == 0) return ok();
+  moe::Gmm16Params p = gmm16_params(dtype, out_dtype, rows, group_offsets, num_groups, n, k);
+  p.a = x; p.b = w; p.out = out; p.trans = transpose_w != 0;
+  return run_gmm16("moe_grouped_matmul", p, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+moe_status moe_grouped_matmul_wgrad_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k,
+                                                   size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul_wgrad_workspace_size: bytes is NULL");
+  if (moe_status s = check_gmm16("moe_grouped_matmul_wgrad", MOE_DTYPE_BF16, MOE_DTYPE_BF16, rows, num_groups, n, k)) return s;
+  Carver cv(nullptr);
+  moe::Gmm16Params p = gmm16_params(MOE_DTYPE_BF16, MOE_DTYPE_FP32, rows, nullptr, num_groups, n, k);
+  p.wgrad = true;
+  carve_gmm16(cv, p);
+  *bytes = cv.off;
+  return ok();
+}
+
+moe_status moe_grouped_matmul_wgrad(const void* grad_out, const void* x, int dtype, int64_t rows,
+                                    const int32_t* group_offsets, int64_t num_groups, int64_t n, int64_t k, void* out,
+                                    int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (moe_status s = check_gmm16("moe_grouped_matmul_wgrad", dtype, out_dtype, rows, num_groups, n, k)) return s;
+  if (!group_offsets && num_groups != 1)
+    return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul_wgrad: num_groups %lld needs group_offsets", (long long)num_groups);
+  moe::Gmm16Params p = gmm16_params(dtype, out_dtype, rows, group_offsets, num_groups, n, k);
+  p.a = grad_out; p.b = x; p.out = out; p.wgrad = true;
+  return run_gmm16("moe_grouped_matmul_wgrad", p, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 moe_status moe_probe_stream(int mode, const void* src, void* dst, int64_t bytes, void* stream) {

@@ -1,0 +1,140 @@
+// 16-bit (bf16 or fp16) product of the rows of expert groups, and its gradients:
+//   out[r] = x[r] w_g^T           w_g [n, k]      (the forward product)
+//   out[r] = x[r] w_g             w_g [k, n]      (grad_x = grad_out w_g of the former)
+//   out_g  = a_g^T b_g            summed over the rows of g (grad_w_g = grad_out_g^T x_g)
+// Products of 16-bit values are exact in fp32; they are added in fp32 by the MFMAs and rounded to
+// the output's type once.
+//
+// The kernel of this file takes every shape: operands are read by elements, whatever their
+// strides, and staged in LDS with the contraction innermost, as V_MFMA_F32_16X16X32 takes them:
+// lane l holds elements 8 (l / 16) .. + 7 of row l % 16. A block of four waves makes a tile of 64 x 64
+// outputs, 32 x 32 a wave.
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "fp4_device.h"
+#include "gmm16_device.h"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 64, kStep = 32, kPitch = kStep + 8;   // (a pitch of 80 bytes: 16-byte reads of 16 rows meet no bank twice)
+
+// Element (i, c) of an operand: base[i * major + c * con] for i < rows, c < length, else 0.
+struct Operand {
+  const uint16_t* base;
+  int64_t major, con;
+  int rows;
+};
+
+__device__ __forceinline__ void stage(const Operand& o, int c0, int length, uint16_t* lds) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < kTile * kStep / 256; ++j) {
+    const int e = t + 256 * j;
+    // neighbouring threads along the dimension that is contiguous in memory
+    const int i = o.con == 1 ? e / kStep : e % kTile, c = o.con == 1 ? e % kStep : e / kTile;
+    uint16_t v = 0;
+    if (i < o.rows && c0 + c < length) v = o.base[i * o.major + (c0 + c) * o.con];
+    lds[i * kPitch + c] = v;
+  }
+}
+
+// acc[i][j]: 16 x 16 blocks of the wave's 32 channels x 32 rows.
+template <typename T>
+__device__ __forceinline__ void multiply(const Operand& chan, const Operand& row, int length, uint16_t* lds,
+                                         v4f (&acc)[2][2]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint16_t *lc = lds, *lr = lds + kTile * kPitch;
+  for (int c0 = 0; c0 < length; c0 += kStep) {
+    stage(chan, c0, length, lc);
+    stage(row, c0, length, lr);
+    __syncthreads();
+    u32x4 a[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = *reinterpret_cast<const u32x4*>(lc + ((wave & 1) * 32 + i * 16 + (lane & 15)) * kPitch + (lane >> 4) * 8);
+      b[i] = *reinterpret_cast<const u32x4*>(lr + ((wave >> 1) * 32 + i * 16 + (lane & 15)) * kPitch + (lane >> 4) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = Mfma<T>::k32(a[i], b[j], acc[i][j]);
+    __syncthreads();
+  }
+}
+
+// Lane l holds channels 4 (l / 16) .. + 3 of row l % 16 of a block.
+template <typename T, typename O>
+__device__ __forceinline__ void store(const v4f (&acc)[2][2], O* out, int64_t pitch, int channels, int rows) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int ch = (wave & 1) * 32 + i * 16 + (lane >> 4) * 4, r = (wave >> 1) * 32 + j * 16 + (lane & 15);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (ch + e < channels && r < rows) out[r * pitch + ch + e] = Mfma<T>::template out<O>(acc[i][j][e]);
+    }
+}
+
+template <typename T, typename O, bool WGRAD>
+__global__ __launch_bounds__(256) void gmm16_any_kernel(Gmm16Params p) {
+  __shared__ __align__(16) uint16_t lds[2 * kTile * kPitch];
+  __shared__ int ends[kMaxGroups], scratch[4];
+  const int ncol = ((WGRAD ? p.k : p.n) + kTile - 1) / kTile, nrow = (p.n + kTile - 1) / kTile;
+  const int tiles = WGRAD ? p.groups * nrow : count_tiles<kTile>(p.off, p.groups, (int)p.rows, ends, scratch);
+  const int64_t total = (int64_t)tiles * ncol;
+  for (int64_t it = blockIdx.x; it < total; it += gridDim.x) {
+    const int tile = (int)(it / ncol), c0 = (int)(it % ncol) * kTile;
+    v4f acc[2][2] = {};
+    int lo, hi;
+    if constexpr (WGRAD) {
+      const int g = tile / nrow, r0 = (tile - g * nrow) * kTile;
+      group_rows(p.off, g, (int)p.rows, &lo, &hi);
+      const Operand chan{(const uint16_t*)p.b + (int64_t)lo * p.k + c0, 1, p.k, p.k - c0};
+      const Operand row{(const uint16_t*)p.a + (int64_t)lo * p.n + r0, 1, p.n, p.n - r0};
+      multiply<T>(chan, row, hi - lo, lds, acc);
+      store<T>(acc, (O*)p.out + ((int64_t)g * p.n + r0) * p.k + c0, p.k, p.k - c0, p.n - r0);
+    } else {
+      const int g = group_of_tile(ends, p.groups, tile);
+      group_rows(p.off, g, (int)p.rows, &lo, &hi);
+      const int r0 = lo + (tile - (g > 0 ? ends[g - 1] : 0)) * kTile, rows = min(kTile, hi - r0);
+      const uint16_t* w = (const uint16_t*)p.b + (int64_t)g * p.n * p.k;
+      const Operand chan = p.trans ? Operand{w + c0, 1, p.n, p.n - c0} : Operand{w + (int64_t)c0 * p.k, p.k, 1, p.n - c0};
+      const Operand row{(const uint16_t*)p.a + (int64_t)r0 * p.k, p.k, 1, rows};
+      multiply<T>(chan, row, p.k, lds, acc);
+      store<T>(acc, (O*)p.out + (int64_t)r0 * p.n + c0, p.n, p.n - c0, rows);
+    }
+  }
+}
+
+template <typename T, typename O>
+hipError_t launch_any(const Gmm16Params& p, hipStream_t stream) {
+  const int64_t nrow = (p.n + kTile - 1) / kTile;
+  const int64_t items = p.wgrad ? p.groups * nrow * ((p.k + kTile - 1) / kTile)
+                                : ((p.rows + kTile - 1) / kTile + std::min<int64_t>(p.groups, p.rows)) * nrow;
+  const unsigned grid = (unsigned)std::min<int64_t>(items, 1 << 20);
+  if (p.wgrad)
+    gmm16_any_kernel<T, O, true><<<grid, 256, 0, stream>>>(p);
+  else
+    gmm16_any_kernel<T, O, false><<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
+  return p.out_fp32 ? launch_any<T, float>(p, stream) : launch_any<T, uint16_t>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {
+  if (p.rows <= 0 && !p.wgrad) return hipSuccess;
+  return p.half ? launch_as<_Float16>(p, stream) : launch_as<__bf16>(p, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,92 @@
+// Device helpers of the 16-bit grouped products (gmm16.hip, gmm16_tile.hip).
+#pragma once
+
+#include "device_common.h"
+#include "fp4_device.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxGroups = 1024;
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// The MFMAs of an element type: 16 bytes a lane of each operand.
+template <typename T> struct Mfma;
+
+template <> struct Mfma<__bf16> {
+  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ v4f k32(u32x4 a, u32x4 b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v16f k16(u32x4 a, u32x4 b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) { return bf16x2(a, b); }
+  template <typename O> static __device__ __forceinline__ O out(float v) {
+    if constexpr (sizeof(O) == 4) return v;
+    else return (uint16_t)bf16x2(v, v);
+  }
+};
+
+template <> struct Mfma<_Float16> {
+  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ v4f k32(u32x4 a, u32x4 b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v16f k16(u32x4 a, u32x4 b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {   // to nearest even, each by itself
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, h2{(_Float16)a, (_Float16)b});
+  }
+  template <typename O> static __device__ __forceinline__ O out(float v) {
+    if constexpr (sizeof(O) == 4) return v;
+    else return __builtin_bit_cast(uint16_t, (_Float16)v);
+  }
+};
+
+// ends[g] = tiles of MT rows of groups 0 .. g (all 256 threads; ends has room for kMaxGroups,
+// scratch for 4). Returns the number of tiles.
+template <int MT>
+__device__ __forceinline__ int count_tiles(const int32_t* off, int groups, int rows, int* ends, int* scratch) {
+  const int t = threadIdx.x, lane = t & 63;
+  int n[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = 4 * t + i;
+    int lo = 0, hi = 0;
+    if (g < groups) group_rows(off, g, rows, &lo, &hi);
+    sum += (hi - lo + MT - 1) / MT;
+    n[i] = sum;
+  }
+  int incl = sum;
+  for (int s = 1; s < 64; s *= 2) {
+    const int v = __shfl_up(incl, s, 64);
+    incl += lane >= s ? v : 0;
+  }
+  if (lane == 63) scratch[t >> 6] = incl;
+  __syncthreads();
+  int base = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    base += w < (t >> 6) ? scratch[w] : 0;
+    total += scratch[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ends[4 * t + i] = base + n[i];
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+// The group of tile t: the first that ends behind it.
+__device__ __forceinline__ int group_of_tile(const int* ends, int groups, int t) {
+  int g = 0;
+  for (int s = kMaxGroups / 2; s > 0; s /= 2)
+    if (g + s <= groups - 1 && ends[g + s - 1] <= t) g += s;
+  return g;
+}
+
+}  // namespace
+}  // namespace moe

@@ -326,6 +326,59 @@ int fp4_tile_rows(int64_t rows, int64_t groups, int64_t n, int64_t k, bool value
 hipError_t launch_fp4_tiles(const Fp4MatmulParams& p, hipStream_t stream);
 hipError_t launch_fp4_matmul(const Fp4MatmulParams& p, hipStream_t stream);
 
+// ---- root-mean-square norm (norm.hip) --------------------------------------------------
+struct NormParams {
+  const void* x = nullptr;         // [rows, cols] of dtype (MOE_DTYPE_FP32 / _FP16 / _BF16)
+  const void* residual = nullptr;  // the same, or null
+  const void* weight = nullptr;    // [cols] of weight_dtype (dtype or FP32)
+  int dtype = 2, weight_dtype = 2;
+  int64_t rows = 0;
+  int cols = 0;                    // <= 16384
+  float eps = 0.0f;
+  int quant = 0;                   // 0 none, 1 E4M3, 2 E5M2, 3 E2M1 (cols % 32 == 0)
+  int scale_cols = 0;
+  void* y = nullptr;               // or null
+  void* h = nullptr;               // with residual
+  float* rstd = nullptr;
+  uint8_t* codes = nullptr;
+  uint8_t* scales = nullptr;
+};
+hipError_t launch_norm(const NormParams& p, hipStream_t stream);
+
+int norm_parts(int64_t rows);
+struct NormGradParams {
+  const void* grad_y = nullptr;
+  const void* h = nullptr;
+  const void* grad_h = nullptr;    // or null
+  const void* weight = nullptr;
+  const float* rstd = nullptr;
+  int dtype = 2, weight_dtype = 2;
+  int64_t rows = 0;
+  int cols = 0, parts = 1;
+  float* part = nullptr;           // workspace [parts, cols]
+  void* grad_x = nullptr;
+  float* grad_w = nullptr;
+};
+hipError_t launch_norm_backward(const NormGradParams& p, hipStream_t stream);
+
+// ---- 16-bit product of expert groups (gmm16.hip) -----------------------------------------
+// rows = false: out[r] = sum_c x[r, c] w[g](j, c) for the rows r of group g, w[g] stored
+// [n, k] (trans: [k, n]); x [rows, k], out [rows, n].
+// wgrad: out[g][i, j] = sum over the group's rows r of a[r, i] b[r, j]; a [rows, n], b [rows, k].
+struct Gmm16Params {
+  const void* a = nullptr;         // x, or the gradient of the output (wgrad)
+  const void* b = nullptr;         // w, or x (wgrad)
+  bool half = false;               // fp16, else bf16
+  bool trans = false, wgrad = false;
+  int64_t rows = 0;
+  const int32_t* off = nullptr;    // [groups + 1], or null: one group
+  int groups = 1;
+  int n = 0, k = 0;
+  bool out_fp32 = false;           // else the operands' type
+  void* out = nullptr;
+};
+hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream);
+
 // ---- static scratch of the allocation-free entry point (noalloc.hip) ---------------------
 // Bytes of the per-device scratch array moe_init_routing_noalloc uses instead of a
 // caller workspace.
