@@ -130,10 +130,23 @@ hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
   return p.out_fp32 ? launch_any<T, float>(p, stream) : launch_any<T, uint16_t>(p, stream);
 }
 
+// Rows of a tile of the LDS-staged kernels for a call: a little more than the average group has.
+int tile_rows(const Gmm16Params& p) {
+  if (p.wgrad) return 256;
+  const int64_t per = (p.rows + p.groups - 1) / p.groups;
+  return per <= 20 ? 32 : per <= 48 ? 64 : per <= 100 ? 128 : 256;
+}
+
 }  // namespace
 
 hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {
   if (p.rows <= 0 && !p.wgrad) return hipSuccess;
+  const auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+  if (p.n % 8 == 0 && p.k % 8 == 0 && on16(p.a) && on16(p.b) && on16(p.out)) {
+    Gmm16Params q = p;
+    q.mt = tile_rows(p);
+    if (q.mt) return p.wgrad ? launch_gmm16_weights(q, stream) : p.trans ? launch_gmm16_transposed(q, stream) : launch_gmm16_forward(q, stream);
+  }
   return p.half ? launch_as<_Float16>(p, stream) : launch_as<__bf16>(p, stream);
 }
 

@@ -1,0 +1,5 @@
+#include "gmm16_tile.h"
+
+namespace moe {
+hipError_t launch_gmm16_transposed(const Gmm16Params& p, hipStream_t stream) { return launch_tile16_form<kTransposed>(p, stream); }
+}  // namespace moe

@@ -376,7 +376,11 @@ struct Gmm16Params {
   int n = 0, k = 0;
   bool out_fp32 = false;           // else the operands' type
   void* out = nullptr;
+  int mt = 0;                      // rows of a tile of the LDS-staged kernels, 0: the kernel for every shape
 };
+hipError_t launch_gmm16_forward(const Gmm16Params& p, hipStream_t stream);
+hipError_t launch_gmm16_transposed(const Gmm16Params& p, hipStream_t stream);
+hipError_t launch_gmm16_weights(const Gmm16Params& p, hipStream_t stream);
 hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream);
 
 // ---- static scratch of the allocation-free entry point (noalloc.hip) ---------------------
