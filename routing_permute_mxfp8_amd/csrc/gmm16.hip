@@ -130,7 +130,6 @@ hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
   return p.out_fp32 ? launch_any<T, float>(p, stream) : launch_any<T, uint16_t>(p, stream);
 }
 
-// Rows of a tile of the LDS-staged kernels for a call: a little more than the average group has.
 int tile_rows(const Gmm16Params& p) {
   if (p.wgrad) return 256;
   const int64_t per = (p.rows + p.groups - 1) / p.groups;

@@ -67,11 +67,12 @@ __device__ __forceinline__ void pin(v16f (&acc)[CB][RB]) {
     for (int j = 0; j < RB; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-// Waits for the wave's loads and LDS accesses, then for the other waves: what was loaded or
-// written is there for all, and what was read may be written again.
+// Waits for the wave's LDS accesses (and with DMA for its direct-to-LDS loads), then for the other
+// waves: what was loaded or written is there for all, and what was read may be written again.
+template <bool DMA>
 __device__ __forceinline__ void slot_barrier() {
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (0 << 8));
+  __builtin_amdgcn_s_waitcnt(DMA ? (0 << 14) | (7 << 4) | (0 << 8) | 0 : (3 << 14) | (7 << 4) | (0 << 8) | 15);
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
@@ -96,7 +97,7 @@ struct Item16 {
 // The body gets the two slots and the rest of LDS as three restrict pointers, which is what they
 // are: apart. A slot is never read while loads into it are in flight, and so the compiler, which
 // makes an LDS read wait for the direct-to-LDS loads that may write there, has nothing to wait for.
-template <int FORM, int WC, int CB, int RB, bool ONCE, typename T>
+template <int FORM, int WC, int CB, int RB, bool ONCE, bool DMA, typename T>
 __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __restrict__ slot0,
                                             uint8_t* __restrict__ slot1, uint8_t* __restrict__ lds) {
   using S = Tile16<WC, CB, RB>;
@@ -226,32 +227,44 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     }
   };
   int con_rows = 0;   // of the item being loaded: rows of a transposed operand
-  auto load = [&](const uint8_t* base, int bytes, int voff, int soff, uint8_t* to, bool once) {
-    const auto r = buffer_of(base, bytes);
-    if (once)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)to, 16, voff, soff, 0, 2);
-    else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)to, 16, voff, soff, 0, 0);
+  // load i of step `step`: its buffer and the lane's place in it
+  struct Source {
+    __amdgpu_buffer_rsrc_t r;
+    int voff, soff;
   };
-  // load i of step `step` into slot `slot` (a constant)
-  auto issue = [&](int slot, int step, int i) {
-    uint8_t* base = slot ? slot1 : slot0;
+  auto source = [&](int step, int i) {
     const bool in = step < steps;
     const int left = min(max(con_rows - step * kCon, 0), kCon);
     if (i < S::kLA) {
-      uint8_t* to = base + (wave * S::kLA + i) * 1024;
       if constexpr (kDirA)
-        load(pa, in ? na : 0, va[i] + (step == tail_step ? ta[i & 1] : 0), step * 2 * kCon, to, ONCE);
+        return Source{buffer_of(pa, in ? na : 0), va[i] + (step == tail_step ? ta[i & 1] : 0), step * 2 * kCon};
       else
-        load(pa + (int64_t)step * kCon * 2 * p.nc, left > 0 ? left * 2 * p.nc - na : 0, va[i], 0, to, ONCE);
+        return Source{buffer_of(pa + (int64_t)step * kCon * 2 * p.nc, left > 0 ? left * 2 * p.nc - na : 0), va[i], 0};
     } else {
       i -= S::kLA;
-      uint8_t* to = base + S::kA + (wave * S::kLB + i) * 1024;
       if constexpr (kDirB)
-        load(pb, in ? nb : 0, vb[i] + (step == tail_step ? tb[i & 1] : 0), step * 2 * kCon, to, false);
+        return Source{buffer_of(pb, in ? nb : 0), vb[i] + (step == tail_step ? tb[i & 1] : 0), step * 2 * kCon};
       else
-        load(pb + (int64_t)step * kCon * 2 * p.nr, left > 0 ? left * 2 * p.nr - nb : 0, vb[i], 0, to, false);
+        return Source{buffer_of(pb + (int64_t)step * kCon * 2 * p.nr, left > 0 ? left * 2 * p.nr - nb : 0), vb[i], 0};
     }
+  };
+  auto place = [&](int slot, int i) {   // of load i in a slot (a constant): 1 KB
+    return (slot ? slot1 : slot0) + (i < S::kLA ? (wave * S::kLA + i) * 1024 : S::kA + (wave * S::kLB + i - S::kLA) * 1024);
+  };
+  u32x4 held[DMA ? 1 : S::kLA + S::kLB];
+  auto fetch = [&](int slot, int step, int i) {
+    const Source f = source(step, i);
+    const bool once = ONCE && i < S::kLA;
+    if constexpr (DMA) {
+      if (once) __builtin_amdgcn_raw_ptr_buffer_load_lds(f.r, (lds_ptr)place(slot, i), 16, f.voff, f.soff, 0, 2);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(f.r, (lds_ptr)place(slot, i), 16, f.voff, f.soff, 0, 0);
+    } else {
+      if (once) held[i] = __builtin_amdgcn_raw_buffer_load_b128(f.r, f.voff, f.soff, 2);
+      else held[i] = __builtin_amdgcn_raw_buffer_load_b128(f.r, f.voff, f.soff, 0);
+    }
+  };
+  auto put = [&](int slot, int i) {
+    if constexpr (!DMA) *reinterpret_cast<u32x4*>(place(slot, i) + lane * 16) = held[i];
   };
   constexpr int kLoads = S::kLA + S::kLB;
 
@@ -313,17 +326,42 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     for (int i = lo + m * per; i < lo + (m + 1) * per; ++i)
       if (i < hi) f(i);
   };
-  // Slot `slot` (a constant), whose first sub-step's operands are in registers; the loads of step
-  // `next` of the item aimed at go into it when it is read.
-  auto run_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>, int next) {
+  // The MFMAs of a slot's last sub-step, and of the next slot's first three. Behind the barrier
+  // that lies before them the slot SLOT is read: the step after next goes into it. DMA: its loads
+  // are issued in the first of these sub-steps. Else what was fetched before is put there, a part
+  // with each of the four sub-steps, and in the place of each part that of step `next` of the item
+  // aimed at is fetched: every load has a whole slot's time, and the loads are spread evenly (the
+  // CU's L1 takes half of a slot's time for them; in a burst they hold up the waves).
+  auto load_part = [&]<int SLOT>(std::integral_constant<int, SLOT>, int quarter, int m, int next) {
+    if constexpr (DMA) {
+      if (quarter == 0) dealt(m, 0, kLoads, [&](int i) { fetch(SLOT, next, i); });
+    } else {
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
-      multiply(s, [&](int m) { dealt(m, 0, CB + RB, [&](int i) { read(SLOT, s + 1, i); }); });
-    slot_barrier();
+      for (int i = 0; i < kLoads; ++i)
+        if (i * 4 * M / kLoads == quarter * M + m) {
+          put(SLOT, i);
+          fetch(SLOT, next, i);
+        }
+    }
+  };
+  auto end_slot = [&]<int SLOT>(std::integral_constant<int, SLOT> k, int next) {
     multiply(3, [&](int m) {
       dealt(m, 0, CB + RB, [&](int i) { read(SLOT ^ 1, 0, i); });
-      dealt(m, 0, kLoads, [&](int i) { issue(SLOT, next, i); });
+      load_part(k, 0, m, next);
     });
+  };
+  auto begin_slot = [&]<int SLOT>(std::integral_constant<int, SLOT> k, int next) {   // of the other slot than SLOT
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+      multiply(s, [&](int m) {
+        dealt(m, 0, CB + RB, [&](int i) { read(SLOT ^ 1, s + 1, i); });
+        load_part(k, s + 1, m, next);
+      });
+    slot_barrier<DMA>();
+  };
+  auto turn = [&](auto k, int next) {
+    end_slot(k, next);
+    begin_slot(k, next);
   };
   constexpr std::integral_constant<int, 0> k0{};
   constexpr std::integral_constant<int, 1> k1{};
@@ -332,14 +370,28 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   Item16 cur = item(0);
   aim(cur);
   con_rows = FORM == kWeights ? cur.rows : p.con;
+  // DMA: steps 0 and 1 are on their way into the slots. Else step 0 is in its slot, and steps 1 and 2
+  // are where the turn before the first would have left them: step 1's first quarter put and step
+  // 2's fetched.
+  constexpr int kQuarter = (kLoads + 3) / 4;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) issue(0, 0, i);
+  for (int i = 0; i < kLoads; ++i) fetch(0, 0, i);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) issue(1, 1, i);
-  slot_barrier();
+  for (int i = 0; i < kLoads; ++i) put(0, i);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) fetch(1, 1, i);
+  if constexpr (!DMA) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (i * 4 * M / kLoads < M) {
+        put(1, i);
+        fetch(1, 2, i);
+      }
+  }
+  slot_barrier<DMA>();
 #pragma unroll
   for (int i = 0; i < CB + RB; ++i) read(0, 0, i);
-  for (int64_t n = 0;;) {
+  auto zero = [&]() {
 #pragma unroll
     for (int i = 0; i < CB; ++i)
 #pragma unroll
@@ -347,21 +399,28 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     pin(acc);
-    const int pairs = max(1, (steps + 1) / 2);   // (an odd number of steps: the last is one of zeros)
-    for (int q = 0; q < pairs - 1; ++q) {
-      run_slot(k0, 2 * q + 2);
-      run_slot(k1, 2 * q + 3);
+  };
+  zero();
+  begin_slot(k1, 2);
+  for (int64_t n = 0;;) {
+    // steps of the item, an even number (those behind its last are zeros)
+    const int all = max(DMA ? 2 : 4, (steps + 1) / 2 * 2);
+    for (int t = 0; t < all - (DMA ? 2 : 4); t += 2) {
+      turn(k0, t + (DMA ? 2 : 3));
+      turn(k1, t + (DMA ? 3 : 4));
       pin(acc);
     }
-    // the item's last pair: the next item's first is loaded behind it
+    if constexpr (!DMA) turn(k0, all - 1);
+    // the next item's first steps are loaded behind the item's last
     const bool more = n + 1 < count;
     if (more && (n + 1) % kList == 0) fill(n + 1);
     const Item16 next = more ? item(n + 1) : cur;
     aim(next);
     con_rows = FORM == kWeights ? next.rows : p.con;
     if (!more) steps = con_rows = 0;
-    run_slot(k0, 0);
-    run_slot(k1, 1);
+    if constexpr (!DMA) turn(k1, 0);
+    turn(k0, DMA ? 0 : 1);
+    end_slot(k1, DMA ? 1 : 2);
     pin(acc);
     // ---- output: lane (h, r) holds row r, channels 8 e + 4 h + 0..3 of a block. Lane halves and
     // quarters change places until a row's 64 bytes are next to one another, in lanes l, l + 16,
@@ -408,15 +467,17 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     }
     if (++n >= count) break;
     cur = next;
+    zero();
+    begin_slot(k1, DMA ? 1 : 2);
   }
   __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (15 << 8));   // no direct-to-LDS load outlives the block
 }
 
-template <int FORM, int WC, int CB, int RB, int BLOCKS, bool ONCE, typename T>
+template <int FORM, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BLOCKS))) void gmm16_tile_kernel(Tile16Args p) {
   extern __shared__ __align__(16) uint8_t lds_area[];
   constexpr int kSlot = Tile16<WC, CB, RB>::kSlot;
-  tile16_body<FORM, WC, CB, RB, ONCE, T>(p, lds_area, lds_area + kSlot, lds_area + 2 * kSlot);
+  tile16_body<FORM, WC, CB, RB, ONCE, DMA, T>(p, lds_area, lds_area + kSlot, lds_area + 2 * kSlot);
 }
 
 // The device's compute units, rounded up to whole XCDs' shares; the kernel's LDS size set
@@ -439,13 +500,13 @@ inline hipError_t tile16_grid(const void* kernel, int lds, int* grid) {
   return hipSuccess;
 }
 
-template <int FORM, int WC, int CB, int RB, int BLOCKS, bool ONCE, typename T>
+template <int FORM, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
 hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
   using S = Tile16<WC, CB, RB>;
   static_assert(S::kLds * BLOCKS <= 160 * 1024, "LDS of a compute unit");
   static_assert(S::kMT >= 64 || FORM != kWeights, "a transposed operand is 64 wide at least");
   int grid = 0;
-  const auto kernel = gmm16_tile_kernel<FORM, WC, CB, RB, BLOCKS, ONCE, T>;
+  const auto kernel = gmm16_tile_kernel<FORM, WC, CB, RB, BLOCKS, ONCE, DMA, T>;
   hipError_t e = tile16_grid(reinterpret_cast<const void*>(kernel), S::kLds, &grid);
   if (e != hipSuccess) return e;
   kernel<<<grid * BLOCKS, kThreads, S::kLds, stream>>>(a);
@@ -455,13 +516,14 @@ hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
 // mt: rows of a tile.
 template <int FORM, typename T>
 hipError_t launch_tile16_as(const Tile16Args& a, int mt, hipStream_t stream) {
+  constexpr bool dma = FORM == kForward;   // (the transposing read waits for every direct-to-LDS load in flight)
   switch (mt) {
-    case 256: return launch_tile16<FORM, 2, 4, 4, 1, false, T>(a, stream);
-    case 128: return launch_tile16<FORM, 2, 4, 2, 1, false, T>(a, stream);
-    case 64: return launch_tile16<FORM, 4, 1, 2, 2, FORM != kWeights, T>(a, stream);
+    case 256: return launch_tile16<FORM, 2, 4, 4, 1, false, false, T>(a, stream);
+    case 128: return launch_tile16<FORM, 2, 4, 2, 1, false, dma, T>(a, stream);
+    case 64: return launch_tile16<FORM, 4, 1, 2, 2, FORM != kWeights, dma, T>(a, stream);
     default:
       if constexpr (FORM == kWeights) return hipErrorInvalidValue;
-      else return launch_tile16<FORM, 4, 1, 1, 3, true, T>(a, stream);
+      else return launch_tile16<FORM, 4, 1, 1, 3, true, dma, T>(a, stream);
   }
 }
 
