@@ -86,7 +86,7 @@ __global__ __launch_bounds__(256) void gmm16_any_kernel(Gmm16Params p) {
   __shared__ __align__(16) uint16_t lds[2 * kTile * kPitch];
   __shared__ int ends[kMaxGroups], scratch[4];
   const int ncol = ((WGRAD ? p.k : p.n) + kTile - 1) / kTile, nrow = (p.n + kTile - 1) / kTile;
-  const int tiles = WGRAD ? p.groups * nrow : count_tiles<kTile>(p.off, p.groups, (int)p.rows, ends, scratch);
+  const int tiles = WGRAD ? p.groups * nrow : count_tiles<kTile, 4>(p.off, p.groups, (int)p.rows, ends, scratch);
   const int64_t total = (int64_t)tiles * ncol;
   for (int64_t it = blockIdx.x; it < total; it += gridDim.x) {
     const int tile = (int)(it / ncol), c0 = (int)(it % ncol) * kTile;

@@ -9,8 +9,6 @@ namespace {
 
 constexpr int kMaxGroups = 1024;
 
-typedef float v16f __attribute__((ext_vector_type(16)));
-
 // The MFMAs of an element type: 16 bytes a lane of each operand.
 template <typename T> struct Mfma;
 
@@ -19,8 +17,9 @@ template <> struct Mfma<__bf16> {
   static __device__ __forceinline__ v4f k32(u32x4 a, u32x4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
-  static __device__ __forceinline__ v16f k16(u32x4 a, u32x4 b, v16f c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  // c += a b in place; c is left alone until settled.
+  static __device__ __forceinline__ void k32_into(v4f& c, u32x4 a, u32x4 b) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ uint32_t pair(float a, float b) { return bf16x2(a, b); }
   template <typename O> static __device__ __forceinline__ O out(float v) {
@@ -34,8 +33,9 @@ template <> struct Mfma<_Float16> {
   static __device__ __forceinline__ v4f k32(u32x4 a, u32x4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
-  static __device__ __forceinline__ v16f k16(u32x4 a, u32x4 b, v16f c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  // c += a b in place; c is left alone until settled.
+  static __device__ __forceinline__ void k32_into(v4f& c, u32x4 a, u32x4 b) {
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ uint32_t pair(float a, float b) {   // to nearest even, each by itself
     typedef _Float16 h2 __attribute__((ext_vector_type(2)));
@@ -47,15 +47,16 @@ template <> struct Mfma<_Float16> {
   }
 };
 
-// ends[g] = tiles of MT rows of groups 0 .. g (all 256 threads; ends has room for kMaxGroups,
-// scratch for 4). Returns the number of tiles.
-template <int MT>
+// ends[g] = tiles of MT rows of groups 0 .. g (all 64 WAVES threads; ends has room for kMaxGroups,
+// scratch for WAVES). Returns the number of tiles.
+template <int MT, int WAVES>
 __device__ __forceinline__ int count_tiles(const int32_t* off, int groups, int rows, int* ends, int* scratch) {
+  constexpr int kEach = kMaxGroups / (64 * WAVES);
   const int t = threadIdx.x, lane = t & 63;
-  int n[4], sum = 0;
+  int n[kEach], sum = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int g = 4 * t + i;
+  for (int i = 0; i < kEach; ++i) {
+    const int g = kEach * t + i;
     int lo = 0, hi = 0;
     if (g < groups) group_rows(off, g, rows, &lo, &hi);
     sum += (hi - lo + MT - 1) / MT;
@@ -70,12 +71,12 @@ __device__ __forceinline__ int count_tiles(const int32_t* off, int groups, int r
   __syncthreads();
   int base = incl - sum, total = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     base += w < (t >> 6) ? scratch[w] : 0;
     total += scratch[w];
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) ends[4 * t + i] = base + n[i];
+  for (int i = 0; i < kEach; ++i) ends[kEach * t + i] = base + n[i];
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(total);
 }

@@ -1,23 +1,26 @@
 // 16-bit grouped products with both operands staged in LDS (the kernel of the three files
 // gmm16_forward.hip, gmm16_transposed.hip and gmm16_weights.hip).
 //
-// A work item is a tile of MT output rows by NT output channels, computed by four waves, each
-// holding CB x RB accumulators of 32 channels x 32 rows (V_MFMA_F32_32X32X16: lane l holds 8
-// contraction elements, 8 (l / 32) on, of row l % 32 of an operand; weights in the A slot, so that
+// A work item is a tile of MT output rows by NT output channels, computed by four or eight waves, each
+// holding CB x RB accumulators of 16 channels x 16 rows (V_MFMA_F32_16X16X32: lane l holds 8
+// contraction elements, 8 (l / 16) on, of row l % 16 of an operand; weights in the A slot, so that
 // a lane holds 4 neighbouring channels of one row). Blocks are persistent and XCD-aware.
 //
-// A slot of LDS holds 64 contraction elements of both operands; there are two. What a slot holds
-// is read into registers a sub-step of 16 ahead of its MFMAs; in a slot's last sub-step all waves
-// have read it (the barrier lies before), the loads of the step after next begin to fill it, and
-// the next slot's first operands are read. The loads go straight to LDS and go on across items.
+// A slot of LDS holds 64 contraction elements of both operands, two sub-steps of 32; there are two
+// slots. The MFMAs of a sub-step run in groups, one for each of the wave's RB row blocks: the CB
+// weight operands of the next sub-step are read beside them into a second set of registers, a row
+// operand into its own when its group has been issued. Behind the first group of a slot's second
+// sub-step all waves have read the slot (there is the barrier) and the loads of the step after next
+// begin to fill it. Loads go on across items.
 //
 // An operand whose contraction is contiguous in memory ("direct") lies in LDS as rows of 64
 // elements, 128 bytes; 16-byte chunk c of row r at place c ^ (r / 2 % 8), so that the sixteen lanes
 // of a read pass touch all banks once. One whose channels are contiguous ("transposed") lies as
 // 64 rows of the contraction, as it comes, and is transposed on its way to the registers
 // (DS_READ_B64_TR_B16: of the 16 x 4 elements that four lanes a contraction row address, 4 rows of
-// 16 channels, lane j gets the 4 contraction elements of channel j). There 64-byte blocks of row r
-// are exchanged by r % 4, so that the four rows of such a read lie in different banks.
+// 16 channels, lane j gets the 4 contraction elements of channel j). 32 lanes a clock are served,
+// rows 0 - 3 and 8 - 11 of 32 bytes each: 64-byte blocks of row r are exchanged by r % 4, their halves
+// by r / 8 % 2, so that these lie in different banks.
 #pragma once
 
 #include <algorithm>
@@ -32,7 +35,6 @@ namespace {
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-constexpr int kThreads = 256;
 constexpr int kList = 64;   // items described at a time
 constexpr int kCon = 64;    // contraction elements of a slot
 
@@ -48,24 +50,14 @@ struct Tile16Args {
   void* out;
 };
 
-template <int WC, int CB, int RB>
+template <int WAVES, int WC, int CB, int RB>
 struct Tile16 {
-  static constexpr int kNT = 32 * WC * CB, kMT = 32 * (4 / WC) * RB;
+  static constexpr int kNT = 16 * WC * CB, kMT = 16 * (WAVES / WC) * RB;
   static constexpr int kA = kNT * 2 * kCon, kB = kMT * 2 * kCon;   // bytes of a slot: channels, rows
-  static constexpr int kSlot = kA + kB;
   static constexpr int kEnds = 0, kItems = 4 * kMaxGroups;          // behind the slots
-  static constexpr int kLds = 2 * kSlot + kItems + 16 * kList;
-  static constexpr int kLA = kNT / 32, kLB = kMT / 32;              // loads of 1 KB a wave and slot
+  static constexpr int kLds = 2 * (kA + kB) + kItems + 16 * kList;
+  static constexpr int kLA = kNT / (8 * WAVES), kLB = kMT / (8 * WAVES);   // loads of 1 KB a wave and slot
 };
-
-// Keeps the accumulators in accumulation registers across loop edges.
-template <int CB, int RB>
-__device__ __forceinline__ void pin(v16f (&acc)[CB][RB]) {
-#pragma unroll
-  for (int i = 0; i < CB; ++i)
-#pragma unroll
-    for (int j = 0; j < RB; ++j) asm volatile("" : "+a"(acc[i][j]));
-}
 
 // Waits for the wave's LDS accesses (and with DMA for its direct-to-LDS loads), then for the other
 // waves: what was loaded or written is there for all, and what was read may be written again.
@@ -79,28 +71,19 @@ __device__ __forceinline__ void slot_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Lanes 16 - 31 and 48 - 63 of a change places with lanes 0 - 15 and 32 - 47 of b.
-__device__ __forceinline__ void swap_rows(u32x4& a, u32x4& b) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const auto s = __builtin_amdgcn_permlane16_swap(a[c], b[c], false, false);
-    a[c] = s[0];
-    b[c] = s[1];
-  }
-}
-
 struct Item16 {
   int group, lo, rows;   // rows [lo, lo + rows): the tile's (kWeights: the group's, which are summed)
   int rt, cb;            // channel block; row tile of the output (kWeights)
 };
 
-// The body gets the two slots and the rest of LDS as three restrict pointers, which is what they
-// are: apart. A slot is never read while loads into it are in flight, and so the compiler, which
+// The body gets the slots (both of the channels' operand, both of the rows') and the rest of LDS as
+// restrict pointers, which is what they are: apart. A slot is never read while loads into it are in flight, and so the compiler, which
 // makes an LDS read wait for the direct-to-LDS loads that may write there, has nothing to wait for.
-template <int FORM, int WC, int CB, int RB, bool ONCE, bool DMA, typename T>
-__device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __restrict__ slot0,
-                                            uint8_t* __restrict__ slot1, uint8_t* __restrict__ lds) {
-  using S = Tile16<WC, CB, RB>;
+template <int FORM, int WAVES, int WC, int CB, int RB, bool ONCE, bool DMA, typename T>
+__device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __restrict__ a0, uint8_t* __restrict__ a1,
+                                            uint8_t* __restrict__ b0, uint8_t* __restrict__ b1,
+                                            uint8_t* __restrict__ lds) {
+  using S = Tile16<WAVES, WC, CB, RB>;
   constexpr int MT = S::kMT, NT = S::kNT;
   constexpr bool kDirA = FORM == kForward, kDirB = FORM != kWeights;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -110,12 +93,12 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   int4* const list = reinterpret_cast<int4*>(lds + S::kItems);
 
   // ---- items: each XCD takes a contiguous share, dealt to its blocks in turn ----------------
-  const int tiles = FORM == kWeights ? p.groups * nrt : count_tiles<MT>(p.off, p.groups, p.rows, ends, reinterpret_cast<int*>(list));
+  const int tiles = FORM == kWeights ? p.groups * nrt : count_tiles<MT, WAVES>(p.off, p.groups, p.rows, ends, reinterpret_cast<int*>(list));
   const int64_t total = (int64_t)tiles * ncb;
   const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
   const int64_t begin = total * xcd / 8 + (blockIdx.x >> 3), end = total * (xcd + 1) / 8;
   if (begin >= end) return;   // the whole block
-  const int64_t count = (end - begin + per - 1) / per;
+  const int count = (int)((end - begin + per - 1) / per);
   // Item `it`: four row tiles run through the channel blocks together, so that the items in flight
   // on one XCD share both operands in its L2.
   auto describe = [&](int64_t it) {
@@ -142,12 +125,12 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
       return make_int4(g, row0, min(MT, hi - row0), cb);
     }
   };
-  auto fill = [&](int64_t first) {   // list[i] = this block's item first + i
+  auto fill = [&](int first) {   // list[i] = this block's item first + i
     __syncthreads();
-    if (tid < kList && first + tid < count) list[tid] = describe(begin + (first + tid) * per);
+    if (tid < kList && first + tid < count) list[tid] = describe(begin + (int64_t)(first + tid) * per);
     __syncthreads();
   };
-  auto item = [&](int64_t i) {
+  auto item = [&](int i) {
     const int4 v = list[i % kList];
     Item16 r;
     r.group = __builtin_amdgcn_readfirstlane(v.x);
@@ -161,95 +144,83 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   auto steps_of = [&](const Item16& it) { return ((FORM == kWeights ? it.rows : p.con) + kCon - 1) / kCon; };
 
   // ---- loads: load i of a wave and operand fills 1 KB of it, lane l the 16 bytes at 16 l -------
-  // direct: 8 rows of 128 bytes; transposed: 1024 / (2 NT) rows of the contraction
-  int va[S::kLA], vb[S::kLB];
-  int ta[2] = {0, 0}, tb[2] = {0, 0};   // direct, the step that the contraction ends in: what moves a lane outside
+  // direct: 8 rows of 128 bytes; transposed: 1024 / (2 NT) rows of the contraction. Which chunk
+  // belongs at a lane's place depends on a few bits of the load's number only: what does is kept
+  // in registers, the rest is scalar.
+  constexpr int kRowsA = kDirA ? 8 : 512 / NT, kRowsB = kDirB ? 8 : 512 / MT;   // rows of a load
+  auto trans_swap = [](int width, int row) {   // what the chunks of a row of `width` channels are exchanged by
+    return 4 * (width == 64 ? (row >> 1) & 1 : row & 3) + 2 * ((row >> 3) & 1);
+  };
+  int va[2], vb[2], ta[2] = {0, 0}, tb[2] = {0, 0};
   const int tail_step = p.con % kCon ? p.con / kCon : -1;
-  auto direct_chunk = [&](int load) {   // the chunk of a direct operand's row that belongs at the lane's place
-    const int row = load * 8 + (lane >> 3);
-    return (lane & 7) ^ ((row >> 1) & 7);
+  auto lane_parts = [&](bool direct, int width, int per_wave, int (&v)[2], int (&t)[2], int pitch) {
+    if (direct) {   // v: the lane's place in an even and an odd load; t: what moves it outside in the step the contraction ends in
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int chunk = (lane & 7) ^ ((((wave * per_wave + i) * 8 + (lane >> 3)) >> 1) & 7);
+        v[i] = (lane >> 3) * pitch + 16 * chunk;
+        t[i] = 8 * chunk >= p.con % kCon ? kOutside : 0;
+      }
+    } else {        // v[0]: its row, v[1]: its chunk, but for the bits that load_swap exchanges
+      v[0] = lane / (width / 8) * pitch;
+      v[1] = 16 * (lane % (width / 8) ^ trans_swap(width, wave * per_wave * (512 / width) + lane / (width / 8)));
+    }
   };
-  auto trans_place = [&](int width, int load, int* row, int* chunk) {   // width: channels of a row in LDS
-    const int at = load * 64 + lane, places = width / 8;
-    *row = at / places;
-    const int x = width == 64 ? (*row >> 1) & 1 : *row & 3;
-    *chunk = (at % places) ^ (4 * x);
-  };
-  if constexpr (kDirA) {
-#pragma unroll
-    for (int i = 0; i < S::kLA; ++i) va[i] = ((wave * S::kLA + i) * 8 + (lane >> 3)) * 2 * p.con + 16 * direct_chunk(wave * S::kLA + i);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) ta[i] = 8 * direct_chunk(wave * S::kLA + i) >= p.con % kCon ? kOutside : 0;
-  }
-  if constexpr (kDirB) {
-#pragma unroll
-    for (int i = 0; i < S::kLB; ++i) vb[i] = ((wave * S::kLB + i) * 8 + (lane >> 3)) * 2 * p.con + 16 * direct_chunk(wave * S::kLB + i);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) tb[i] = 8 * direct_chunk(wave * S::kLB + i) >= p.con % kCon ? kOutside : 0;
-  }
+  // (a wave's loads begin at a row that is a multiple of 8, so their rows' bits are exchanged independently)
+  auto load_swap = [&](int width, int i) { return 16 * trans_swap(width, i * (512 / width)); };
+  static_assert(kDirA || S::kLA * kRowsA % 8 == 0, "a wave's rows of a transposed operand");
+  static_assert(kDirB || S::kLB * kRowsB % 8 == 0, "a wave's rows of a transposed operand");
+  const int pitch_a = 2 * (kDirA ? p.con : p.nc), pitch_b = 2 * (kDirB ? p.con : p.nr);
+  lane_parts(kDirA, NT, S::kLA, va, ta, pitch_a);
+  lane_parts(kDirB, MT, S::kLB, vb, tb, pitch_b);
 
   // The item being loaded: buffers of exactly what belongs to it (the rest reads as zeros,
-  // without memory traffic); channels of a transposed operand behind its last are left out too.
+  // without memory traffic).
   const uint8_t *pa, *pb;
-  int na, nb, steps;      // direct: bytes; transposed: bytes cut off a row's front (its first channel)
+  int na, nb, steps, con_rows;   // direct: rows; transposed: bytes cut off a row's front (its first channel)
   auto aim = [&](const Item16& it) {
     steps = steps_of(it);
+    con_rows = FORM == kWeights ? it.rows : p.con;
     if constexpr (FORM == kWeights) {
       pa = reinterpret_cast<const uint8_t*>(p.chan + (int64_t)it.lo * p.nc + it.cb * NT);
       pb = reinterpret_cast<const uint8_t*>(p.row + (int64_t)it.lo * p.nr + it.rt * MT);
       na = 2 * it.cb * NT;
       nb = 2 * it.rt * MT;
-#pragma unroll
-      for (int i = 0; i < S::kLB; ++i) {
-        int row, chunk;
-        trans_place(MT, wave * S::kLB + i, &row, &chunk);
-        vb[i] = it.rt * MT + 8 * chunk < p.nr ? row * 2 * p.nr + 16 * chunk : kOutside;
-      }
     } else {
       pb = reinterpret_cast<const uint8_t*>(p.row + (int64_t)it.lo * p.con);
-      nb = it.rows * 2 * p.con;
+      nb = it.rows;
       const uint16_t* w = p.chan + (int64_t)it.group * p.nc * p.con;
       if constexpr (kDirA) {
         pa = reinterpret_cast<const uint8_t*>(w + (int64_t)it.cb * NT * p.con);
-        na = min(NT, p.nc - it.cb * NT) * 2 * p.con;
+        na = min(NT, p.nc - it.cb * NT);
       } else {
         pa = reinterpret_cast<const uint8_t*>(w + it.cb * NT);
         na = 2 * it.cb * NT;
       }
     }
-    if constexpr (!kDirA) {
-#pragma unroll
-      for (int i = 0; i < S::kLA; ++i) {
-        int row, chunk;
-        trans_place(NT, wave * S::kLA + i, &row, &chunk);
-        va[i] = it.cb * NT + 8 * chunk < p.nc ? row * 2 * p.nc + 16 * chunk : kOutside;
-      }
-    }
   };
-  int con_rows = 0;   // of the item being loaded: rows of a transposed operand
-  // load i of step `step`: its buffer and the lane's place in it
+  // load i of an operand's step `step`: its buffer and the lane's place in it
   struct Source {
     __amdgpu_buffer_rsrc_t r;
     int voff, soff;
   };
-  auto source = [&](int step, int i) {
-    const bool in = step < steps;
-    const int left = min(max(con_rows - step * kCon, 0), kCon);
-    if (i < S::kLA) {
-      if constexpr (kDirA)
-        return Source{buffer_of(pa, in ? na : 0), va[i] + (step == tail_step ? ta[i & 1] : 0), step * 2 * kCon};
-      else
-        return Source{buffer_of(pa + (int64_t)step * kCon * 2 * p.nc, left > 0 ? left * 2 * p.nc - na : 0), va[i], 0};
-    } else {
-      i -= S::kLA;
-      if constexpr (kDirB)
-        return Source{buffer_of(pb, in ? nb : 0), vb[i] + (step == tail_step ? tb[i & 1] : 0), step * 2 * kCon};
-      else
-        return Source{buffer_of(pb + (int64_t)step * kCon * 2 * p.nr, left > 0 ? left * 2 * p.nr - nb : 0), vb[i], 0};
+  auto source_of = [&](bool direct, int width, const uint8_t* base, int n, int pitch, const int (&v)[2], const int (&t)[2],
+                       int row0, int step, int i) {
+    if (direct) {   // rows row0 .. row0 + 7 of the operand's n
+      const int left = step < steps ? max(n - row0, 0) : 0;
+      return Source{buffer_of(base + (int64_t)row0 * pitch, left * pitch), v[i & 1] + (step == tail_step ? t[i & 1] : 0),
+                    step * 2 * kCon};
     }
+    const int left = con_rows - step * kCon - row0;
+    return Source{buffer_of(base + (int64_t)(step * kCon + row0) * pitch, left > 0 ? min(left, kCon) * pitch - n : 0),
+                  (v[1] ^ load_swap(width, i)) + v[0], 0};
+  };
+  auto source = [&](int step, int i) {
+    return i < S::kLA ? source_of(kDirA, NT, pa, na, pitch_a, va, ta, (wave * S::kLA + i) * kRowsA, step, i)
+                      : source_of(kDirB, MT, pb, nb, pitch_b, vb, tb, (wave * S::kLB + i - S::kLA) * kRowsB, step, i - S::kLA);
   };
   auto place = [&](int slot, int i) {   // of load i in a slot (a constant): 1 KB
-    return (slot ? slot1 : slot0) + (i < S::kLA ? (wave * S::kLA + i) * 1024 : S::kA + (wave * S::kLB + i - S::kLA) * 1024);
+    return i < S::kLA ? (slot ? a1 : a0) + (wave * S::kLA + i) * 1024 : (slot ? b1 : b0) + (wave * S::kLB + i - S::kLA) * 1024;
   };
   u32x4 held[DMA ? 1 : S::kLA + S::kLB];
   auto fetch = [&](int slot, int step, int i) {
@@ -268,98 +239,102 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   };
   constexpr int kLoads = S::kLA + S::kLB;
 
-  // ---- operand reads of a wave: sub-step s (16 elements) of a slot ---------------------------
-  const int h = lane >> 5;
-  const int read0 = (lane & 31) * 128 + ((h ^ ((lane >> 1) & 7)) * 16);
-  int ra[CB], rb[RB];   // transposed: the lane's place in each block
-  auto trans_read = [&](int width, int blk) {
-    const int q = lane >> 4, i = lane & 15, row = 8 * (q >> 1) + (i >> 2);
-    const int x = width == 64 ? i >> 3 : i >> 2;
-    return row * 2 * width + (((blk ^ x) * 4 + 2 * (q & 1) + ((i & 3) >> 1)) * 16) + (i & 1) * 8;
+  // ---- operand reads of a wave: sub-step s (32 elements) of a slot ---------------------------
+  const int g4 = lane >> 4;
+  auto read_base = [&](bool direct, int width, int blk) {   // the lane's place in block blk
+    if (direct) return blk * 2048 + (lane & 15) * 128 + ((g4 ^ ((lane >> 1) & 7)) * 16);
+    const int i = lane & 15, row = 8 * g4 + (i >> 2);
+    return row * 2 * width + (((2 * blk + ((i & 3) >> 1)) ^ trans_swap(width, row)) * 16) + (i & 1) * 8;
   };
-  if constexpr (!kDirA)
-#pragma unroll
-    for (int i = 0; i < CB; ++i) ra[i] = trans_read(NT, wc * CB + i);
-  if constexpr (!kDirB)
-#pragma unroll
-    for (int i = 0; i < RB; ++i) rb[i] = trans_read(MT, wr * RB + i);
-  u32x4 a[2][CB], b[2][RB];
-  auto read_trans = [&](const uint8_t* at, int pitch) {
+  int ra = read_base(kDirA, NT, wc * CB), rb = read_base(kDirB, MT, wr * RB);
+  u32x4 a[2][CB], b[RB];
+  auto read_trans = [&](const uint8_t* at, int pitch) {   // (rows r and r + 4 are exchanged alike)
     typedef short s4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4* s4_lds;
     const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((s4_lds)at));
     const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((s4_lds)(at + 4 * pitch)));
     return u32x4{lo.x, lo.y, hi.x, hi.y};
   };
-  auto read = [&](int slot, int s, int i) {   // operand i of sub-step s (constants)
-    const uint8_t* base = slot ? slot1 : slot0;
-    if (i < CB) {
-      if constexpr (kDirA)
-        a[s & 1][i] = *reinterpret_cast<const u32x4*>(base + (wc * CB + i) * 4096 + (read0 ^ (32 * s)));
-      else
-        a[s & 1][i] = read_trans(base + s * 32 * NT + ra[i], 2 * NT);
-    } else {
-      i -= CB;
-      if constexpr (kDirB)
-        b[s & 1][i] = *reinterpret_cast<const u32x4*>(base + S::kA + (wr * RB + i) * 4096 + (read0 ^ (32 * s)));
-      else
-        b[s & 1][i] = read_trans(base + S::kA + s * 32 * MT + rb[i], 2 * MT);
-    }
+  // (transposed: block numbers differ in the bits of 32 i, which nothing else of an address has)
+  auto read_a = [&](int slot, int s, int i) {   // (constants)
+    const uint8_t* base = slot ? a1 : a0;
+    if constexpr (kDirA)
+      a[s][i] = *reinterpret_cast<const u32x4*>(base + i * 2048 + (ra ^ (64 * s)));
+    else
+      a[s][i] = read_trans(base + s * 64 * NT + (ra ^ (32 * i)), 2 * NT);
   };
+  auto read_b = [&](int slot, int s, int i) {
+    const uint8_t* base = slot ? b1 : b0;
+    if constexpr (kDirB)
+      b[i] = *reinterpret_cast<const u32x4*>(base + i * 2048 + (rb ^ (64 * s)));
+    else
+      b[i] = read_trans(base + s * 64 * MT + (rb ^ (32 * i)), 2 * MT);
+  };
+  // Addresses are made anew in each turn: kept, they would take the registers of accumulators.
+  auto renew = [&]() { asm volatile("" : "+v"(ra), "+v"(rb), "+v"(va[0]), "+v"(va[1]), "+v"(vb[0]), "+v"(vb[1])); };
 
-  // ---- MFMAs of a sub-step; behind MFMA m `between(m)`, in the order written -------------------
-  v16f acc[CB][RB];
-  constexpr int M = CB * RB;
-  auto multiply = [&](int s, auto between) {
+  // ---- MFMAs: group j of sub-step s; behind MFMA i `between(i)`, in the order written ------------
+  // They are written in assembly because the compiler gives the result of a 16 x 16 MFMA other
+  // registers than its accumulator had: with all 256 accumulation registers in use it moves them
+  // about and spills. settle() keeps the waits that the compiler would have put between an MFMA and
+  // any other access to its accumulator: 32 wait states, more than any of them needs.
+  v4f acc[CB][RB];
+  auto multiply = [&](int s, int j, auto between) {
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int i = m % CB, j = m / CB;
-      acc[i][j] = Mfma<T>::k16(a[s & 1][i], b[s & 1][j], acc[i][j]);
-      between(m);
+    for (int i = 0; i < CB; ++i) {
+      Mfma<T>::k32_into(acc[i][j], a[s][i], b[j]);
+      between(i);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // part m of things lo .. hi - 1 dealt over the M places
-  auto dealt = [](int m, int lo, int hi, auto f) {
-    const int per = (hi - lo + M - 1) / M;
+  // Beside group j and MFMA i of sub-step s: the reads of the sub-step after it, slot `slot`, sub-step
+  // `to`. The weights two a group; a group's row operand behind its last MFMA, but that of group 0
+  // of a second sub-step, which lies before the barrier, with group 1.
+  auto reads = [&](int slot, int to, int j, int i) {
+    const int first = to == 0 ? 1 : 0;   // the first group that may read
+    constexpr int kPer = (CB + RB - 2) / (RB - 1) > 2 ? (CB + RB - 2) / (RB - 1) : 2;   // weights a group
 #pragma unroll
-    for (int i = lo + m * per; i < lo + (m + 1) * per; ++i)
-      if (i < hi) f(i);
+    for (int w = 0; w < kPer; ++w)
+      if (i == w * CB / kPer && (j - first) * kPer + w < CB) read_a(slot, to, (j - first) * kPer + w);
+    if (first && j == 1 && i == 0) read_b(slot, to, 0);
+    if (i == CB - 1) read_b(slot, to, j);
   };
-  // The MFMAs of a slot's last sub-step, and of the next slot's first three. Behind the barrier
-  // that lies before them the slot SLOT is read: the step after next goes into it. DMA: its loads
-  // are issued in the first of these sub-steps. Else what was fetched before is put there, a part
-  // with each of the four sub-steps, and in the place of each part that of step `next` of the item
-  // aimed at is fetched: every load has a whole slot's time, and the loads are spread evenly (the
-  // CU's L1 takes half of a slot's time for them; in a burst they hold up the waves).
-  auto load_part = [&]<int SLOT>(std::integral_constant<int, SLOT>, int quarter, int m, int next) {
-    if constexpr (DMA) {
-      if (quarter == 0) dealt(m, 0, kLoads, [&](int i) { fetch(SLOT, next, i); });
-    } else {
+  // The loads beside the groups between two barriers, RB - 1 behind the one that sets slot SLOT free
+  // and RB + 1 of the other slot: DMA: those of the step after next are issued first. Else what was
+  // fetched before is put there, a part beside each group, and in the place of each part that of
+  // step `next` of the item aimed at is fetched: every load has a whole slot's time, and the loads
+  // are spread evenly (the CU's L1 takes half of a slot's time for them; in a burst they hold up
+  // the waves).
+  auto loads = [&](int slot, int group, int i, int next) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        if (i * 4 * M / kLoads == quarter * M + m) {
-          put(SLOT, i);
-          fetch(SLOT, next, i);
-        }
+    for (int l = 0; l < kLoads; ++l) {
+      const int place = DMA ? l * RB * CB / kLoads : l * 2 * RB * CB / kLoads;
+      if (place == group * CB + i) {
+        put(slot, l);
+        fetch(slot, next, l);
+      }
     }
   };
-  auto end_slot = [&]<int SLOT>(std::integral_constant<int, SLOT> k, int next) {
-    multiply(3, [&](int m) {
-      dealt(m, 0, CB + RB, [&](int i) { read(SLOT ^ 1, 0, i); });
-      load_part(k, 0, m, next);
-    });
-  };
-  auto begin_slot = [&]<int SLOT>(std::integral_constant<int, SLOT> k, int next) {   // of the other slot than SLOT
+  auto end_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>, int next) {
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
-      multiply(s, [&](int m) {
-        dealt(m, 0, CB + RB, [&](int i) { read(SLOT ^ 1, s + 1, i); });
-        load_part(k, s + 1, m, next);
+    for (int j = 1; j < RB; ++j)
+      multiply(1, j, [&](int i) {
+        reads(SLOT ^ 1, 0, j, i);
+        loads(SLOT, j - 1, i, next);
       });
+  };
+  auto begin_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>, int next) {   // of the other slot than SLOT
+#pragma unroll
+    for (int j = 0; j < RB; ++j)
+      multiply(0, j, [&](int i) {
+        reads(SLOT ^ 1, 1, j, i);
+        loads(SLOT, RB - 1 + j, i, next);
+      });
+    multiply(1, 0, [&](int i) { loads(SLOT, 2 * RB - 1, i, next); });
     slot_barrier<DMA>();
   };
   auto turn = [&](auto k, int next) {
+    renew();
     end_slot(k, next);
     begin_slot(k, next);
   };
@@ -369,11 +344,9 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   fill(0);
   Item16 cur = item(0);
   aim(cur);
-  con_rows = FORM == kWeights ? cur.rows : p.con;
   // DMA: steps 0 and 1 are on their way into the slots. Else step 0 is in its slot, and steps 1 and 2
-  // are where the turn before the first would have left them: step 1's first quarter put and step
-  // 2's fetched.
-  constexpr int kQuarter = (kLoads + 3) / 4;
+  // are where the first part of a turn before the first would have left them: the parts beside its
+  // RB - 1 groups of step 1 put and of step 2 fetched.
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) fetch(0, 0, i);
 #pragma unroll
@@ -383,32 +356,41 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   if constexpr (!DMA) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      if (i * 4 * M / kLoads < M) {
+      if (i * 2 * RB * CB / kLoads < (RB - 1) * CB) {
         put(1, i);
         fetch(1, 2, i);
       }
   }
   slot_barrier<DMA>();
 #pragma unroll
-  for (int i = 0; i < CB + RB; ++i) read(0, 0, i);
+  for (int i = 0; i < CB; ++i) read_a(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < RB; ++i) read_b(0, 0, i);
+  auto settle = [&]() {
+    asm volatile("s_nop 15\n\ts_nop 15" ::);
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+#pragma unroll
+      for (int j = 0; j < RB; ++j) asm volatile("" : "+a"(acc[i][j]));
+    asm volatile("s_nop 15\n\ts_nop 15" ::);
+  };
   auto zero = [&]() {
 #pragma unroll
     for (int i = 0; i < CB; ++i)
 #pragma unroll
       for (int j = 0; j < RB; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    pin(acc);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+    settle();
   };
   zero();
-  begin_slot(k1, 2);
-  for (int64_t n = 0;;) {
+  begin_slot(k1, DMA ? 1 : 2);
+  for (int n = 0;;) {
     // steps of the item, an even number (those behind its last are zeros)
     const int all = max(DMA ? 2 : 4, (steps + 1) / 2 * 2);
     for (int t = 0; t < all - (DMA ? 2 : 4); t += 2) {
       turn(k0, t + (DMA ? 2 : 3));
       turn(k1, t + (DMA ? 3 : 4));
-      pin(acc);
     }
     if constexpr (!DMA) turn(k0, all - 1);
     // the next item's first steps are loaded behind the item's last
@@ -416,52 +398,36 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     if (more && (n + 1) % kList == 0) fill(n + 1);
     const Item16 next = more ? item(n + 1) : cur;
     aim(next);
-    con_rows = FORM == kWeights ? next.rows : p.con;
     if (!more) steps = con_rows = 0;
     if constexpr (!DMA) turn(k1, 0);
     turn(k0, DMA ? 0 : 1);
     end_slot(k1, DMA ? 1 : 2);
-    pin(acc);
-    // ---- output: lane (h, r) holds row r, channels 8 e + 4 h + 0..3 of a block. Lane halves and
-    // quarters change places until a row's 64 bytes are next to one another, in lanes l, l + 16,
-    // l + 32, l + 48 (pieces of 8 or 16 bytes would be write requests of their own to the L2).
+    settle();
+    // ---- output: lane (g, r) holds row r, channels 4 g + 0..3 of a block: 64 neighbouring bytes of
+    // a row in fp32. Of 16-bit values those of two blocks are exchanged until a lane has 8
+    // neighbouring channels and a row's 64 bytes are in lanes l, l + 32, l + 16, l + 48 (pieces of 8
+    // bytes would be write requests of their own to the L2).
     const int rows = FORM == kWeights ? min(MT, p.nr - cur.rt * MT) : cur.rows;
     const int64_t first = FORM == kWeights ? (int64_t)cur.group * p.nr + cur.rt * MT : cur.lo;
 #pragma unroll
     for (int j = 0; j < RB; ++j) {
+      const int row = (wr * RB + j) * 16 + (lane & 15);
+      if (!p.out_fp32) {
+        uint16_t* to = (uint16_t*)p.out + (first + row) * p.nc;
 #pragma unroll
-      for (int i = 0; i < CB; ++i) {
-        const int row = (wr * RB + j) * 32 + (lane & 15), ch = cur.cb * NT + (wc * CB + i) * 32;
-        if (!p.out_fp32) {
-          u32x4 v[2];   // lane (h, r): channels 16 e + 8 h + 0..7
+        for (int i = 0; i < CB; i += 2) {
+          const auto at = [&](int k, int c) { return Mfma<T>::pair(acc[i + k][j][c], acc[i + k][j][c + 1]); };
+          const auto s0 = __builtin_amdgcn_permlane16_swap(at(0, 0), at(1, 0), false, false);
+          const auto s1 = __builtin_amdgcn_permlane16_swap(at(0, 2), at(1, 2), false, false);
+          const int c = cur.cb * NT + (wc * CB + i) * 16 + 16 * (g4 & 1) + 8 * (g4 >> 1);
+          if (row < rows && c < p.nc) *reinterpret_cast<u32x4*>(to + c) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+        }
+      } else {
+        float* to = (float*)p.out + (first + row) * p.nc;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const auto at = [&](int c) { return Mfma<T>::pair(acc[i][j][8 * e + c], acc[i][j][8 * e + c + 1]); };
-            const auto s0 = __builtin_amdgcn_permlane32_swap(at(0), at(4), false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(at(2), at(6), false, false);
-            v[e] = u32x4{s0[0], s1[0], s0[1], s1[1]};
-          }
-          swap_rows(v[0], v[1]);
-          const int c = ch + 16 * ((lane >> 4) & 1) + 8 * h;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (row + 16 * e < rows && c < p.nc)
-              *reinterpret_cast<u32x4*>((uint16_t*)p.out + (first + row + 16 * e) * p.nc + c) = v[e];
-        } else {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            u32x4 v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) v[e][c] = __float_as_uint(acc[i][j][8 * g + 4 * e + c]);
-            swap_rows(v[0], v[1]);
-            const int c = ch + 16 * g + 8 * ((lane >> 4) & 1) + 4 * h;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (row + 16 * e < rows && c < p.nc)
-                *reinterpret_cast<u32x4*>((float*)p.out + (first + row + 16 * e) * p.nc + c) = v[e];
-          }
+        for (int i = 0; i < CB; ++i) {
+          const int c = cur.cb * NT + (wc * CB + i) * 16 + 4 * g4;
+          if (row < rows && c < p.nc) *reinterpret_cast<v4f*>(to + c) = acc[i][j];
         }
       }
     }
@@ -473,11 +439,12 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (15 << 8));   // no direct-to-LDS load outlives the block
 }
 
-template <int FORM, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BLOCKS))) void gmm16_tile_kernel(Tile16Args p) {
+template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(BLOCKS * WAVES / 4))) void gmm16_tile_kernel(Tile16Args p) {
   extern __shared__ __align__(16) uint8_t lds_area[];
-  constexpr int kSlot = Tile16<WC, CB, RB>::kSlot;
-  tile16_body<FORM, WC, CB, RB, ONCE, DMA, T>(p, lds_area, lds_area + kSlot, lds_area + 2 * kSlot);
+  using S = Tile16<WAVES, WC, CB, RB>;
+  uint8_t* const b = lds_area + 2 * S::kA;
+  tile16_body<FORM, WAVES, WC, CB, RB, ONCE, DMA, T>(p, lds_area, lds_area + S::kA, b, b + S::kB, b + 2 * S::kB);
 }
 
 // The device's compute units, rounded up to whole XCDs' shares; the kernel's LDS size set
@@ -500,16 +467,16 @@ inline hipError_t tile16_grid(const void* kernel, int lds, int* grid) {
   return hipSuccess;
 }
 
-template <int FORM, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
+template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
 hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
-  using S = Tile16<WC, CB, RB>;
+  using S = Tile16<WAVES, WC, CB, RB>;
   static_assert(S::kLds * BLOCKS <= 160 * 1024, "LDS of a compute unit");
   static_assert(S::kMT >= 64 || FORM != kWeights, "a transposed operand is 64 wide at least");
   int grid = 0;
-  const auto kernel = gmm16_tile_kernel<FORM, WC, CB, RB, BLOCKS, ONCE, DMA, T>;
+  const auto kernel = gmm16_tile_kernel<FORM, WAVES, WC, CB, RB, BLOCKS, ONCE, DMA, T>;
   hipError_t e = tile16_grid(reinterpret_cast<const void*>(kernel), S::kLds, &grid);
   if (e != hipSuccess) return e;
-  kernel<<<grid * BLOCKS, kThreads, S::kLds, stream>>>(a);
+  kernel<<<grid * BLOCKS, 64 * WAVES, S::kLds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -518,12 +485,12 @@ template <int FORM, typename T>
 hipError_t launch_tile16_as(const Tile16Args& a, int mt, hipStream_t stream) {
   constexpr bool dma = FORM == kForward;   // (the transposing read waits for every direct-to-LDS load in flight)
   switch (mt) {
-    case 256: return launch_tile16<FORM, 2, 4, 4, 1, false, false, T>(a, stream);
-    case 128: return launch_tile16<FORM, 2, 4, 2, 1, false, dma, T>(a, stream);
-    case 64: return launch_tile16<FORM, 4, 1, 2, 2, FORM != kWeights, dma, T>(a, stream);
+    case 256: return launch_tile16<FORM, 4, 2, 8, 8, 1, false, false, T>(a, stream);
+    case 128: return launch_tile16<FORM, 4, 2, 8, 4, 1, false, dma, T>(a, stream);
+    case 64: return launch_tile16<FORM, 4, 4, 2, 4, 2, FORM != kWeights, dma, T>(a, stream);
     default:
       if constexpr (FORM == kWeights) return hipErrorInvalidValue;
-      else return launch_tile16<FORM, 4, 1, 1, 3, true, dma, T>(a, stream);
+      else return launch_tile16<FORM, 4, 4, 2, 2, 3, true, dma, T>(a, stream);
   }
 }
 
