@@ -144,40 +144,34 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   auto steps_of = [&](const Item16& it) { return ((FORM == kWeights ? it.rows : p.con) + kCon - 1) / kCon; };
 
   // ---- loads: load i of a wave and operand fills 1 KB of it, lane l the 16 bytes at 16 l -------
-  // direct: 8 rows of 128 bytes; transposed: 1024 / (2 NT) rows of the contraction. Which chunk
-  // belongs at a lane's place depends on a few bits of the load's number only: what does is kept
-  // in registers, the rest is scalar.
-  constexpr int kRowsA = kDirA ? 8 : 512 / NT, kRowsB = kDirB ? 8 : 512 / MT;   // rows of a load
+  // direct: 8 rows of 128 bytes; transposed: 1024 / (2 NT) rows of the contraction
+  const int pitch_a = 2 * (kDirA ? p.con : p.nc), pitch_b = 2 * (kDirB ? p.con : p.nr);
+  const int tail_step = p.con % kCon ? p.con / kCon : -1;   // direct: the step that the contraction ends in
   auto trans_swap = [](int width, int row) {   // what the chunks of a row of `width` channels are exchanged by
     return 4 * (width == 64 ? (row >> 1) & 1 : row & 3) + 2 * ((row >> 3) & 1);
   };
-  int va[2], vb[2], ta[2] = {0, 0}, tb[2] = {0, 0};
-  const int tail_step = p.con % kCon ? p.con / kCon : -1;
-  auto lane_parts = [&](bool direct, int width, int per_wave, int (&v)[2], int (&t)[2], int pitch) {
-    if (direct) {   // v: the lane's place in an even and an odd load; t: what moves it outside in the step the contraction ends in
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int chunk = (lane & 7) ^ ((((wave * per_wave + i) * 8 + (lane >> 3)) >> 1) & 7);
-        v[i] = (lane >> 3) * pitch + 16 * chunk;
-        t[i] = 8 * chunk >= p.con % kCon ? kOutside : 0;
-      }
-    } else {        // v[0]: its row, v[1]: its chunk, but for the bits that load_swap exchanges
-      v[0] = lane / (width / 8) * pitch;
-      v[1] = 16 * (lane % (width / 8) ^ trans_swap(width, wave * per_wave * (512 / width) + lane / (width / 8)));
-    }
+  auto direct_chunk = [&](int load) { return (lane & 7) ^ (((load * 8 + (lane >> 3)) >> 1) & 7); };
+  auto lane_place = [&](bool direct, int width, int pitch, int load) {
+    if (direct) return (load * 8 + (lane >> 3)) * pitch + 16 * direct_chunk(load);
+    const int at = load * 64 + lane, row = at / (width / 8);
+    return row * pitch + 16 * (at % (width / 8) ^ trans_swap(width, row));
   };
-  // (a wave's loads begin at a row that is a multiple of 8, so their rows' bits are exchanged independently)
-  auto load_swap = [&](int width, int i) { return 16 * trans_swap(width, i * (512 / width)); };
-  static_assert(kDirA || S::kLA * kRowsA % 8 == 0, "a wave's rows of a transposed operand");
-  static_assert(kDirB || S::kLB * kRowsB % 8 == 0, "a wave's rows of a transposed operand");
-  const int pitch_a = 2 * (kDirA ? p.con : p.nc), pitch_b = 2 * (kDirB ? p.con : p.nr);
-  lane_parts(kDirA, NT, S::kLA, va, ta, pitch_a);
-  lane_parts(kDirB, MT, S::kLB, vb, tb, pitch_b);
+  int va[S::kLA], vb[S::kLB];
+#pragma unroll
+  for (int i = 0; i < S::kLA; ++i) va[i] = lane_place(kDirA, NT, pitch_a, wave * S::kLA + i);
+#pragma unroll
+  for (int i = 0; i < S::kLB; ++i) vb[i] = lane_place(kDirB, MT, pitch_b, wave * S::kLB + i);
+  int ta[2], tb[2];   // what moves a lane of an even and an odd load outside in that step
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ta[i] = kDirA && 8 * direct_chunk(wave * S::kLA + i) >= p.con % kCon ? kOutside : 0;
+    tb[i] = kDirB && 8 * direct_chunk(wave * S::kLB + i) >= p.con % kCon ? kOutside : 0;
+  }
 
   // The item being loaded: buffers of exactly what belongs to it (the rest reads as zeros,
   // without memory traffic).
   const uint8_t *pa, *pb;
-  int na, nb, steps, con_rows;   // direct: rows; transposed: bytes cut off a row's front (its first channel)
+  int na, nb, steps, con_rows;   // direct: bytes; transposed: bytes cut off a row's front (its first channel)
   auto aim = [&](const Item16& it) {
     steps = steps_of(it);
     con_rows = FORM == kWeights ? it.rows : p.con;
@@ -188,50 +182,49 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
       nb = 2 * it.rt * MT;
     } else {
       pb = reinterpret_cast<const uint8_t*>(p.row + (int64_t)it.lo * p.con);
-      nb = it.rows;
+      nb = it.rows * pitch_b;
       const uint16_t* w = p.chan + (int64_t)it.group * p.nc * p.con;
       if constexpr (kDirA) {
         pa = reinterpret_cast<const uint8_t*>(w + (int64_t)it.cb * NT * p.con);
-        na = min(NT, p.nc - it.cb * NT);
+        na = min(NT, p.nc - it.cb * NT) * pitch_a;
       } else {
         pa = reinterpret_cast<const uint8_t*>(w + it.cb * NT);
         na = 2 * it.cb * NT;
       }
     }
   };
-  // load i of an operand's step `step`: its buffer and the lane's place in it
-  struct Source {
-    __amdgpu_buffer_rsrc_t r;
-    int voff, soff;
-  };
-  auto source_of = [&](bool direct, int width, const uint8_t* base, int n, int pitch, const int (&v)[2], const int (&t)[2],
-                       int row0, int step, int i) {
-    if (direct) {   // rows row0 .. row0 + 7 of the operand's n
-      const int left = step < steps ? max(n - row0, 0) : 0;
-      return Source{buffer_of(base + (int64_t)row0 * pitch, left * pitch), v[i & 1] + (step == tail_step ? t[i & 1] : 0),
-                    step * 2 * kCon};
+  // The step being loaded
+  const uint8_t *qa, *qb;
+  int ma, mb, soff, ua[2] = {0, 0}, ub[2] = {0, 0};
+  auto aim_step = [&](int step) {
+    const bool in = step < steps, tail = step == tail_step;
+    const int left = min(max(con_rows - step * kCon, 0), kCon);
+    soff = kDirB ? step * 2 * kCon : 0;
+    qa = kDirA ? pa : pa + (int64_t)step * kCon * pitch_a;
+    qb = kDirB ? pb : pb + (int64_t)step * kCon * pitch_b;
+    ma = kDirA ? (in ? na : 0) : left > 0 ? left * pitch_a - na : 0;
+    mb = kDirB ? (in ? nb : 0) : left > 0 ? left * pitch_b - nb : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (kDirA) ua[i] = tail ? ta[i] : 0;
+      if constexpr (kDirB) ub[i] = tail ? tb[i] : 0;
     }
-    const int left = con_rows - step * kCon - row0;
-    return Source{buffer_of(base + (int64_t)(step * kCon + row0) * pitch, left > 0 ? min(left, kCon) * pitch - n : 0),
-                  (v[1] ^ load_swap(width, i)) + v[0], 0};
-  };
-  auto source = [&](int step, int i) {
-    return i < S::kLA ? source_of(kDirA, NT, pa, na, pitch_a, va, ta, (wave * S::kLA + i) * kRowsA, step, i)
-                      : source_of(kDirB, MT, pb, nb, pitch_b, vb, tb, (wave * S::kLB + i - S::kLA) * kRowsB, step, i - S::kLA);
   };
   auto place = [&](int slot, int i) {   // of load i in a slot (a constant): 1 KB
     return i < S::kLA ? (slot ? a1 : a0) + (wave * S::kLA + i) * 1024 : (slot ? b1 : b0) + (wave * S::kLB + i - S::kLA) * 1024;
   };
   u32x4 held[DMA ? 1 : S::kLA + S::kLB];
-  auto fetch = [&](int slot, int step, int i) {
-    const Source f = source(step, i);
-    const bool once = ONCE && i < S::kLA;
+  auto fetch = [&](int slot, int i) {
+    const bool chan = i < S::kLA;
+    const int k = chan ? i : i - S::kLA;
+    const auto r = buffer_of(chan ? qa : qb, chan ? ma : mb);
+    const int voff = chan ? va[k] + ua[k & 1] : vb[k] + ub[k & 1], so = chan && !kDirA ? 0 : soff;
     if constexpr (DMA) {
-      if (once) __builtin_amdgcn_raw_ptr_buffer_load_lds(f.r, (lds_ptr)place(slot, i), 16, f.voff, f.soff, 0, 2);
-      else __builtin_amdgcn_raw_ptr_buffer_load_lds(f.r, (lds_ptr)place(slot, i), 16, f.voff, f.soff, 0, 0);
+      if (ONCE && chan) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)place(slot, i), 16, voff, so, 0, 2);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)place(slot, i), 16, voff, so, 0, 0);
     } else {
-      if (once) held[i] = __builtin_amdgcn_raw_buffer_load_b128(f.r, f.voff, f.soff, 2);
-      else held[i] = __builtin_amdgcn_raw_buffer_load_b128(f.r, f.voff, f.soff, 0);
+      if (ONCE && chan) held[i] = __builtin_amdgcn_raw_buffer_load_b128(r, voff, so, 2);
+      else held[i] = __builtin_amdgcn_raw_buffer_load_b128(r, voff, so, 0);
     }
   };
   auto put = [&](int slot, int i) {
@@ -270,8 +263,8 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     else
       b[i] = read_trans(base + s * 64 * MT + (rb ^ (32 * i)), 2 * MT);
   };
-  // Addresses are made anew in each turn: kept, they would take the registers of accumulators.
-  auto renew = [&]() { asm volatile("" : "+v"(ra), "+v"(rb), "+v"(va[0]), "+v"(va[1]), "+v"(vb[0]), "+v"(vb[1])); };
+  // Addresses are made anew in each turn: kept, they would take the registers of operands.
+  auto renew = [&]() { asm volatile("" : "+v"(ra), "+v"(rb)); };
 
   // ---- MFMAs: group j of sub-step s; behind MFMA i `between(i)`, in the order written ------------
   // They are written in assembly because the compiler gives the result of a 16 x 16 MFMA other
@@ -295,48 +288,51 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     constexpr int kPer = (CB + RB - 2) / (RB - 1) > 2 ? (CB + RB - 2) / (RB - 1) : 2;   // weights a group
 #pragma unroll
     for (int w = 0; w < kPer; ++w)
-      if (i == w * CB / kPer && (j - first) * kPer + w < CB) read_a(slot, to, (j - first) * kPer + w);
+      if (i == (2 * w + 1) * CB / (2 * kPer + 2) && (j - first) * kPer + w < CB) read_a(slot, to, (j - first) * kPer + w);
     if (first && j == 1 && i == 0) read_b(slot, to, 0);
     if (i == CB - 1) read_b(slot, to, j);
   };
   // The loads beside the groups between two barriers, RB - 1 behind the one that sets slot SLOT free
-  // and RB + 1 of the other slot: DMA: those of the step after next are issued first. Else what was
-  // fetched before is put there, a part beside each group, and in the place of each part that of
-  // step `next` of the item aimed at is fetched: every load has a whole slot's time, and the loads
+  // and RB + 1 of the other slot: DMA: those of the step after next are issued in the first half.
+  // Else what was fetched before is put there, a part beside each group, and in the place of each
+  // part that of the step aimed at is fetched: every load has a whole slot's time, and the loads
   // are spread evenly (the CU's L1 takes half of a slot's time for them; in a burst they hold up
-  // the waves).
-  auto loads = [&](int slot, int group, int i, int next) {
+  // the waves). An MFMA takes the time of four other instructions: more between two of them would
+  // leave the matrix core idle.
+  auto loads = [&](int slot, int group, int i) {
+    // (in groups of eight MFMAs away from the reads, and the two parts of a load behind different ones)
+    constexpr int kPlaces = (DMA ? 1 : 2) * RB * CB, kBack = CB >= 8 ? 4 : 0, kFetch = CB >= 8 ? 1 : 0;
+    static_assert((kLoads - 1) * kPlaces / kLoads + kBack + kFetch < 2 * RB * CB, "every load has its place");
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
-      const int place = DMA ? l * RB * CB / kLoads : l * 2 * RB * CB / kLoads;
-      if (place == group * CB + i) {
-        put(slot, l);
-        fetch(slot, next, l);
-      }
+      const int at = l * kPlaces / kLoads + kBack, here = group * CB + i;
+      if (at == here) put(slot, l);
+      if (at + kFetch == here) fetch(slot, l);
     }
   };
-  auto end_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>, int next) {
+  auto end_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>) {
 #pragma unroll
     for (int j = 1; j < RB; ++j)
       multiply(1, j, [&](int i) {
         reads(SLOT ^ 1, 0, j, i);
-        loads(SLOT, j - 1, i, next);
+        loads(SLOT, j - 1, i);
       });
   };
-  auto begin_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>, int next) {   // of the other slot than SLOT
+  auto begin_slot = [&]<int SLOT>(std::integral_constant<int, SLOT>) {   // of the other slot than SLOT
 #pragma unroll
     for (int j = 0; j < RB; ++j)
       multiply(0, j, [&](int i) {
         reads(SLOT ^ 1, 1, j, i);
-        loads(SLOT, RB - 1 + j, i, next);
+        loads(SLOT, RB - 1 + j, i);
       });
-    multiply(1, 0, [&](int i) { loads(SLOT, 2 * RB - 1, i, next); });
+    multiply(1, 0, [&](int i) { loads(SLOT, 2 * RB - 1, i); });
     slot_barrier<DMA>();
   };
   auto turn = [&](auto k, int next) {
     renew();
-    end_slot(k, next);
-    begin_slot(k, next);
+    aim_step(next);
+    end_slot(k);
+    begin_slot(k);
   };
   constexpr std::integral_constant<int, 0> k0{};
   constexpr std::integral_constant<int, 1> k1{};
@@ -347,19 +343,20 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   // DMA: steps 0 and 1 are on their way into the slots. Else step 0 is in its slot, and steps 1 and 2
   // are where the first part of a turn before the first would have left them: the parts beside its
   // RB - 1 groups of step 1 put and of step 2 fetched.
+  aim_step(0);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(0, 0, i);
+  for (int i = 0; i < kLoads; ++i) fetch(0, i);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) put(0, i);
+  aim_step(1);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(1, 1, i);
+  for (int i = 0; i < kLoads; ++i) fetch(1, i);
   if constexpr (!DMA) {
+    aim_step(2);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      if (i * 2 * RB * CB / kLoads < (RB - 1) * CB) {
-        put(1, i);
-        fetch(1, 2, i);
-      }
+    for (int g = 0; g < RB - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < CB; ++i) loads(1, g, i);
   }
   slot_barrier<DMA>();
 #pragma unroll
@@ -384,7 +381,7 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     settle();
   };
   zero();
-  begin_slot(k1, DMA ? 1 : 2);
+  begin_slot(k1);
   for (int n = 0;;) {
     // steps of the item, an even number (those behind its last are zeros)
     const int all = max(DMA ? 2 : 4, (steps + 1) / 2 * 2);
@@ -401,7 +398,8 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     if (!more) steps = con_rows = 0;
     if constexpr (!DMA) turn(k1, 0);
     turn(k0, DMA ? 0 : 1);
-    end_slot(k1, DMA ? 1 : 2);
+    aim_step(DMA ? 1 : 2);
+    end_slot(k1);
     settle();
     // ---- output: lane (g, r) holds row r, channels 4 g + 0..3 of a block: 64 neighbouring bytes of
     // a row in fp32. Of 16-bit values those of two blocks are exchanged until a lane has 8
@@ -434,7 +432,7 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     if (++n >= count) break;
     cur = next;
     zero();
-    begin_slot(k1, DMA ? 1 : 2);
+    begin_slot(k1);
   }
   __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (15 << 8));   // no direct-to-LDS load outlives the block
 }
