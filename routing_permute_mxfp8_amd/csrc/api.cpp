@@ -506,7 +506,12 @@ moe::Gmm16Params gmm16_params(int dtype, int out_dtype, int64_t rows, const int3
   return p;
 }
 
-void carve_gmm16(Carver&, moe::Gmm16Params&) {}
+void carve_gmm16(Carver& cv, moe::Gmm16Params& p) {
+  moe::gmm16_plan(p);
+  if (p.part_floats) p.part = cv.take<float>(p.part_floats);
+  if (p.copy_a) p.a16 = cv.take<uint16_t>(p.copy_a);
+  if (p.copy_b) p.b16 = cv.take<uint16_t>(p.copy_b);
+}
 
 moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!p.out || (p.rows > 0 && (!p.a || !p.b)))

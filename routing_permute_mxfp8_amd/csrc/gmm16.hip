@@ -130,23 +130,72 @@ hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
   return p.out_fp32 ? launch_any<T, float>(p, stream) : launch_any<T, uint16_t>(p, stream);
 }
 
+// Rows of a matrix of 16-bit elements copied to rows of `pitch` elements, a multiple of 8, with zeros
+// behind: 8 elements of the copy a thread.
+__global__ __launch_bounds__(256) void pad16_kernel(const uint16_t* __restrict__ from, int64_t rows, int cols,
+                                                    uint16_t* __restrict__ to, int pitch) {
+  const int per = pitch / 8;
+  const int64_t all = rows * per;
+  for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < all; v += (int64_t)gridDim.x * 256) {
+    const int64_t r = v / per;
+    const int c = (int)(v - r * per) * 8;
+    uint16_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? from[r * cols + c + i] : (uint16_t)0;
+    u32x4 u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
+    reinterpret_cast<u32x4*>(to)[v] = u;
+  }
+}
+
+hipError_t launch_pad16(const void* from, int64_t rows, int cols, uint16_t* to, int pitch, hipStream_t stream) {
+  const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
+  if (blocks == 0) return hipSuccess;
+  pad16_kernel<<<(unsigned)std::min<int64_t>(blocks, 1 << 20), 256, 0, stream>>>((const uint16_t*)from, rows, cols, to, pitch);
+  return hipGetLastError();
+}
+
 int tile_rows(const Gmm16Params& p) {
-  if (p.wgrad) return 256;
   const int64_t per = (p.rows + p.groups - 1) / p.groups;
+  if (p.wgrad) return 256;
   return per <= 20 ? 32 : per <= 48 ? 64 : per <= 100 ? 128 : 256;
 }
 
 }  // namespace
 
+void gmm16_plan(Gmm16Params& p) {
+  p.mt = tile_rows(p);
+  const int64_t rows_b = p.wgrad ? p.rows : (int64_t)p.groups * (p.trans ? p.k : p.n);
+  const int cols_a = p.wgrad ? p.n : p.k, cols_b = p.wgrad || !p.trans ? p.k : p.n;
+  p.pitch_a = (cols_a + 7) / 8 * 8;
+  p.pitch_b = (cols_b + 7) / 8 * 8;
+  p.copy_a = p.pitch_a != cols_a ? (size_t)p.rows * p.pitch_a : 0;
+  p.copy_b = p.pitch_b != cols_b ? (size_t)rows_b * p.pitch_b : 0;
+  const int nt = p.mt >= 128 ? 256 : 128, blocks = p.mt >= 128 ? 1 : p.mt == 64 ? 2 : 3;
+  p.gain = 16;
+  const int64_t steps = p.wgrad ? p.rows / p.groups / 64 : (p.k + 63) / 64;
+  p.part_floats = steps >= 2 * p.gain || steps >= 8 ? (size_t)kTile16Units * blocks * p.mt * nt : 0;
+}
+
 hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {
   if (p.rows <= 0 && !p.wgrad) return hipSuccess;
   const auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  if (p.n % 8 == 0 && p.k % 8 == 0 && on16(p.a) && on16(p.b) && on16(p.out)) {
-    Gmm16Params q = p;
-    q.mt = tile_rows(p);
-    if (q.mt) return p.wgrad ? launch_gmm16_weights(q, stream) : p.trans ? launch_gmm16_transposed(q, stream) : launch_gmm16_forward(q, stream);
+  if (!p.mt || !((p.copy_a || on16(p.a)) && (p.copy_b || on16(p.b))))
+    return p.half ? launch_as<_Float16>(p, stream) : launch_as<__bf16>(p, stream);
+  Gmm16Params q = p;
+  hipError_t e;
+  if (p.copy_a) {
+    if ((e = launch_pad16(p.a, p.rows, p.wgrad ? p.n : p.k, p.a16, p.pitch_a, stream)) != hipSuccess) return e;
+    q.a = p.a16;
   }
-  return p.half ? launch_as<_Float16>(p, stream) : launch_as<__bf16>(p, stream);
+  if (p.copy_b) {
+    const int64_t rows = p.wgrad ? p.rows : (int64_t)p.groups * (p.trans ? p.k : p.n);
+    if ((e = launch_pad16(p.b, rows, p.wgrad || !p.trans ? p.k : p.n, p.b16, p.pitch_b, stream)) != hipSuccess) return e;
+    q.b = p.b16;
+  }
+  q.odd = !on16(p.out) || (p.wgrad ? p.k : p.n) % (p.out_fp32 ? 4 : 8) != 0;
+  return p.wgrad ? launch_gmm16_weights(q, stream) : p.trans ? launch_gmm16_transposed(q, stream) : launch_gmm16_forward(q, stream);
 }
 
 }  // namespace moe

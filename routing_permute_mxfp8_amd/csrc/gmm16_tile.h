@@ -42,12 +42,16 @@ enum Form { kForward, kTransposed, kWeights };
 
 struct Tile16Args {
   const uint16_t* row;   // what makes the output's rows: [rows, con], kWeights: [rows, nr]
-  const uint16_t* chan;  // and its channels: [groups, nc, con], [groups, con, nc], kWeights: [rows, nc]
+  const uint16_t* chan;  // and its channels: [groups, nc, con], [groups, con_t, nc], kWeights: [rows, nc]
+  int pitch_row, pitch_chan;   // elements from one row of them to the next, multiples of 8
   const int32_t* off;
   int groups, rows;
-  int nc, nr, con;       // nr: kWeights only, con: not there
+  int nc, nr;            // nr: kWeights only
+  int con, con_t;        // contraction, of a direct operand (with zeros up to a multiple of 8) and of a transposed one
   bool out_fp32;
   void* out;
+  float* part;           // workspace of shared items: a tile for each block, or null: items are not shared
+  int steps, gain;       // steps of an item (kWeights: on average); how many have to be saved for an item to be shared
 };
 
 template <int WAVES, int WC, int CB, int RB>
@@ -71,15 +75,127 @@ __device__ __forceinline__ void slot_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// ---- which item a block works at ------------------------------------------------------------
+// The items are the output's tiles by their channel blocks. Each XCD takes a contiguous share of
+// them, dealt to its blocks in turn. What is left for a last, part-filled round is shared: the
+// contraction of each of these items is cut into `parts`, one for each block; the blocks leave
+// fp32 tiles, which gmm16_join_kernel adds in order.
+struct Share {
+  int64_t begin;          // the XCD's first item
+  int full, rem, parts;   // whole rounds, items behind them, blocks an item of those
+};
+__device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int xcd, int per) {
+  Share s;
+  s.begin = total * xcd / 8;
+  const int64_t n = total * (xcd + 1) / 8 - s.begin;
+  s.full = (int)(n / per);
+  s.rem = (int)(n - (int64_t)s.full * per);
+  s.parts = s.rem ? min(per / s.rem, p.steps / 4) : 1;   // (a part has four steps at least)
+  if (!p.part || s.parts < 2 || p.steps - (p.steps + s.parts - 1) / s.parts < p.gain) s.parts = 1;
+  return s;
+}
+
+// Item `it`: (group, first row, rows, tile and channel block). Four row tiles run through the
+// channel blocks together, so that the items in flight on one XCD share both operands in its L2.
+template <int FORM, int MT>
+__device__ __forceinline__ int4 describe16(const Tile16Args& p, const int* ends, int tiles, int nrt, int ncb, int64_t it) {
+  int64_t base = 0;
+  int height = tiles;          // row tiles that are numbered together
+  int g = 0;
+  if constexpr (FORM == kWeights) {
+    g = (int)(it / ((int64_t)nrt * ncb));
+    base = (int64_t)g * nrt * ncb;
+    height = nrt;
+  }
+  const int64_t in_all = it - base;
+  const int64_t block = in_all / (4 * (int64_t)ncb);
+  const int in = (int)(in_all - block * 4 * ncb);
+  const int width = min(4, height - 4 * (int)block);
+  const int cb = in / width, t = 4 * (int)block + in - cb * width;
+  int lo, hi;
+  if constexpr (FORM == kWeights) {
+    group_rows(p.off, g, p.rows, &lo, &hi);
+    return make_int4(g, lo, hi - lo, t * ncb + cb);
+  } else {
+    g = group_of_tile(ends, p.groups, t);
+    group_rows(p.off, g, p.rows, &lo, &hi);
+    const int row0 = lo + (t - (g > 0 ? ends[g - 1] : 0)) * MT;
+    return make_int4(g, row0, min(MT, hi - row0), cb);
+  }
+}
+
+// Transposed: what the chunks of a row of `width` channels are exchanged by.
+__device__ constexpr int trans_swap(int width, int row) {
+  return 4 * (width == 64 ? (row >> 1) & 1 : row & 3) + 2 * ((row >> 3) & 1);
+}
+// The first load of a wave whose lanes' chunks are exchanged as load i's are (a wave's loads begin at a
+// row that is a multiple of 8): their places differ by whole rows only.
+__device__ constexpr int load_like(bool direct, int width, int i) {
+  if (direct) return i & 1;
+  for (int k = 0; k < i; ++k)
+    if (trans_swap(width, k * (512 / width)) == trans_swap(width, i * (512 / width))) return k;
+  return i;
+}
+
 struct Item16 {
   int group, lo, rows;   // rows [lo, lo + rows): the tile's (kWeights: the group's, which are summed)
   int rt, cb;            // channel block; row tile of the output (kWeights)
 };
+template <int FORM>
+__device__ __forceinline__ Item16 item16(const int4& v, int ncb) {
+  Item16 r;
+  r.group = __builtin_amdgcn_readfirstlane(v.x);
+  r.lo = __builtin_amdgcn_readfirstlane(v.y);
+  r.rows = __builtin_amdgcn_readfirstlane(v.z);
+  const int w = __builtin_amdgcn_readfirstlane(v.w);
+  r.rt = FORM == kWeights ? w / ncb : 0;
+  r.cb = w - r.rt * ncb;
+  return r;
+}
+
+// ---- output -----------------------------------------------------------------------------------
+// A row block's accumulators: lane (g, r) holds row r, channels 4 g + 0..3 of each 16-channel block: 64
+// neighbouring bytes of a row in fp32. Of 16-bit values those of two blocks are exchanged until a
+// lane has 8 neighbouring channels and a row's 64 bytes are in lanes l, l + 32, l + 16, l + 48
+// (pieces of 8 bytes would be write requests of their own to the L2). ODD: the output's rows are no
+// whole 16-byte vectors, and stored by elements.
+template <bool ODD, typename T, int CB>
+__device__ __forceinline__ void store_rows(const Tile16Args& p, const v4f (&acc)[CB], bool valid, int64_t row, int c0) {
+  const int g4 = (threadIdx.x & 63) >> 4;
+  if constexpr (ODD) {
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = c0 + 16 * i + 4 * g4 + e;
+        if (!valid || c >= p.nc) continue;
+        if (p.out_fp32) ((float*)p.out)[row * p.nc + c] = acc[i][e];
+        else ((uint16_t*)p.out)[row * p.nc + c] = Mfma<T>::template out<uint16_t>(acc[i][e]);
+      }
+  } else if (p.out_fp32) {
+    float* to = (float*)p.out + row * p.nc;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      const int c = c0 + 16 * i + 4 * g4;
+      if (valid && c < p.nc) *reinterpret_cast<v4f*>(to + c) = acc[i];
+    }
+  } else {
+    uint16_t* to = (uint16_t*)p.out + row * p.nc;
+#pragma unroll
+    for (int i = 0; i < CB; i += 2) {
+      const auto at = [&](int k, int c) { return Mfma<T>::pair(acc[i + k][c], acc[i + k][c + 1]); };
+      const auto s0 = __builtin_amdgcn_permlane16_swap(at(0, 0), at(1, 0), false, false);
+      const auto s1 = __builtin_amdgcn_permlane16_swap(at(0, 2), at(1, 2), false, false);
+      const int c = c0 + 16 * i + 16 * (g4 & 1) + 8 * (g4 >> 1);
+      if (valid && c < p.nc) *reinterpret_cast<u32x4*>(to + c) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+    }
+  }
+}
 
 // The body gets the slots (both of the channels' operand, both of the rows') and the rest of LDS as
 // restrict pointers, which is what they are: apart. A slot is never read while loads into it are in flight, and so the compiler, which
 // makes an LDS read wait for the direct-to-LDS loads that may write there, has nothing to wait for.
-template <int FORM, int WAVES, int WC, int CB, int RB, bool ONCE, bool DMA, typename T>
+template <int FORM, int WAVES, int WC, int CB, int RB, bool ONCE, bool DMA, bool ODD, typename T>
 __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __restrict__ a0, uint8_t* __restrict__ a1,
                                             uint8_t* __restrict__ b0, uint8_t* __restrict__ b1,
                                             uint8_t* __restrict__ lds) {
@@ -92,64 +208,27 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   int* const ends = reinterpret_cast<int*>(lds + S::kEnds);
   int4* const list = reinterpret_cast<int4*>(lds + S::kItems);
 
-  // ---- items: each XCD takes a contiguous share, dealt to its blocks in turn ----------------
   const int tiles = FORM == kWeights ? p.groups * nrt : count_tiles<MT, WAVES>(p.off, p.groups, p.rows, ends, reinterpret_cast<int*>(list));
-  const int64_t total = (int64_t)tiles * ncb;
-  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
-  const int64_t begin = total * xcd / 8 + (blockIdx.x >> 3), end = total * (xcd + 1) / 8;
-  if (begin >= end) return;   // the whole block
-  const int count = (int)((end - begin + per - 1) / per);
-  // Item `it`: four row tiles run through the channel blocks together, so that the items in flight
-  // on one XCD share both operands in its L2.
-  auto describe = [&](int64_t it) {
-    int64_t base = 0;
-    int height = tiles;          // row tiles that are numbered together
-    int g = 0;
-    if constexpr (FORM == kWeights) {
-      g = (int)(it / ((int64_t)nrt * ncb));
-      base = (int64_t)g * nrt * ncb;
-      height = nrt;
-    }
-    const int64_t in_all = it - base;
-    const int block = (int)(in_all / (4 * ncb)), in = (int)(in_all - (int64_t)block * 4 * ncb);
-    const int width = min(4, height - 4 * block);
-    const int cb = in / width, t = 4 * block + in - cb * width;
-    int lo, hi;
-    if constexpr (FORM == kWeights) {
-      group_rows(p.off, g, p.rows, &lo, &hi);
-      return make_int4(g, lo, hi - lo, t * ncb + cb);
-    } else {
-      g = group_of_tile(ends, p.groups, t);
-      group_rows(p.off, g, p.rows, &lo, &hi);
-      const int row0 = lo + (t - (g > 0 ? ends[g - 1] : 0)) * MT;
-      return make_int4(g, row0, min(MT, hi - row0), cb);
-    }
-  };
+  const int xcd = blockIdx.x & 7, slot_in = blockIdx.x >> 3, per = gridDim.x >> 3;
+  const Share share = share_of(p, (int64_t)tiles * ncb, xcd, per);
+  const bool shared = share.parts > 1 && slot_in < share.rem * share.parts;   // the block's last item is a part of one
+  const int count = share.full + (share.parts > 1 ? shared : slot_in < share.rem);
+  if (count == 0) return;   // the whole block
   auto fill = [&](int first) {   // list[i] = this block's item first + i
     __syncthreads();
-    if (tid < kList && first + tid < count) list[tid] = describe(begin + (int64_t)(first + tid) * per);
+    if (tid < kList && first + tid < count) {
+      const int n = first + tid;
+      const int in = n == share.full && shared ? slot_in % share.rem : slot_in;
+      list[tid] = describe16<FORM, MT>(p, ends, tiles, nrt, ncb, share.begin + (int64_t)n * per + in);
+    }
     __syncthreads();
   };
-  auto item = [&](int i) {
-    const int4 v = list[i % kList];
-    Item16 r;
-    r.group = __builtin_amdgcn_readfirstlane(v.x);
-    r.lo = __builtin_amdgcn_readfirstlane(v.y);
-    r.rows = __builtin_amdgcn_readfirstlane(v.z);
-    const int w = __builtin_amdgcn_readfirstlane(v.w);
-    r.rt = FORM == kWeights ? w / ncb : 0;
-    r.cb = w - r.rt * ncb;
-    return r;
-  };
-  auto steps_of = [&](const Item16& it) { return ((FORM == kWeights ? it.rows : p.con) + kCon - 1) / kCon; };
+  auto item = [&](int i) { return item16<FORM>(list[i % kList], ncb); };
 
   // ---- loads: load i of a wave and operand fills 1 KB of it, lane l the 16 bytes at 16 l -------
   // direct: 8 rows of 128 bytes; transposed: 1024 / (2 NT) rows of the contraction
-  const int pitch_a = 2 * (kDirA ? p.con : p.nc), pitch_b = 2 * (kDirB ? p.con : p.nr);
+  const int pitch_a = 2 * p.pitch_chan, pitch_b = 2 * p.pitch_row;
   const int tail_step = p.con % kCon ? p.con / kCon : -1;   // direct: the step that the contraction ends in
-  auto trans_swap = [](int width, int row) {   // what the chunks of a row of `width` channels are exchanged by
-    return 4 * (width == 64 ? (row >> 1) & 1 : row & 3) + 2 * ((row >> 3) & 1);
-  };
   auto direct_chunk = [&](int load) { return (lane & 7) ^ (((load * 8 + (lane >> 3)) >> 1) & 7); };
   auto lane_place = [&](bool direct, int width, int pitch, int load) {
     if (direct) return (load * 8 + (lane >> 3)) * pitch + 16 * direct_chunk(load);
@@ -170,45 +249,87 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
 
   // The item being loaded: buffers of exactly what belongs to it (the rest reads as zeros,
   // without memory traffic).
-  const uint8_t *pa, *pb;
-  int na, nb, steps, con_rows;   // direct: bytes; transposed: bytes cut off a row's front (its first channel)
-  auto aim = [&](const Item16& it) {
-    steps = steps_of(it);
-    con_rows = FORM == kWeights ? it.rows : p.con;
+  struct Step {
+    const uint8_t *a, *b;   // the step's operands (direct: the item's)
+    int ma, mb;             // bytes from there on that belong to the item
+    int left;               // transposed: rows of the contraction from here on
+    int steps, soff;        // steps from here on; direct: where the step begins in a row
+  };
+  Step st, nx;              // the step being loaded and the one after it
+  int na, nb;               // direct: the item's bytes; transposed: bytes cut off a row's front (its first channel)
+  const int stride_a = kCon * pitch_a, stride_b = kCon * pitch_b;
+  auto rows_bytes = [&](int left, int pitch, int cut) { return max(min(left, kCon) * pitch - cut, 0); };   // (left may be negative)
+  auto aim = [&](const Item16& it, bool part, bool there) {   // nx: the item's first step; !there: zeros
+    const int con_rows = FORM == kWeights ? it.rows : p.con_t;
+    const int all = ((FORM == kWeights ? it.rows : p.con) + kCon - 1) / kCon;
+    int first = 0, steps = there ? all : 0;
+    if (part) {
+      const int each = (all + share.parts - 1) / share.parts;
+      first = min(all, slot_in / share.rem * each);
+      steps = min(all - first, each);
+    }
+    nx.steps = steps;
+    nx.soff = first * 2 * kCon;
+    nx.left = steps > 0 ? min(con_rows - first * kCon, steps * kCon) : 0;
     if constexpr (FORM == kWeights) {
-      pa = reinterpret_cast<const uint8_t*>(p.chan + (int64_t)it.lo * p.nc + it.cb * NT);
-      pb = reinterpret_cast<const uint8_t*>(p.row + (int64_t)it.lo * p.nr + it.rt * MT);
+      nx.a = reinterpret_cast<const uint8_t*>(p.chan + ((int64_t)it.lo + first * kCon) * p.pitch_chan + it.cb * NT);
+      nx.b = reinterpret_cast<const uint8_t*>(p.row + ((int64_t)it.lo + first * kCon) * p.pitch_row + it.rt * MT);
       na = 2 * it.cb * NT;
       nb = 2 * it.rt * MT;
     } else {
-      pb = reinterpret_cast<const uint8_t*>(p.row + (int64_t)it.lo * p.con);
+      nx.b = reinterpret_cast<const uint8_t*>(p.row + (int64_t)it.lo * p.pitch_row);
       nb = it.rows * pitch_b;
-      const uint16_t* w = p.chan + (int64_t)it.group * p.nc * p.con;
       if constexpr (kDirA) {
-        pa = reinterpret_cast<const uint8_t*>(w + (int64_t)it.cb * NT * p.con);
+        nx.a = reinterpret_cast<const uint8_t*>(p.chan + ((int64_t)it.group * p.nc + it.cb * NT) * p.pitch_chan);
         na = min(NT, p.nc - it.cb * NT) * pitch_a;
       } else {
-        pa = reinterpret_cast<const uint8_t*>(w + it.cb * NT);
+        nx.a = reinterpret_cast<const uint8_t*>(p.chan + ((int64_t)it.group * p.con_t + first * kCon) * p.pitch_chan + it.cb * NT);
         na = 2 * it.cb * NT;
       }
     }
+    nx.ma = kDirA ? (steps > 0 ? na : 0) : rows_bytes(nx.left, pitch_a, na);
+    nx.mb = kDirB ? (steps > 0 ? nb : 0) : rows_bytes(nx.left, pitch_b, nb);
+    return steps;
   };
-  // The step being loaded
-  const uint8_t *qa, *qb;
-  int ma, mb, soff, ua[2] = {0, 0}, ub[2] = {0, 0};
-  auto aim_step = [&](int step) {
-    const bool in = step < steps, tail = step == tail_step;
-    const int left = min(max(con_rows - step * kCon, 0), kCon);
-    soff = kDirB ? step * 2 * kCon : 0;
-    qa = kDirA ? pa : pa + (int64_t)step * kCon * pitch_a;
-    qb = kDirB ? pb : pb + (int64_t)step * kCon * pitch_b;
-    ma = kDirA ? (in ? na : 0) : left > 0 ? left * pitch_a - na : 0;
-    mb = kDirB ? (in ? nb : 0) : left > 0 ? left * pitch_b - nb : 0;
+  // nx from st, in parts: between the MFMAs there is room for a few scalar instructions each
+  constexpr int kNextParts = 5;
+  auto next_part = [&](int part) {
+    if (part == 0) {
+      nx.steps = st.steps - 1;
+      nx.soff = st.soff + 2 * kCon;
+      nx.left = st.left - kCon;
+    }
+    if (part == 1) nx.a = kDirA ? st.a : st.a + stride_a;
+    if (part == 2) nx.b = kDirB ? st.b : st.b + stride_b;
+    if (part == 3) nx.ma = kDirA ? (nx.steps > 0 ? na : 0) : rows_bytes(nx.left, pitch_a, na);
+    if (part == 4) nx.mb = kDirB ? (nx.steps > 0 ? nb : 0) : rows_bytes(nx.left, pitch_b, nb);
+  };
+  int ua[2] = {0, 0}, ub[2] = {0, 0};
+  auto take_step = [&]() {   // st = nx
+    // (scalars: from vector registers, where the compiler puts some of them, each load would loop
+    // over the lanes)
+    auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    auto scalar_ptr = [&](const uint8_t* q) {
+      const uint64_t u = reinterpret_cast<uint64_t>(q);
+      return reinterpret_cast<const uint8_t*>((uint64_t)(uint32_t)scalar((int)(uint32_t)u) | (uint64_t)(uint32_t)scalar((int)(u >> 32)) << 32);
+    };
+    st.a = scalar_ptr(nx.a);
+    st.b = scalar_ptr(nx.b);
+    st.ma = scalar(nx.ma);
+    st.mb = scalar(nx.mb);
+    st.left = scalar(nx.left);
+    st.steps = scalar(nx.steps);
+    st.soff = scalar(nx.soff);
+    const bool tail = st.soff == tail_step * 2 * kCon;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if constexpr (kDirA) ua[i] = tail ? ta[i] : 0;
       if constexpr (kDirB) ub[i] = tail ? tb[i] : 0;
     }
+  };
+  auto step_on = [&]() {
+    for (int k = 0; k < kNextParts; ++k) next_part(k);
+    take_step();
   };
   auto place = [&](int slot, int i) {   // of load i in a slot (a constant): 1 KB
     return i < S::kLA ? (slot ? a1 : a0) + (wave * S::kLA + i) * 1024 : (slot ? b1 : b0) + (wave * S::kLB + i - S::kLA) * 1024;
@@ -217,8 +338,11 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   auto fetch = [&](int slot, int i) {
     const bool chan = i < S::kLA;
     const int k = chan ? i : i - S::kLA;
-    const auto r = buffer_of(chan ? qa : qb, chan ? ma : mb);
-    const int voff = chan ? va[k] + ua[k & 1] : vb[k] + ub[k & 1], so = chan && !kDirA ? 0 : soff;
+    const auto r = buffer_of(chan ? st.a : st.b, chan ? st.ma : st.mb);
+    // (few lane places are kept, and the rows between them added: registers are short)
+    const int like = chan ? load_like(kDirA, NT, k) : load_like(kDirB, MT, k);
+    const int rows = (k - like) * (chan ? (kDirA ? 8 : 512 / NT) : kDirB ? 8 : 512 / MT);
+    const int voff = (chan ? va[like] + ua[k & 1] : vb[like] + ub[k & 1]) + rows * (chan ? pitch_a : pitch_b), so = (chan ? kDirA : kDirB) ? st.soff : 0;
     if constexpr (DMA) {
       if (ONCE && chan) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)place(slot, i), 16, voff, so, 0, 2);
       else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)place(slot, i), 16, voff, so, 0, 0);
@@ -324,13 +448,17 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
       multiply(0, j, [&](int i) {
         reads(SLOT ^ 1, 1, j, i);
         loads(SLOT, RB - 1 + j, i);
+        constexpr int kEach = (kNextParts + RB - 2) / (RB - 1);   // parts beside a group
+        if (i == CB - 2 && j < RB - 1)
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) next_part(j * kEach + k);
       });
     multiply(1, 0, [&](int i) { loads(SLOT, 2 * RB - 1, i); });
     slot_barrier<DMA>();
   };
-  auto turn = [&](auto k, int next) {
+  auto turn = [&](auto k) {
     renew();
-    aim_step(next);
+    take_step();
     end_slot(k);
     begin_slot(k);
   };
@@ -339,20 +467,20 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
 
   fill(0);
   Item16 cur = item(0);
-  aim(cur);
+  int steps = aim(cur, shared && share.full == 0, true);
   // DMA: steps 0 and 1 are on their way into the slots. Else step 0 is in its slot, and steps 1 and 2
   // are where the first part of a turn before the first would have left them: the parts beside its
   // RB - 1 groups of step 1 put and of step 2 fetched.
-  aim_step(0);
+  take_step();
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) fetch(0, i);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) put(0, i);
-  aim_step(1);
+  step_on();
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) fetch(1, i);
   if constexpr (!DMA) {
-    aim_step(2);
+    step_on();
 #pragma unroll
     for (int g = 0; g < RB - 1; ++g)
 #pragma unroll
@@ -386,47 +514,37 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     // steps of the item, an even number (those behind its last are zeros)
     const int all = max(DMA ? 2 : 4, (steps + 1) / 2 * 2);
     for (int t = 0; t < all - (DMA ? 2 : 4); t += 2) {
-      turn(k0, t + (DMA ? 2 : 3));
-      turn(k1, t + (DMA ? 3 : 4));
+      turn(k0);
+      turn(k1);
     }
-    if constexpr (!DMA) turn(k0, all - 1);
+    if constexpr (!DMA) turn(k0);
     // the next item's first steps are loaded behind the item's last
     const bool more = n + 1 < count;
     if (more && (n + 1) % kList == 0) fill(n + 1);
     const Item16 next = more ? item(n + 1) : cur;
-    aim(next);
-    if (!more) steps = con_rows = 0;
-    if constexpr (!DMA) turn(k1, 0);
-    turn(k0, DMA ? 0 : 1);
-    aim_step(DMA ? 1 : 2);
+    steps = aim(next, more && shared && n + 1 == share.full, more);
+    if constexpr (!DMA) turn(k1);
+    turn(k0);
+    take_step();
     end_slot(k1);
     settle();
-    // ---- output: lane (g, r) holds row r, channels 4 g + 0..3 of a block: 64 neighbouring bytes of
-    // a row in fp32. Of 16-bit values those of two blocks are exchanged until a lane has 8
-    // neighbouring channels and a row's 64 bytes are in lanes l, l + 32, l + 16, l + 48 (pieces of 8
-    // bytes would be write requests of their own to the L2).
+    const bool part = shared && n == share.full;
     const int rows = FORM == kWeights ? min(MT, p.nr - cur.rt * MT) : cur.rows;
-    const int64_t first = FORM == kWeights ? (int64_t)cur.group * p.nr + cur.rt * MT : cur.lo;
+    const int64_t out_row = FORM == kWeights ? (int64_t)cur.group * p.nr + cur.rt * MT : cur.lo;
+    const auto sums = buffer_of(p.part + ((int64_t)blockIdx.x * WAVES + wave) * (RB * CB * 256), RB * CB * 1024);
 #pragma unroll
     for (int j = 0; j < RB; ++j) {
-      const int row = (wr * RB + j) * 16 + (lane & 15);
-      if (!p.out_fp32) {
-        uint16_t* to = (uint16_t*)p.out + (first + row) * p.nc;
+      v4f of[CB];
 #pragma unroll
-        for (int i = 0; i < CB; i += 2) {
-          const auto at = [&](int k, int c) { return Mfma<T>::pair(acc[i + k][j][c], acc[i + k][j][c + 1]); };
-          const auto s0 = __builtin_amdgcn_permlane16_swap(at(0, 0), at(1, 0), false, false);
-          const auto s1 = __builtin_amdgcn_permlane16_swap(at(0, 2), at(1, 2), false, false);
-          const int c = cur.cb * NT + (wc * CB + i) * 16 + 16 * (g4 & 1) + 8 * (g4 >> 1);
-          if (row < rows && c < p.nc) *reinterpret_cast<u32x4*>(to + c) = u32x4{s0[0], s1[0], s0[1], s1[1]};
-        }
+      for (int i = 0; i < CB; ++i) of[i] = acc[i][j];
+      int row = (wr * RB + j) * 16 + (lane & 15);
+      asm volatile("" : "+v"(row));   // (addresses made here: kept for all items, they would be spilled)
+      if (part) {   // the sums as they are, for gmm16_join_kernel
+#pragma unroll
+        for (int i = 0; i < CB; ++i)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, of[i]), sums, lane * 16, (j * CB + i) * 1024, 0);
       } else {
-        float* to = (float*)p.out + (first + row) * p.nc;
-#pragma unroll
-        for (int i = 0; i < CB; ++i) {
-          const int c = cur.cb * NT + (wc * CB + i) * 16 + 4 * g4;
-          if (row < rows && c < p.nc) *reinterpret_cast<v4f*>(to + c) = acc[i][j];
-        }
+        store_rows<ODD, T, CB>(p, of, row < rows, out_row + row, cur.cb * NT + wc * CB * 16);
       }
     }
     if (++n >= count) break;
@@ -437,16 +555,46 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   __builtin_amdgcn_s_waitcnt((0 << 14) | (7 << 4) | (15 << 8));   // no direct-to-LDS load outlives the block
 }
 
-template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
+template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, bool ODD, typename T>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(BLOCKS * WAVES / 4))) void gmm16_tile_kernel(Tile16Args p) {
   extern __shared__ __align__(16) uint8_t lds_area[];
   using S = Tile16<WAVES, WC, CB, RB>;
   uint8_t* const b = lds_area + 2 * S::kA;
-  tile16_body<FORM, WAVES, WC, CB, RB, ONCE, DMA, T>(p, lds_area, lds_area + S::kA, b, b + S::kB, b + 2 * S::kB);
+  tile16_body<FORM, WAVES, WC, CB, RB, ONCE, DMA, ODD, T>(p, lds_area, lds_area + S::kA, b, b + S::kB, b + 2 * S::kB);
 }
 
-// The device's compute units, rounded up to whole XCDs' shares; the kernel's LDS size set
-// once for each device.
+// The shared items' parts added, in the order of the contraction, and stored: blockIdx.x takes item
+// blockIdx.x / 8 of XCD blockIdx.x % 8's shared ones, blockIdx.y one row block of each wave.
+template <int FORM, int WAVES, int WC, int CB, int RB, bool ODD, typename T>
+__global__ __launch_bounds__(64 * WAVES) void gmm16_join_kernel(Tile16Args p, int blocks) {
+  using S = Tile16<WAVES, WC, CB, RB>;
+  __shared__ int ends[FORM == kWeights ? 1 : kMaxGroups], scratch[WAVES];
+  const int ncb = (p.nc + S::kNT - 1) / S::kNT, nrt = (p.nr + S::kMT - 1) / S::kMT;
+  int tiles = p.groups * nrt;
+  if constexpr (FORM != kWeights) tiles = count_tiles<S::kMT, WAVES>(p.off, p.groups, p.rows, ends, scratch);
+  const int xcd = blockIdx.x & 7, r = blockIdx.x >> 3, per = blocks >> 3;
+  const Share share = share_of(p, (int64_t)tiles * ncb, xcd, per);
+  if (share.parts < 2 || r >= share.rem) return;
+  const Item16 it = item16<FORM>(describe16<FORM, S::kMT>(p, ends, tiles, nrt, ncb, share.begin + (int64_t)share.full * per + r), ncb);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = blockIdx.y;
+  v4f acc[CB] = {};
+  for (int part = 0; part < share.parts; ++part) {
+    const int block = xcd + 8 * (part * share.rem + r);
+    const v4f* from = reinterpret_cast<const v4f*>(p.part) + (((int64_t)block * WAVES + wave) * RB + j) * (CB * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      const v4f v = from[i * 64];
+      acc[i] += v;
+    }
+  }
+  const int row = ((wave / WC) * RB + j) * 16 + (lane & 15);
+  const int rows = FORM == kWeights ? min(S::kMT, p.nr - it.rt * S::kMT) : it.rows;
+  const int64_t out_row = FORM == kWeights ? (int64_t)it.group * p.nr + it.rt * S::kMT : it.lo;
+  store_rows<ODD, T, CB>(p, acc, row < rows, out_row + row, it.cb * S::kNT + (wave % WC) * CB * 16);
+}
+
+// Blocks of a launch (the device's compute units, rounded up to whole XCDs' shares, and no more than
+// the workspace of shared items is laid out for); the kernel's LDS size set once for each device.
 inline hipError_t tile16_grid(const void* kernel, int lds, int* grid) {
   static std::mutex mu;
   static std::map<std::pair<int, const void*>, int> known;
@@ -459,47 +607,57 @@ inline hipError_t tile16_grid(const void* kernel, int lds, int* grid) {
     int cus = 0;
     if ((e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds)) != hipSuccess) return e;
     if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
-    at = known.emplace(std::make_pair(dev, kernel), (cus + 7) / 8 * 8).first;
+    at = known.emplace(std::make_pair(dev, kernel), std::min((cus + 7) / 8 * 8, kTile16Units)).first;
   }
   *grid = at->second;
   return hipSuccess;
 }
 
-template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, typename T>
+template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, bool ODD, typename T>
 hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
   using S = Tile16<WAVES, WC, CB, RB>;
   static_assert(S::kLds * BLOCKS <= 160 * 1024, "LDS of a compute unit");
   static_assert(S::kMT >= 64 || FORM != kWeights, "a transposed operand is 64 wide at least");
+  static_assert((FORM == kForward || S::kLA * (512 / S::kNT) % 8 == 0) && (FORM != kWeights || S::kLB * (512 / S::kMT) % 8 == 0),
+                "a wave's loads of a transposed operand begin at a multiple of 8 rows");
   int grid = 0;
-  const auto kernel = gmm16_tile_kernel<FORM, WAVES, WC, CB, RB, BLOCKS, ONCE, DMA, T>;
+  const auto kernel = gmm16_tile_kernel<FORM, WAVES, WC, CB, RB, BLOCKS, ONCE, DMA, ODD, T>;
   hipError_t e = tile16_grid(reinterpret_cast<const void*>(kernel), S::kLds, &grid);
   if (e != hipSuccess) return e;
-  kernel<<<grid * BLOCKS, 64 * WAVES, S::kLds, stream>>>(a);
+  grid *= BLOCKS;
+  kernel<<<grid, 64 * WAVES, S::kLds, stream>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess || !a.part) return e;
+  gmm16_join_kernel<FORM, WAVES, WC, CB, RB, ODD, T><<<dim3(grid / 2, RB), 64 * WAVES, 0, stream>>>(a, grid);
   return hipGetLastError();
 }
 
 // mt: rows of a tile.
-template <int FORM, typename T>
+template <int FORM, bool ODD, typename T>
 hipError_t launch_tile16_as(const Tile16Args& a, int mt, hipStream_t stream) {
   constexpr bool dma = FORM == kForward;   // (the transposing read waits for every direct-to-LDS load in flight)
   switch (mt) {
-    case 256: return launch_tile16<FORM, 4, 2, 8, 8, 1, false, false, T>(a, stream);
-    case 128: return launch_tile16<FORM, 4, 2, 8, 4, 1, false, dma, T>(a, stream);
-    case 64: return launch_tile16<FORM, 4, 4, 2, 4, 2, FORM != kWeights, dma, T>(a, stream);
+    case 256: return launch_tile16<FORM, 4, 2, 8, 8, 1, false, false, ODD, T>(a, stream);
+    case 128: return launch_tile16<FORM, 4, 2, 8, 4, 1, false, dma, ODD, T>(a, stream);
+    case 64: return launch_tile16<FORM, 4, 4, 2, 4, 2, FORM != kWeights, dma, ODD, T>(a, stream);
     default:
       if constexpr (FORM == kWeights) return hipErrorInvalidValue;
-      else return launch_tile16<FORM, 4, 4, 2, 2, 3, true, dma, T>(a, stream);
+      else return launch_tile16<FORM, 4, 4, 2, 2, 3, true, dma, ODD, T>(a, stream);
   }
+}
+template <int FORM, typename T>
+hipError_t launch_tile16_odd(const Tile16Args& a, int mt, bool odd, hipStream_t stream) {
+  return odd ? launch_tile16_as<FORM, true, T>(a, mt, stream) : launch_tile16_as<FORM, false, T>(a, mt, stream);
 }
 
 template <int FORM>
 hipError_t launch_tile16_form(const Gmm16Params& p, hipStream_t stream) {
   Tile16Args a{};
-  a.row = (const uint16_t*)p.a; a.chan = (const uint16_t*)p.b; a.off = p.off; a.groups = p.groups; a.rows = (int)p.rows;
-  a.out_fp32 = p.out_fp32; a.out = p.out;
-  if (FORM == kWeights) { a.nc = p.k; a.nr = p.n; a.con = kCon; }
-  else { a.nc = p.n; a.nr = 1; a.con = p.k; }
-  return p.half ? launch_tile16_as<FORM, _Float16>(a, p.mt, stream) : launch_tile16_as<FORM, __bf16>(a, p.mt, stream);
+  a.row = (const uint16_t*)p.a; a.chan = (const uint16_t*)p.b; a.pitch_row = p.pitch_a; a.pitch_chan = p.pitch_b;
+  a.off = p.off; a.groups = p.groups; a.rows = (int)p.rows; a.out_fp32 = p.out_fp32; a.out = p.out;
+  if (FORM == kWeights) { a.nc = p.k; a.nr = p.n; a.con = a.con_t = kCon; a.steps = (int)(p.rows / p.groups / kCon); }
+  else { a.nc = p.n; a.nr = 1; a.con = (p.k + 7) / 8 * 8; a.con_t = p.k; a.steps = (a.con + kCon - 1) / kCon; }
+  a.part = p.part; a.gain = p.gain;
+  return p.half ? launch_tile16_odd<FORM, _Float16>(a, p.mt, p.odd, stream) : launch_tile16_odd<FORM, __bf16>(a, p.mt, p.odd, stream);
 }
 
 }  // namespace

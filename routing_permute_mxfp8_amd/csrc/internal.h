@@ -376,8 +376,19 @@ struct Gmm16Params {
   int n = 0, k = 0;
   bool out_fp32 = false;           // else the operands' type
   void* out = nullptr;
+  // what gmm16_plan makes of the sizes:
   int mt = 0;                      // rows of a tile of the LDS-staged kernels, 0: the kernel for every shape
+  int pitch_a = 0, pitch_b = 0;    // elements from one row of a, b to the next there, multiples of 8
+  int gain = 0;                    // steps that sharing an item between blocks has to save
+  size_t part_floats = 0, copy_a = 0, copy_b = 0;   // workspace: fp32 parts; elements of copies with those pitches
+  // and the workspace
+  float* part = nullptr;
+  uint16_t* a16 = nullptr;
+  uint16_t* b16 = nullptr;
+  bool odd = false;                // out is stored by elements
 };
+constexpr int kTile16Units = 256;  // compute units that the workspace of shared items is laid out for
+void gmm16_plan(Gmm16Params& p);
 hipError_t launch_gmm16_forward(const Gmm16Params& p, hipStream_t stream);
 hipError_t launch_gmm16_transposed(const Gmm16Params& p, hipStream_t stream);
 hipError_t launch_gmm16_weights(const Gmm16Params& p, hipStream_t stream);
