@@ -11,6 +11,7 @@
 // outputs, 32 x 32 a wave.
 
 #include <algorithm>
+#include <cmath>
 
 #include "device_common.h"
 #include "fp4_device.h"
@@ -156,10 +157,71 @@ hipError_t launch_pad16(const void* from, int64_t rows, int cols, uint16_t* to, 
   return hipGetLastError();
 }
 
+// ---- which tile -----------------------------------------------------------------------------
+// The LDS-staged kernel's tiles: mt rows by nt channels, `blocks` of them at a time on a compute
+// unit. step: microseconds that these take for 64 contraction elements; item: for the rest of a
+// tile (its output and the next one's start). step fits products of one group, 7168 deep, of 256 or
+// 512 tiles (256: 214 us, 192: 176, 160: 150, 128: 134, 64: 126, 32: 105), item the slope of shorter
+// ones.
+struct Shape16 {
+  int mt, nt, blocks;
+  float step, item;
+};
+constexpr Shape16 kShapes[] = {{256, 256, 1, 1.80f, 4.0f}, {192, 256, 1, 1.45f, 3.0f}, {160, 256, 1, 1.23f, 2.5f},
+                               {128, 256, 1, 1.08f, 2.0f}, {64, 128, 2, 1.00f, 1.5f},  {32, 128, 3, 1.10f, 1.0f}};
+
+// Tiles of mt rows that a group of `mean` rows fills on average. The host does not know the groups'
+// sizes (they are on the device): it takes them to scatter by the square root of the mean, as those of
+// rows that choose their group at random do. One group has exactly `mean` rows.
+double tiles_of(double mean, int mt, bool one) {
+  if (one) return std::ceil(mean / mt);
+  if (mean <= 0) return 0;
+  const double sd = std::sqrt(mean);
+  double sum = 1.0 - std::exp(-mean);   // groups with rows at all
+  for (double at = mt; at < mean + 6 * sd; at += mt) sum += 0.5 * std::erfc((at + 0.5 - mean) / (std::sqrt(2.0) * sd));
+  return sum;
+}
+
+// Steps that sharing an item between blocks has to save: the join takes a launch and, for 256 tiles
+// of 256 x 256, 64 MB written and read, some 30 us in all.
+constexpr int kGain = 16;
+
+// Microseconds of a call with tiles of shape s, but for the memory traffic, which they share.
+double estimate(const Gmm16Params& p, const Shape16& s) {
+  const double mean = (double)p.rows / p.groups;
+  const double steps = std::max(1.0, std::ceil((p.wgrad ? mean : (double)p.k) / 64));
+  const double columns = std::ceil((double)(p.wgrad ? p.k : p.n) / s.nt);
+  const double items = p.groups * columns * (p.wgrad ? std::ceil((double)p.n / s.mt) : tiles_of(mean, s.mt, p.groups == 1));
+  const double units = (double)kTile16Units * s.blocks;
+  const double full = std::floor(items / units), rem = items - full * units;
+  double t = full * (steps * s.step + s.item);
+  if (rem > 0) {
+    const double parts = std::min(std::floor(units / rem), std::floor(steps / 4));
+    const double one = steps * s.step * (rem <= kTile16Units ? 0.5 + 0.5 / s.blocks : 1.0);   // fewer blocks a unit
+    if (parts >= 2 && steps - std::ceil(steps / parts) >= kGain)
+      t += std::ceil(steps / parts) * s.step + s.item + 6 + rem * parts * s.mt * s.nt * 8 / 5e6;
+    else
+      t += one + s.item;
+  }
+  return t;
+}
+
+// The tile with the least estimate. Groups of about 256 rows, e.g., take two tiles of 160 rows rather
+// than one and often a second of 256 (8192 rows on 32 groups of 4096 x 7168, forward and transposed:
+// 577 and 618 us, with 192 rows 605 and 662, with 256 591 and 657, with 128 718 and 760). Limits: where rows outside the groups or a few large groups make the mean a poor
+// guide, the tile is larger or smaller than it should be.
 int tile_rows(const Gmm16Params& p) {
-  const int64_t per = (p.rows + p.groups - 1) / p.groups;
-  if (p.wgrad) return 256;
-  return per <= 20 ? 32 : per <= 48 ? 64 : per <= 100 ? 128 : 256;
+  int best = 0;
+  double least = 0;
+  for (const Shape16& s : kShapes) {
+    if (p.wgrad && s.mt != 256 && s.mt != 128 && s.mt != 64) continue;
+    const double t = estimate(p, s);
+    if (best == 0 || t < least) {
+      best = s.mt;
+      least = t;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -172,10 +234,10 @@ void gmm16_plan(Gmm16Params& p) {
   p.pitch_b = (cols_b + 7) / 8 * 8;
   p.copy_a = p.pitch_a != cols_a ? (size_t)p.rows * p.pitch_a : 0;
   p.copy_b = p.pitch_b != cols_b ? (size_t)rows_b * p.pitch_b : 0;
-  const int nt = p.mt >= 128 ? 256 : 128, blocks = p.mt >= 128 ? 1 : p.mt == 64 ? 2 : 3;
-  p.gain = 16;
+  p.gain = kGain;
   const int64_t steps = p.wgrad ? p.rows / p.groups / 64 : (p.k + 63) / 64;
-  p.part_floats = steps >= 2 * p.gain || steps >= 8 ? (size_t)kTile16Units * blocks * p.mt * nt : 0;
+  for (const Shape16& s : kShapes)
+    if (s.mt == p.mt) p.part_floats = steps - (steps + 1) / 2 >= p.gain ? (size_t)kTile16Units * s.blocks * s.mt * s.nt : 0;
 }
 
 hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {

@@ -631,18 +631,26 @@ hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// mt: rows of a tile.
+// mt: rows of a tile, one of gmm16.hip's kShapes.
 template <int FORM, bool ODD, typename T>
 hipError_t launch_tile16_as(const Tile16Args& a, int mt, hipStream_t stream) {
-  constexpr bool dma = FORM == kForward;   // (the transposing read waits for every direct-to-LDS load in flight)
+  // Direct-to-LDS loads for the small tiles, whose few waves' MFMAs hide little (64 groups of 4096 x
+  // 4096, 56 rows each: 429 us, through registers 446); but not beside transposing reads, for which
+  // the compiler waits for every such load in flight.
+  constexpr bool dma = FORM == kForward;
   switch (mt) {
     case 256: return launch_tile16<FORM, 4, 2, 8, 8, 1, false, false, ODD, T>(a, stream);
-    case 128: return launch_tile16<FORM, 4, 2, 8, 4, 1, false, dma, ODD, T>(a, stream);
+    case 128: return launch_tile16<FORM, 4, 2, 8, 4, 1, false, false, ODD, T>(a, stream);
     case 64: return launch_tile16<FORM, 4, 4, 2, 4, 2, FORM != kWeights, dma, ODD, T>(a, stream);
-    default:
-      if constexpr (FORM == kWeights) return hipErrorInvalidValue;
-      else return launch_tile16<FORM, 4, 4, 2, 2, 3, true, dma, ODD, T>(a, stream);
+    default: break;
   }
+  if constexpr (FORM != kWeights) switch (mt) {
+    case 192: return launch_tile16<FORM, 4, 2, 8, 6, 1, false, false, ODD, T>(a, stream);
+    case 160: return launch_tile16<FORM, 4, 2, 8, 5, 1, false, false, ODD, T>(a, stream);
+    case 32: return launch_tile16<FORM, 4, 4, 2, 2, 3, true, dma, ODD, T>(a, stream);
+    default: break;
+  }
+  return hipErrorInvalidValue;
 }
 template <int FORM, typename T>
 hipError_t launch_tile16_odd(const Tile16Args& a, int mt, bool odd, hipStream_t stream) {
