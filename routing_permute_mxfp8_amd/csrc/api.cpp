@@ -1210,7 +1210,7 @@ moe_status moe_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm_backward_workspace_size: bytes is NULL");
   if (moe_status s = check_norm("moe_rms_norm_backward", MOE_DTYPE_FP32, rows, cols, MOE_DTYPE_FP32)) return s;
   Carver cv(nullptr);
-  cv.take<float>((size_t)moe::norm_parts(rows) * cols);
+  cv.take<float>((size_t)moe::norm_parts(rows, cols) * cols);
   *bytes = cv.off;
   return ok();
 }
@@ -1226,7 +1226,7 @@ moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* 
       misaligned(4, {rstd, grad_weight}))
     return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm_backward: tensors must be aligned to their elements");
   moe::NormGradParams p;
-  p.parts = moe::norm_parts(rows);
+  p.parts = moe::norm_parts(rows, cols);
   Carver need(nullptr);
   need.take<float>((size_t)p.parts * cols);
   if (moe_status s = check_ws("moe_rms_norm_backward", need.off, workspace, workspace_bytes)) return s;

@@ -345,7 +345,7 @@ struct NormParams {
 };
 hipError_t launch_norm(const NormParams& p, hipStream_t stream);
 
-int norm_parts(int64_t rows);
+int norm_parts(int64_t rows, int64_t cols);
 struct NormGradParams {
   const void* grad_y = nullptr;
   const void* h = nullptr;

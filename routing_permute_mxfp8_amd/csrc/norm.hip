@@ -11,10 +11,19 @@
 // that, sees the same rows; and the codes are those of y rounded to T, so that they are the bytes
 // that moe_mx_quantize makes of y. The squares are summed in 64 bits: no finite row overflows.
 //
-// A thread holds 8 neighbouring elements (16 bytes of a 16-bit type) of a row, or two such chunks,
-// so every input is read and every output written once; an MX group of 32 is four lanes, whose
-// largest magnitude takes two DPP steps. Rows whose chunks are no 16-byte vectors (an odd number
-// of columns, a tensor that starts elsewhere) are read and written by elements.
+// Both passes are bound by memory: every input is read and every output written once, 530 MB for
+// 8192 x 7168 bf16 rows with a residual and MXFP8 codes, 470 MB for their gradient. A thread holds 8
+// neighbouring elements (16 bytes of a 16-bit type) of a row, or two such chunks past 8192 columns;
+// an MX group of 32 is four lanes, whose largest magnitude takes two DPP steps. A row has 16 lanes,
+// a wave, or a block with as many waves as it has chunks for; the blocks that fit on the card at
+// once go over the rows, and load the next row before they sum one. Measured at that size, the
+// gradient with the sum of its weight's partial sums:
+//   a block a row, no row loaded in advance                 104 us,  its gradient 117 us
+//   blocks that go over the rows, rows loaded in advance    100                   101
+//   row sums by DPP and lane swaps (shuffles through LDS addresses: 20 more registers),
+//   loads that pass the caches by (the outputs stay there for the next kernel)
+//                                                            85 (6.2 TB/s)         84 (5.6 TB/s)
+// Stores that pass the caches by as well: 96 and 88.
 
 #include <algorithm>
 
@@ -25,99 +34,90 @@ namespace moe {
 namespace {
 
 // ---- element types ----------------------------------------------------------------------
-// 8 elements of a row as floats; n of them exist (the others come as 0 and are not written).
-template <typename T> struct Row8;
+// 8 elements of a row as they are in memory, in dwords (as a vector of 16-bit elements the compiler
+// keeps each in a register of its own across a branch). n of them exist: the others come as 0 and
+// are not written.
+template <typename T> using Raw8 = uint32_t __attribute__((ext_vector_type(2 * sizeof(T))));
 
-template <> struct Row8<uint16_t> {   // bf16
-  static __device__ __forceinline__ void load(const uint16_t* p, float (&f)[8]) {
-    const u32x4 u = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f(*p); }
-  static __device__ __forceinline__ float round(float v) { return __uint_as_float(bf16x2(v, v) << 16); }
-  static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
-    u32x4 u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = bf16x2(f[2 * i], f[2 * i + 1]);
-    *reinterpret_cast<u32x4*>(p) = u;
-  }
-  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)bf16x2(v, v); }
-};
-
-template <> struct Row8<_Float16> {
-  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ void load(const _Float16* p, float (&f)[8]) {
-    const h8 h = *reinterpret_cast<const h8*>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
-  }
-  static __device__ __forceinline__ float one(const _Float16* p) { return (float)*p; }
-  static __device__ __forceinline__ float round(float v) { return (float)(_Float16)v; }
-  static __device__ __forceinline__ void store(_Float16* p, const float (&f)[8]) {
-    h8 h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (_Float16)f[i];
-    *reinterpret_cast<h8*>(p) = h;
-  }
-  static __device__ __forceinline__ void put(_Float16* p, float v) { *p = (_Float16)v; }
-};
-
-template <> struct Row8<float> {
-  static __device__ __forceinline__ void load(const float* p, float (&f)[8]) {
-    const v4f a = *reinterpret_cast<const v4f*>(p), b = *reinterpret_cast<const v4f*>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = a[i];
-      f[4 + i] = b[i];
-    }
-  }
-  static __device__ __forceinline__ float one(const float* p) { return *p; }
-  static __device__ __forceinline__ float round(float v) { return v; }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-    v4f a, b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = f[i];
-      b[i] = f[4 + i];
-    }
-    *reinterpret_cast<v4f*>(p) = a;
-    *reinterpret_cast<v4f*>(p + 4) = b;
-  }
-  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-};
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* p, int n, float (&f)[8]) {
-  if constexpr (VEC) {
-    Row8<T>::load(p, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? Row8<T>::one(p + i) : 0.0f;
-  }
+template <typename T> __device__ __forceinline__ float value(Raw8<T> r, int i) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
+  else if constexpr (__is_same(T, _Float16)) return (float)__builtin_bit_cast(_Float16, (uint16_t)(r[i / 2] >> (i % 2 * 16)));
+  else return __uint_as_float(i % 2 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
 }
 
+// To the rows' type, each to the nearest, ties to even.
+template <typename T>
+__device__ __forceinline__ Raw8<T> rounded(const float (&f)[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < 2 * (int)sizeof(T); ++i) {
+    if constexpr (sizeof(T) == 4) {
+      r[i] = __float_as_uint(f[i]);
+    } else if constexpr (__is_same(T, _Float16)) {
+      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+      r[i] = __builtin_bit_cast(uint32_t, h2{(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
+    } else {
+      r[i] = bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  return r;
+}
+
+// VEC: every chunk is whole and starts at a multiple of 16 bytes. Otherwise a whole chunk is one
+// access too, at an address that is a multiple of an element only (the memory takes it; 32768 x
+// 1001 fp16: by elements 161 us, so 53), and a row's last elements go one by one.
+template <typename T> struct AnyRaw8 {
+  Raw8<T> v;
+} __attribute__((packed, aligned(sizeof(T))));
+
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* p, int n, const float (&f)[8]) {
+__device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
+  Raw8<T> r = {};
   if constexpr (VEC) {
-    Row8<T>::store(p, f);
+    if (n > 0) r = __builtin_nontemporal_load(reinterpret_cast<const Raw8<T>*>(p));
+  } else if (n >= 8) {
+    r = reinterpret_cast<const AnyRaw8<T>*>(p)->v;
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) r[i] = __float_as_uint(p[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) Row8<T>::put(p + i, f[i]);
+      if (i < n) r[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (i % 2 * 16);
+  }
+  return r;
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* p, int n, Raw8<T> r) {
+  if constexpr (VEC) {
+    *reinterpret_cast<Raw8<T>*>(p) = r;
+  } else if (n >= 8) {
+    reinterpret_cast<AnyRaw8<T>*>(p)->v = r;
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = __uint_as_float(r[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = __builtin_bit_cast(T, (uint16_t)(r[i / 2] >> (i % 2 * 16)));
   }
 }
 
-// The same of the weight, which is of the rows' type or fp32.
+// The weight's, which is of the rows' type or fp32, as floats.
 template <bool VEC, typename T>
 __device__ __forceinline__ void load_weight(const void* w, bool fp32, int c, int n, float (&f)[8]) {
-  if (fp32)
-    load8<VEC>((const float*)w + c, n, f);
-  else
-    load8<VEC>((const T*)w + c, n, f);
+  if (fp32) {
+    const Raw8<float> r = load8<VEC>((const float*)w + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = value<float>(r, i);
+  } else {
+    const Raw8<T> r = load8<VEC>((const T*)w + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = value<T>(r, i);
+  }
 }
 
 // MX codes (8 elements; F as in device_common.h) of y over its group's scale to row element c.
@@ -140,68 +140,113 @@ __device__ __forceinline__ int quantise8(const float (&y)[8], uint8_t* codes, in
   return b;
 }
 
-// Sum over a row's LANES threads (a power of two; rows of fewer than 64 share a wave, wider
-// ones have the block to themselves), the same in all of them. slot: 16 values of LDS.
+constexpr int rows_of(int lanes) { return lanes ? 256 / lanes : 1; }
+
+// Sum of v over a row's lanes, the same in all: LANES lanes of a block of 256 threads, or (LANES = 0)
+// the whole block, whatever its size. slot: one of two sets of 16 values of LDS, used in
+// turn by a block's rows (a wave that is behind may still read the last row's).
+template <int STEP, typename S>   // v + the v of the lane that step exchanges with this one
+__device__ __forceinline__ S add_step(S v) {
+  constexpr int kWords = sizeof(S) / 4;
+  typedef uint32_t words __attribute__((ext_vector_type(2)));
+  words a, b;
+  if constexpr (kWords == 2) a = __builtin_bit_cast(words, v); else a[0] = __builtin_bit_cast(uint32_t, v);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    if constexpr (STEP < 16) {   // quad_perm [1,0,3,2], [2,3,0,1], then mirrored halves of 8, rows of 16
+      constexpr int ctrl = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;
+      b[i] = __builtin_amdgcn_mov_dpp((int)a[i], ctrl, 0xF, 0xF, false);
+    } else {   // each lane gets both halves' values: one in each of the two results
+      const auto r = STEP == 16 ? __builtin_amdgcn_permlane16_swap(a[i], a[i], false, false)
+                                : __builtin_amdgcn_permlane32_swap(a[i], a[i], false, false);
+      a[i] = r[0];
+      b[i] = r[1];
+    }
+  }
+  if constexpr (kWords == 2) return __builtin_bit_cast(S, a) + __builtin_bit_cast(S, b);
+  else return __builtin_bit_cast(S, (uint32_t)a[0]) + __builtin_bit_cast(S, (uint32_t)b[0]);
+}
+
 template <int LANES, typename S>
 __device__ __forceinline__ S row_sum(S v, S* slot) {
-#pragma unroll
-  for (int s = 1; s < (LANES < 64 ? LANES : 64); s *= 2) v += __shfl_xor(v, s, 64);
-  if constexpr (LANES > 64) {
+  v = add_step<8>(add_step<4>(add_step<2>(add_step<1>(v))));
+  if constexpr (LANES != 16) v = add_step<32>(add_step<16>(v));
+  if constexpr (LANES == 0) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0;
 #pragma unroll
-    for (int w = 0; w < LANES / 64; ++w) v += slot[w];
-    __syncthreads();
+    for (int w = 0; w < 16; ++w) v += slot[w];   // (0 past the block's waves)
   }
   return v;
 }
 
 // ---- the norm ---------------------------------------------------------------------------
-// LANES threads a row, NV chunks a thread (chunk v of lane l: elements 8 (v LANES + l)).
+// NV chunks a thread (chunk v of lane l: elements 8 (v lanes + l)); a block takes rows
+// blockIdx.x kRows + i, + gridDim.x kRows, ... and loads the next while it sums one.
 template <typename T, int LANES, int NV, bool VEC, bool QUANT>
-__global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormParams p) {
-  constexpr int kRows = LANES <= 64 ? 256 / LANES : 1;   // rows of a block
-  __shared__ double slot[16];
-  const int lane = threadIdx.x % LANES;
+__global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) {
+  constexpr int kRows = rows_of(LANES);   // rows of a block
+  __shared__ double slots[2][16];
+  if constexpr (LANES == 0) {
+    if (threadIdx.x < 32) slots[0][threadIdx.x] = 0;
+    __syncthreads();
+  }
+  const int lanes = LANES ? LANES : blockDim.x, lane = LANES ? threadIdx.x % (LANES + !LANES) : threadIdx.x;
   const int C = p.cols;
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += (int64_t)gridDim.x * kRows) {
-    const int64_t row = first + threadIdx.x / LANES;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + (LANES ? threadIdx.x / (LANES + !LANES) : 0);
+  const int64_t mine = row - (int64_t)blockIdx.x * kRows;
+  Raw8<T> x[NV], r[NV];
+  const auto load = [&](int64_t at) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (v * lanes + lane), n = at < p.rows ? C - c : 0;
+      x[v] = load8<VEC>((const T*)p.x + at * C + c, n);
+      if (p.residual) r[v] = load8<VEC>((const T*)p.residual + at * C + c, n);
+    }
+  };
+  load(row);
+  float w[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (v * lanes + lane);
+    load_weight<VEC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
+  }
+  for (int turn = 0; row - mine < p.rows; row += step, turn ^= 1) {
     const bool live = row < p.rows;
-    const T* x = (const T*)p.x + row * C;
     float h[NV][8];
     double sum = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (v * LANES + lane), n = live ? C - c : 0;
+      const int c = 8 * (v * lanes + lane), n = live ? C - c : 0;
+      if (p.residual) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = 0.0f;
-      if (n > 0) {
-        load8<VEC>(x + c, n, h[v]);
-        if (p.residual) {
-          float r[8];
-          load8<VEC>((const T*)p.residual + row * C + c, n, r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] = Row8<T>::round(h[v][i] + r[i]);
-          store8<VEC>((T*)p.h + row * C + c, n, h[v]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fma((double)h[v][i], (double)h[v][i], sum);
+        for (int i = 0; i < 8; ++i) h[v][i] = value<T>(x[v], i) + value<T>(r[v], i);
+        x[v] = rounded<T>(h[v]);
+        if (n > 0) store8<VEC>((T*)p.h + row * C + c, n, x[v]);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[v][i] = value<T>(x[v], i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fma((double)h[v][i], (double)h[v][i], sum);
     }
-    sum = row_sum<LANES>(sum, slot);
+    load(row + step);
+    sum = row_sum<LANES>(sum, slots[turn]);
     const float rstd = (float)(1.0 / sqrt(sum / C + (double)p.eps));
     if (live && lane == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (v * LANES + lane), n = live ? C - c : 0;
+      const int c = 8 * (v * lanes + lane), n = live ? C - c : 0;
       if (n <= 0) continue;
-      float w[8], y[8];
-      load_weight<VEC, T>(p.weight, p.weight_dtype == 0, c, n, w);
+      float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = Row8<T>::round(h[v][i] * rstd * w[i]);
-      if (p.y) store8<VEC>((T*)p.y + row * C + c, n, y);
+      for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rstd * w[v][i];
+      const Raw8<T> out = rounded<T>(y);
+      if (p.y) store8<VEC>((T*)p.y + row * C + c, n, out);
       if constexpr (QUANT) {   // (C % 32 == 0: the four lanes of a group are all here)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = value<T>(out, i);
         const int64_t at = row * C + c;
         const int b = p.quant == 1 ? quantise8<0>(y, p.codes, at)
                       : p.quant == 2 ? quantise8<1>(y, p.codes, at) : quantise8<2>(y, p.codes, at);
@@ -216,58 +261,80 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormPar
 }
 
 // ---- its gradient -----------------------------------------------------------------------
-// Block b takes rows b kRows + i, + gridDim.x kRows, ...; the weight's gradient of these rows is
-// summed in registers and goes to part[b][C].
+// Rows to blocks and threads as above; the weight's gradient of a block's rows is summed in
+// registers and goes to part[block][C].
 template <typename T, int LANES, int NV, bool VEC>
-__global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_backward_kernel(NormGradParams p) {
-  constexpr int kRows = LANES <= 64 ? 256 / LANES : 1;
-  __shared__ float slot[16];
-  __shared__ float parts[kRows > 1 ? kRows * 8 * LANES * NV : 1];
-  const int lane = threadIdx.x % LANES, C = p.cols;
-  float acc[NV][8] = {}, w[NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = 8 * (v * LANES + lane);
-    if (c < C) load_weight<VEC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
+__global__ __launch_bounds__(LANES ? 256 : 1024) void norm_backward_kernel(NormGradParams p) {
+  constexpr bool kAhead = NV == 1;   // (two chunks a lane, of 1024 lanes: no registers left for a second row)
+  constexpr int kRows = rows_of(LANES);
+  __shared__ float slots[2][16];
+  if constexpr (LANES == 0) {
+    if (threadIdx.x < 32) slots[0][threadIdx.x] = 0;
+    __syncthreads();
   }
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += (int64_t)gridDim.x * kRows) {
-    const int64_t row = first + threadIdx.x / LANES;
-    const bool live = row < p.rows;
-    const float rstd = live ? p.rstd[row] : 0.0f;
-    float xh[NV][8], a[NV][8], dot = 0.0f;
+  __shared__ float parts[kRows > 1 ? kRows * 8 * LANES * NV : 1];
+  const int lanes = LANES ? LANES : blockDim.x, lane = LANES ? threadIdx.x % (LANES + !LANES) : threadIdx.x;
+  const int C = p.cols;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + (LANES ? threadIdx.x / (LANES + !LANES) : 0);
+  const int64_t mine = row - (int64_t)blockIdx.x * kRows;
+  struct Set { Raw8<T> h[NV], a[NV], g[NV]; float rstd; };
+  const auto load = [&](Set& s, int64_t at) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (v * LANES + lane), n = live ? C - c : 0;
-      if (n <= 0) continue;
-      load8<VEC>((const T*)p.h + row * C + c, n, xh[v]);
-      load8<VEC>((const T*)p.grad_y + row * C + c, n, a[v]);
+      const int c = 8 * (v * lanes + lane), n = at < p.rows ? C - c : 0;
+      s.h[v] = load8<VEC>((const T*)p.h + at * C + c, n);
+      s.a[v] = load8<VEC>((const T*)p.grad_y + at * C + c, n);
+      s.g[v] = load8<VEC>((const T*)p.grad_h + at * C + c, p.grad_h ? n : 0);
+    }
+    s.rstd = at < p.rows ? p.rstd[at] : 0.0f;
+  };
+  float acc[NV][8] = {}, w[NV][8];
+  const auto take = [&](Set& s, int turn) {
+    const bool live = row < p.rows;
+    const float rs = s.rstd;
+    float dot = 0.0f;
+    Set k = s;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (!VEC && i >= n) continue;
-        xh[v][i] *= rstd;
-        acc[v][i] = fmaf(a[v][i], xh[v][i], acc[v][i]);
-        a[v][i] *= w[v][i];
-        dot = fmaf(a[v][i], xh[v][i], dot);
+        const float xh = value<T>(k.h[v], i) * rs, gy = value<T>(k.a[v], i);
+        acc[v][i] = fmaf(gy, xh, acc[v][i]);
+        dot = fmaf(gy * w[v][i], xh, dot);
       }
     }
-    dot = row_sum<LANES>(dot, slot) / (float)C;
+    if (kAhead) load(s, row + step);
+    dot = row_sum<LANES>(dot, slots[turn]) / (float)C;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (v * LANES + lane), n = live ? C - c : 0;
+      const int c = 8 * (v * lanes + lane), n = live ? C - c : 0;
       if (n <= 0) continue;
-      float g[8] = {};
-      if (p.grad_h) load8<VEC>((const T*)p.grad_h + row * C + c, n, g);
+      float g[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] += rstd * (a[v][i] - xh[v][i] * dot);
-      store8<VEC>((T*)p.grad_x + row * C + c, n, g);
+      for (int i = 0; i < 8; ++i)
+        g[i] = value<T>(k.g[v], i) + rs * (value<T>(k.a[v], i) * w[v][i] - value<T>(k.h[v], i) * rs * dot);
+      store8<VEC>((T*)p.grad_x + row * C + c, n, rounded<T>(g));
     }
+    row += step;
+  };
+  Set set;
+  if (kAhead) load(set, row);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (v * lanes + lane);
+    load_weight<VEC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
+  }
+  for (int turn = 0; row - mine < p.rows; turn ^= 1) {
+    if (!kAhead) load(set, row);
+    take(set, turn);
   }
   if constexpr (kRows > 1) {   // the block's rows side by side
-    float* mine = parts + (threadIdx.x / LANES) * 8 * LANES * NV;
+    float* own = parts + (threadIdx.x / LANES) * 8 * LANES * NV;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine[8 * (v * LANES + lane) + i] = acc[v][i];
+      for (int i = 0; i < 8; ++i) own[8 * (v * LANES + lane) + i] = acc[v][i];
     __syncthreads();
     for (int c = threadIdx.x; c < C; c += 256) {
       float s = 0.0f;
@@ -277,27 +344,30 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_backward_kerne
   } else {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (v * LANES + lane);
-      for (int i = 0; i < 8 && c + i < C; ++i) p.part[(int64_t)blockIdx.x * C + c + i] = acc[v][i];
+      const int c = 8 * (v * lanes + lane);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)   // (an index known here: the sums stay in registers)
+        if (c + i < C) p.part[(int64_t)blockIdx.x * C + c + i] = acc[v][i];
     }
   }
 }
 
-// grad_w[c] = sum of part[b][c] over the blocks, in order: 64 columns a block, each by 16 threads
-// that take every sixteenth part.
+// grad_w[c] = sum of part[b][c] over the blocks, in order: 32 columns a block, each by 32 threads
+// that take every 32nd part.
 __global__ __launch_bounds__(1024) void norm_weight_kernel(const float* __restrict__ part, int parts, int cols,
                                                            float* __restrict__ grad_w) {
-  __shared__ float s[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+  __shared__ float s[32][33];
+  const int i = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + i;
   float v = 0.0f;
   if (c < cols)
-    for (int b = g; b < parts; b += 16) v += part[(int64_t)b * cols + c];
-  s[g][threadIdx.x & 63] = v;
+#pragma unroll 8
+    for (int b = g; b < parts; b += 32) v += part[(int64_t)b * cols + c];
+  s[g][i] = v;
   __syncthreads();
-  if (g == 0 && c < cols) {
-    for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
-    grad_w[c] = v;
-  }
+  v = s[i][g];   // part i of column g
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) v += __shfl_xor(v, d, 64);
+  if (i == 0 && blockIdx.x * 32 + g < cols) grad_w[blockIdx.x * 32 + g] = v;
 }
 
 bool aligned16(std::initializer_list<const void*> ps) {
@@ -306,18 +376,33 @@ bool aligned16(std::initializer_list<const void*> ps) {
   return true;
 }
 
-// Calls f with the number of lanes a row of `cols` elements gets and its chunks a lane: a lane a
-// chunk up to 8192 columns, two chunks beyond.
+// A row's lanes (0: a block of its own, of `threads`), the threads of a block and its rows.
+struct Shape {
+  int lanes, threads, rows;
+};
+Shape shape_of(int64_t cols) {
+  const int chunks = (int)((cols + 7) / 8);
+  if (chunks <= 16) return {16, 256, 16};
+  if (chunks <= 64) return {64, 256, 4};
+  const int each = chunks <= 1024 ? 1 : 2;   // chunks a lane
+  return {0, (chunks + 64 * each - 1) / (64 * each) * 64, 1};
+}
+
+// Blocks that take `rows` rows: as many as `lanes` lanes a compute unit make, and no more than there
+// are rows for. The norm takes 2048 (1024: 88 us at the size above, 4096: 102, a block a row: 101),
+// its gradient, whose every block writes a row of partial sums, 1024 (2048: 92 us, 4096: 103).
+int64_t blocks_of(Shape s, int64_t rows, int lanes) {
+  return std::max<int64_t>(1, std::min<int64_t>((rows + s.rows - 1) / s.rows, 256 * std::max(1, lanes / s.threads)));
+}
+
+// Calls f with the lanes of a row of `cols` elements and the chunks of a lane.
 template <typename F>
 hipError_t with_lanes(int cols, F f) {
-  const int chunks = (cols + 7) / 8;
-  if (chunks <= 16) return f.template operator()<16, 1>();
-  if (chunks <= 64) return f.template operator()<64, 1>();
-  if (chunks <= 128) return f.template operator()<128, 1>();
-  if (chunks <= 256) return f.template operator()<256, 1>();
-  if (chunks <= 512) return f.template operator()<512, 1>();
-  if (chunks <= 1024) return f.template operator()<1024, 1>();
-  return f.template operator()<1024, 2>();
+  const Shape s = shape_of(cols);
+  if (s.lanes == 16) return f.template operator()<16, 1>(s);
+  if (s.lanes == 64) return f.template operator()<64, 1>(s);
+  if (cols <= 8192) return f.template operator()<0, 1>(s);
+  return f.template operator()<0, 2>(s);
 }
 
 // Calls f with the rows' element type.
@@ -332,11 +417,8 @@ hipError_t with_type(int dtype, F f) {
 
 template <typename T, bool VEC, bool QUANT>
 hipError_t launch_norm_as(const NormParams& p, hipStream_t stream) {
-  return with_lanes(p.cols, [&]<int LANES, int NV>() {
-    constexpr int rows = LANES <= 64 ? 256 / LANES : 1, threads = LANES <= 64 ? 256 : LANES;
-    // (a launch of 2^32 threads or more would be cut short: blocks go on with further rows)
-    const int64_t grid = std::min<int64_t>((p.rows + rows - 1) / rows, 1 << 21);
-    norm_kernel<T, LANES, NV, VEC, QUANT><<<(unsigned)grid, threads, 0, stream>>>(p);
+  return with_lanes(p.cols, [&]<int LANES, int NV>(Shape s) {
+    norm_kernel<T, LANES, NV, VEC, QUANT><<<(unsigned)blocks_of(s, p.rows, 2048), s.threads, 0, stream>>>(p);
     return hipGetLastError();
   });
 }
@@ -351,24 +433,22 @@ hipError_t launch_norm(const NormParams& p, hipStream_t stream) {
   });
 }
 
-// Blocks of the gradient's first pass (rows of parts of the weight's gradient): two a compute
-// unit, and no more than there are rows.
-int norm_parts(int64_t rows) { return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 512)); }
+// Blocks of the gradient's first pass, each a row of partial sums of the weight's gradient.
+int norm_parts(int64_t rows, int64_t cols) { return (int)blocks_of(shape_of(cols), rows, 1024); }
 
 hipError_t launch_norm_backward(const NormGradParams& p, hipStream_t stream) {
   const bool vec = p.cols % 8 == 0 && aligned16({p.grad_y, p.h, p.grad_h, p.weight, p.grad_x});
   hipError_t e = with_type(p.dtype, [&]<typename T>() {
-    return with_lanes(p.cols, [&]<int LANES, int NV>() {
-      constexpr int threads = LANES <= 64 ? 256 : LANES;
+    return with_lanes(p.cols, [&]<int LANES, int NV>(Shape s) {
       if (vec)
-        norm_backward_kernel<T, LANES, NV, true><<<p.parts, threads, 0, stream>>>(p);
+        norm_backward_kernel<T, LANES, NV, true><<<p.parts, s.threads, 0, stream>>>(p);
       else
-        norm_backward_kernel<T, LANES, NV, false><<<p.parts, threads, 0, stream>>>(p);
+        norm_backward_kernel<T, LANES, NV, false><<<p.parts, s.threads, 0, stream>>>(p);
       return hipGetLastError();
     });
   });
   if (e != hipSuccess) return e;
-  norm_weight_kernel<<<(p.cols + 63) / 64, 1024, 0, stream>>>(p.part, p.parts, p.cols, p.grad_w);
+  norm_weight_kernel<<<(p.cols + 31) / 32, 1024, 0, stream>>>(p.part, p.parts, p.cols, p.grad_w);
   return hipGetLastError();
 }
 
