@@ -16,14 +16,16 @@
 // neighbouring elements (16 bytes of a 16-bit type) of a row, or two such chunks past 8192 columns;
 // an MX group of 32 is four lanes, whose largest magnitude takes two DPP steps. A row has 16 lanes,
 // a wave, or a block with as many waves as it has chunks for; the blocks that fit on the card at
-// once go over the rows, and load the next row before they sum one. Measured at that size, the
-// gradient with the sum of its weight's partial sums:
-//   a block a row, no row loaded in advance                 104 us,  its gradient 117 us
-//   blocks that go over the rows, rows loaded in advance    100                   101
-//   row sums by DPP and lane swaps (shuffles through LDS addresses: 20 more registers),
-//   loads that pass the caches by (the outputs stay there for the next kernel)
-//                                                            85 (6.2 TB/s)         84 (5.6 TB/s)
-// Stores that pass the caches by as well: 96 and 88.
+// once go over the rows, and load the next row before they sum one. Measured at that size, each
+// call's outputs in memory of their own, the gradient with the sum of its weight's partial sums:
+//   a block a row, no row loaded in advance                   104 us, its gradient 117 us
+//   blocks that go over the rows, rows loaded in advance, row
+//   sums by DPP and lane swaps (shuffles through LDS
+//   addresses: 20 more registers)                             105                   92
+//   and loads and stores of rows that pass the caches by    88-93 (5.7-6.0 TB/s)    86 (5.5 TB/s)
+// (the loads alone: 104 and 90; the stores alone: 100 and 89; the codes' stores too, of 8 bytes a
+// lane, which the caches put together: 96). Stores pass them by where the outputs are larger than
+// the cache (see with_access), so not the gradient's at this size.
 
 #include <algorithm>
 
@@ -63,17 +65,20 @@ __device__ __forceinline__ Raw8<T> rounded(const float (&f)[8]) {
   return r;
 }
 
-// VEC: every chunk is whole and starts at a multiple of 16 bytes. Otherwise a whole chunk is one
-// access too, at an address that is a multiple of an element only (the memory takes it; 32768 x
-// 1001 fp16: by elements 161 us, so 53), and a row's last elements go one by one.
+// How rows are read and written. WHOLE: every chunk is whole and starts at a multiple of 16 bytes;
+// rows are loaded past the caches. STREAM: stored past them, too. ANY: a whole chunk is one access
+// at an address that is a multiple of an element only (the memory takes it; 32768 x 1001 fp16: by
+// elements 161 us, so 53), a row's last elements go one by one.
+enum Access { ANY, WHOLE, STREAM };
+
 template <typename T> struct AnyRaw8 {
   Raw8<T> v;
 } __attribute__((packed, aligned(sizeof(T))));
 
-template <bool VEC, typename T>
+template <Access ACC, typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
   Raw8<T> r = {};
-  if constexpr (VEC) {
+  if constexpr (ACC != ANY) {
     if (n > 0) r = __builtin_nontemporal_load(reinterpret_cast<const Raw8<T>*>(p));
   } else if (n >= 8) {
     r = reinterpret_cast<const AnyRaw8<T>*>(p)->v;
@@ -89,9 +94,11 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
   return r;
 }
 
-template <bool VEC, typename T>
+template <Access ACC, typename T>
 __device__ __forceinline__ void store8(T* p, int n, Raw8<T> r) {
-  if constexpr (VEC) {
+  if constexpr (ACC == STREAM) {
+    __builtin_nontemporal_store(r, reinterpret_cast<Raw8<T>*>(p));
+  } else if constexpr (ACC == WHOLE) {
     *reinterpret_cast<Raw8<T>*>(p) = r;
   } else if (n >= 8) {
     reinterpret_cast<AnyRaw8<T>*>(p)->v = r;
@@ -107,17 +114,17 @@ __device__ __forceinline__ void store8(T* p, int n, Raw8<T> r) {
 }
 
 // The weight's, which is of the rows' type or fp32, as floats.
-template <bool VEC, typename T>
+template <Access ACC, typename T>
 __device__ __forceinline__ void load_weight(const void* w, bool fp32, int c, int n, float (&f)[8]) {
-  if (fp32) {
-    const Raw8<float> r = load8<VEC>((const float*)w + c, n);
+  const auto load = [&]<typename W>(const W* p) {
+    Raw8<W> r = {};
+    if constexpr (ACC == ANY) r = load8<ANY>(p, n);
+    else if (n > 0) r = *reinterpret_cast<const Raw8<W>*>(p);   // (every block's: through the caches)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = value<float>(r, i);
-  } else {
-    const Raw8<T> r = load8<VEC>((const T*)w + c, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = value<T>(r, i);
-  }
+    for (int i = 0; i < 8; ++i) f[i] = value<W>(r, i);
+  };
+  if (fp32) load((const float*)w + c);
+  else load((const T*)w + c);
 }
 
 // MX codes (8 elements; F as in device_common.h) of y over its group's scale to row element c.
@@ -184,7 +191,7 @@ __device__ __forceinline__ S row_sum(S v, S* slot) {
 // ---- the norm ---------------------------------------------------------------------------
 // NV chunks a thread (chunk v of lane l: elements 8 (v lanes + l)); a block takes rows
 // blockIdx.x kRows + i, + gridDim.x kRows, ... and loads the next while it sums one.
-template <typename T, int LANES, int NV, bool VEC, bool QUANT>
+template <typename T, int LANES, int NV, Access ACC, bool QUANT>
 __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) {
   constexpr int kRows = rows_of(LANES);   // rows of a block
   __shared__ double slots[2][16];
@@ -202,8 +209,8 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) 
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = 8 * (v * lanes + lane), n = at < p.rows ? C - c : 0;
-      x[v] = load8<VEC>((const T*)p.x + at * C + c, n);
-      if (p.residual) r[v] = load8<VEC>((const T*)p.residual + at * C + c, n);
+      x[v] = load8<ACC>((const T*)p.x + at * C + c, n);
+      if (p.residual) r[v] = load8<ACC>((const T*)p.residual + at * C + c, n);
     }
   };
   load(row);
@@ -211,7 +218,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) 
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = 8 * (v * lanes + lane);
-    load_weight<VEC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
+    load_weight<ACC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
   }
   for (int turn = 0; row - mine < p.rows; row += step, turn ^= 1) {
     const bool live = row < p.rows;
@@ -224,7 +231,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) 
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[v][i] = value<T>(x[v], i) + value<T>(r[v], i);
         x[v] = rounded<T>(h[v]);
-        if (n > 0) store8<VEC>((T*)p.h + row * C + c, n, x[v]);
+        if (n > 0) store8<ACC>((T*)p.h + row * C + c, n, x[v]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[v][i] = value<T>(x[v], i);
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) 
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rstd * w[v][i];
       const Raw8<T> out = rounded<T>(y);
-      if (p.y) store8<VEC>((T*)p.y + row * C + c, n, out);
+      if (p.y) store8<ACC>((T*)p.y + row * C + c, n, out);
       if constexpr (QUANT) {   // (C % 32 == 0: the four lanes of a group are all here)
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = value<T>(out, i);
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(NormParams p) 
 // ---- its gradient -----------------------------------------------------------------------
 // Rows to blocks and threads as above; the weight's gradient of a block's rows is summed in
 // registers and goes to part[block][C].
-template <typename T, int LANES, int NV, bool VEC>
+template <typename T, int LANES, int NV, Access ACC>
 __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_backward_kernel(NormGradParams p) {
   constexpr bool kAhead = NV == 1;   // (two chunks a lane, of 1024 lanes: no registers left for a second row)
   constexpr int kRows = rows_of(LANES);
@@ -283,9 +290,9 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_backward_kernel(NormG
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = 8 * (v * lanes + lane), n = at < p.rows ? C - c : 0;
-      s.h[v] = load8<VEC>((const T*)p.h + at * C + c, n);
-      s.a[v] = load8<VEC>((const T*)p.grad_y + at * C + c, n);
-      s.g[v] = load8<VEC>((const T*)p.grad_h + at * C + c, p.grad_h ? n : 0);
+      s.h[v] = load8<ACC>((const T*)p.h + at * C + c, n);
+      s.a[v] = load8<ACC>((const T*)p.grad_y + at * C + c, n);
+      s.g[v] = load8<ACC>((const T*)p.grad_h + at * C + c, p.grad_h ? n : 0);
     }
     s.rstd = at < p.rows ? p.rstd[at] : 0.0f;
   };
@@ -314,7 +321,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_backward_kernel(NormG
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         g[i] = value<T>(k.g[v], i) + rs * (value<T>(k.a[v], i) * w[v][i] - value<T>(k.h[v], i) * rs * dot);
-      store8<VEC>((T*)p.grad_x + row * C + c, n, rounded<T>(g));
+      store8<ACC>((T*)p.grad_x + row * C + c, n, rounded<T>(g));
     }
     row += step;
   };
@@ -323,7 +330,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_backward_kernel(NormG
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = 8 * (v * lanes + lane);
-    load_weight<VEC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
+    load_weight<ACC, T>(p.weight, p.weight_dtype == 0, c, C - c, w[v]);
   }
   for (int turn = 0; row - mine < p.rows; turn ^= 1) {
     if (!kAhead) load(set, row);
@@ -389,8 +396,8 @@ Shape shape_of(int64_t cols) {
 }
 
 // Blocks that take `rows` rows: as many as `lanes` lanes a compute unit make, and no more than there
-// are rows for. The norm takes 2048 (1024: 88 us at the size above, 4096: 102, a block a row: 101),
-// its gradient, whose every block writes a row of partial sums, 1024 (2048: 92 us, 4096: 103).
+// are rows for. The norm takes 2048 (1024: 100 us at the size above, a block a row: 101), its
+// gradient, whose every block writes a row of partial sums, 1024 (2048: 92 us, 4096: 103).
 int64_t blocks_of(Shape s, int64_t rows, int lanes) {
   return std::max<int64_t>(1, std::min<int64_t>((rows + s.rows - 1) / s.rows, 256 * std::max(1, lanes / s.threads)));
 }
@@ -415,10 +422,22 @@ hipError_t with_type(int dtype, F f) {
   }
 }
 
-template <typename T, bool VEC, bool QUANT>
+// Calls f with the access to rows of `cols` elements in tensors ps, of which `bytes` are written.
+// Rows that stay in the 256 MB cache are read from there by the next kernel: norm and a sum of its
+// outputs (2 x 29 MB): 36 us, stored past the cache 40; the gradient and a product of it (117 MB):
+// 267 and 274. Past its size nothing stays: norm (2 x 117 MB) 88 and 81, the gradient (235 MB) and
+// its negation 249 and 239.
+template <typename F>
+hipError_t with_access(int cols, std::initializer_list<const void*> ps, int64_t bytes, F f) {
+  if (cols % 8 || !aligned16(ps)) return f.template operator()<ANY>();
+  if (bytes <= (int64_t)192 << 20) return f.template operator()<WHOLE>();
+  return f.template operator()<STREAM>();
+}
+
+template <typename T, Access ACC, bool QUANT>
 hipError_t launch_norm_as(const NormParams& p, hipStream_t stream) {
   return with_lanes(p.cols, [&]<int LANES, int NV>(Shape s) {
-    norm_kernel<T, LANES, NV, VEC, QUANT><<<(unsigned)blocks_of(s, p.rows, 2048), s.threads, 0, stream>>>(p);
+    norm_kernel<T, LANES, NV, ACC, QUANT><<<(unsigned)blocks_of(s, p.rows, 2048), s.threads, 0, stream>>>(p);
     return hipGetLastError();
   });
 }
@@ -426,10 +445,11 @@ hipError_t launch_norm_as(const NormParams& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_norm(const NormParams& p, hipStream_t stream) {
-  const bool vec = p.cols % 8 == 0 && aligned16({p.x, p.residual, p.weight, p.y, p.h});
   return with_type(p.dtype, [&]<typename T>() {
-    if (p.quant) return vec ? launch_norm_as<T, true, true>(p, stream) : launch_norm_as<T, false, true>(p, stream);
-    return vec ? launch_norm_as<T, true, false>(p, stream) : launch_norm_as<T, false, false>(p, stream);
+    const int64_t bytes = p.rows * p.cols * (int64_t)sizeof(T) * ((p.y != nullptr) + (p.residual != nullptr));
+    return with_access(p.cols, {p.x, p.residual, p.weight, p.y, p.h}, bytes, [&]<Access ACC>() {
+      return p.quant ? launch_norm_as<T, ACC, true>(p, stream) : launch_norm_as<T, ACC, false>(p, stream);
+    });
   });
 }
 
@@ -437,14 +457,13 @@ hipError_t launch_norm(const NormParams& p, hipStream_t stream) {
 int norm_parts(int64_t rows, int64_t cols) { return (int)blocks_of(shape_of(cols), rows, 1024); }
 
 hipError_t launch_norm_backward(const NormGradParams& p, hipStream_t stream) {
-  const bool vec = p.cols % 8 == 0 && aligned16({p.grad_y, p.h, p.grad_h, p.weight, p.grad_x});
   hipError_t e = with_type(p.dtype, [&]<typename T>() {
-    return with_lanes(p.cols, [&]<int LANES, int NV>(Shape s) {
-      if (vec)
-        norm_backward_kernel<T, LANES, NV, true><<<p.parts, s.threads, 0, stream>>>(p);
-      else
-        norm_backward_kernel<T, LANES, NV, false><<<p.parts, s.threads, 0, stream>>>(p);
-      return hipGetLastError();
+    return with_access(p.cols, {p.grad_y, p.h, p.grad_h, p.weight, p.grad_x}, p.rows * p.cols * (int64_t)sizeof(T),
+                       [&]<Access ACC>() {
+      return with_lanes(p.cols, [&]<int LANES, int NV>(Shape s) {
+        norm_backward_kernel<T, LANES, NV, ACC><<<p.parts, s.threads, 0, stream>>>(p);
+        return hipGetLastError();
+      });
     });
   });
   if (e != hipSuccess) return e;
