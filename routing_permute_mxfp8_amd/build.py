@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libmoe_mx.so"
 SOURCES = ["csrc/api.cpp", "csrc/routing.hip", "csrc/permute_quant.hip", "csrc/tiles.hip", "csrc/gmm.hip",
            "csrc/gmm_stream.hip", "csrc/combine.hip", "csrc/peaks.hip", "csrc/noalloc.hip", "csrc/gate.hip",
-           "csrc/fp4_matmul.hip", "csrc/fp4_tile.hip", "csrc/norm.hip", "csrc/gmm16.hip",
+           "csrc/fp4_matmul.hip", "csrc/fp4_tile.hip", "csrc/norm.hip", "csrc/gmm16.hip", "csrc/gmm16_few.hip",
            "csrc/gmm16_forward.hip", "csrc/gmm16_transposed.hip", "csrc/gmm16_weights.hip"]
 ARCH = os.environ.get("MOE_MX_ARCH", "gfx950")
 

@@ -227,6 +227,8 @@ int tile_rows(const Gmm16Params& p) {
 }  // namespace
 
 void gmm16_plan(Gmm16Params& p) {
+  p.few = gmm16_is_few(p);
+  if (p.few) return;
   p.mt = tile_rows(p);
   const int64_t rows_b = p.wgrad ? p.rows : (int64_t)p.groups * (p.trans ? p.k : p.n);
   const int cols_a = p.wgrad ? p.n : p.k, cols_b = p.wgrad || !p.trans ? p.k : p.n;
@@ -242,8 +244,9 @@ void gmm16_plan(Gmm16Params& p) {
 
 hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {
   if (p.rows <= 0 && !p.wgrad) return hipSuccess;
+  if (p.few) return launch_gmm16_few(p, stream);
   const auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  if (!p.mt || !((p.copy_a || on16(p.a)) && (p.copy_b || on16(p.b))))
+  if (!((p.copy_a || on16(p.a)) && (p.copy_b || on16(p.b))))
     return p.half ? launch_as<_Float16>(p, stream) : launch_as<__bf16>(p, stream);
   Gmm16Params q = p;
   hipError_t e;

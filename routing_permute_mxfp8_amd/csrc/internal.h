@@ -386,9 +386,12 @@ struct Gmm16Params {
   uint16_t* a16 = nullptr;
   uint16_t* b16 = nullptr;
   bool odd = false;                // out is stored by elements
+  bool few = false;                // the kernel of few rows takes it
 };
 constexpr int kTile16Units = 256;  // compute units that the workspace of shared items is laid out for
 void gmm16_plan(Gmm16Params& p);
+bool gmm16_is_few(const Gmm16Params& p);
+hipError_t launch_gmm16_few(const Gmm16Params& p, hipStream_t stream);
 hipError_t launch_gmm16_forward(const Gmm16Params& p, hipStream_t stream);
 hipError_t launch_gmm16_transposed(const Gmm16Params& p, hipStream_t stream);
 hipError_t launch_gmm16_weights(const Gmm16Params& p, hipStream_t stream);
