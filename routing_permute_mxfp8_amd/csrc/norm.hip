@@ -57,7 +57,12 @@ __device__ __forceinline__ Raw8<T> rounded(const float (&f)[8]) {
       r[i] = __float_as_uint(f[i]);
     } else if constexpr (__is_same(T, _Float16)) {
       typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-      r[i] = __builtin_bit_cast(uint32_t, h2{(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
+      // As fp32 first, for every use of the value: the compiler may turn a product and its
+      // conversion into one instruction that rounds once, here and not there, so that the codes
+      // would be those of another value than the one stored.
+      float a = f[2 * i], b = f[2 * i + 1];
+      asm("" : "+v"(a), "+v"(b));
+      r[i] = __builtin_bit_cast(uint32_t, h2{(_Float16)a, (_Float16)b});
     } else {
       r[i] = bf16x2(f[2 * i], f[2 * i + 1]);
     }

@@ -12,8 +12,9 @@ subnormal of T):
          64 lanes and 16 waves are joined: 16 + 6 + 16 additions and the division, so sum(a xh) / C
          is off by at most D = 42 u sum|a xh| / C; rstd (a - xh dot) + grad_h then takes up to 5
          more roundings of each term: 5 u rstd (|a| + |xh dot|) + rstd |xh| D + u |grad_x|, then T;
-  grad_w a block adds at most rows / 512 + 1 rows (a row group of up to 16 rows each), 16 of them
-         and 32 + 16 parts are joined: (rows / 512 + 68) u sum|grad_y xh|."""
+  grad_w a thread adds at most rows / 256 + 1 rows (narrow ones: rows / 4096 + 1), 16 of them, up to
+         32 parts and 5 pairs of sums are joined: rows / 256 + 54 additions, no more than the
+         rows / 512 + 68 allowed, u sum|grad_y xh| each, up to 7168 rows."""
 import numpy as np
 import pytest
 import torch
@@ -268,3 +269,39 @@ def test_in_place_gradients():
                                              ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
             torch.cuda.synchronize()
             assert torch.equal((a, b)[place], want[0]) and torch.equal(gw, want[1])
+
+
+@pytest.mark.parametrize("cols", [100, 500, 1001, 2048, 7168, 8200, 16384])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_blocks_of_many_rows(cols, dtype):
+    """More rows than there are blocks, so that a block loads one while it sums another; codes of them, too."""
+    x, r, w = rows_of(2600, cols, dtype), rows_of(2600, cols, dtype, 2), weight_of(cols, dtype)
+    say(f"rms_norm 2600x{cols} {dtype}")
+    check_norm(x, r, w, rp.rms_norm(on(x), on(w), on(r)))
+    y, h, rstd, codes, scales = rp.rms_norm(on(x), on(w), on(r), quant_mode=rp.QUANT_E4M3) if cols % 32 == 0 else (None,) * 5
+    if codes is not None:
+        check_norm(x, r, w, (y, h, rstd, codes, scales))
+        want_codes, want_scales = rp.mx_quantize(y, quant_mode=rp.QUANT_E4M3)
+        assert torch.equal(codes, want_codes.view(torch.uint8)) and torch.equal(scales, want_scales.view(torch.uint8))
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(16500, 7168, torch.bfloat16), (30000, 2048, torch.float32),
+                                             (270000, 8200, torch.bfloat16)])
+def test_large(rows, cols, dtype):
+    """Outputs larger than the cache, and of more than 2^31 elements: every row as in a small call."""
+    say(f"rms_norm {rows}x{cols} {dtype}")
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    x, r = (torch.empty((rows, cols), dtype=dtype, device=DEV).normal_(0, 1, generator=gen) for _ in range(2))
+    w = on(weight_of(cols, dtype))
+    y, h, rstd, _, _ = rp.rms_norm(x, w, r)
+    gx, gw = rp.rms_norm_backward(x, h, w, rstd, grad_h=r)
+    want_w, mag = torch.zeros(cols, dtype=torch.float64, device=DEV), torch.zeros(cols, dtype=torch.float64, device=DEV)
+    for lo in range(0, rows, 5000):
+        some = slice(lo, lo + 5000)
+        part = rp.rms_norm(x[some], w, r[some])
+        assert torch.equal(y[some], part[0]) and torch.equal(h[some], part[1]) and torch.equal(rstd[some], part[2]), lo
+        assert torch.equal(gx[some], rp.rms_norm_backward(x[some], h[some], w, rstd[some], grad_h=r[some])[0]), lo
+        terms = x[some].double() * (h[some].double() * rstd[some].double()[:, None])
+        want_w += terms.sum(0)
+        mag += terms.abs().sum(0)
+    assert bool(((gw.double() - want_w).abs() <= (rows / 256 + 54) * U * mag).all())
