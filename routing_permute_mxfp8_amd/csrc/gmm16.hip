@@ -132,28 +132,23 @@ hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
 }
 
 // Rows of a matrix of 16-bit elements copied to rows of `pitch` elements, a multiple of 8, with zeros
-// behind: 8 elements of the copy a thread.
+// behind: 8 elements of the copy a thread, read in one piece (at any element: load_chunk). A block
+// has `lines` rows at a time, `lines` x `per` threads at work; one row's chunks past 256 in turns.
 __global__ __launch_bounds__(256) void pad16_kernel(const uint16_t* __restrict__ from, int64_t rows, int cols,
-                                                    uint16_t* __restrict__ to, int pitch) {
-  const int per = pitch / 8;
-  const int64_t all = rows * per;
-  for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < all; v += (int64_t)gridDim.x * 256) {
-    const int64_t r = v / per;
-    const int c = (int)(v - r * per) * 8;
-    uint16_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? from[r * cols + c + i] : (uint16_t)0;
-    u32x4 u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
-    reinterpret_cast<u32x4*>(to)[v] = u;
+                                                    uint16_t* __restrict__ to, int pitch, int lines) {
+  const int per = pitch / 8, line = lines > 1 ? threadIdx.x / per : 0, first = threadIdx.x - line * per;
+  if (line >= lines) return;
+  for (int64_t r = (int64_t)blockIdx.x * lines + line; r < rows; r += (int64_t)gridDim.x * lines) {
+    for (int c = first; c < per; c += 256)
+      *reinterpret_cast<u32x4*>(to + r * pitch + 8 * c) = load_chunk<false>(from + r * cols + 8 * c, cols - 8 * c);
   }
 }
 
 hipError_t launch_pad16(const void* from, int64_t rows, int cols, uint16_t* to, int pitch, hipStream_t stream) {
-  const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
-  if (blocks == 0) return hipSuccess;
-  pad16_kernel<<<(unsigned)std::min<int64_t>(blocks, 1 << 20), 256, 0, stream>>>((const uint16_t*)from, rows, cols, to, pitch);
+  if (rows == 0) return hipSuccess;
+  const int lines = std::max(1, 256 / (pitch / 8));
+  const int64_t blocks = std::min<int64_t>((rows + lines - 1) / lines, 1 << 20);
+  pad16_kernel<<<(unsigned)blocks, 256, 0, stream>>>((const uint16_t*)from, rows, cols, to, pitch, lines);
   return hipGetLastError();
 }
 
@@ -237,7 +232,7 @@ void gmm16_plan(Gmm16Params& p) {
   p.copy_a = p.pitch_a != cols_a ? (size_t)p.rows * p.pitch_a : 0;
   p.copy_b = p.pitch_b != cols_b ? (size_t)rows_b * p.pitch_b : 0;
   p.gain = kGain;
-  const int64_t steps = p.wgrad ? p.rows / p.groups / 64 : (p.k + 63) / 64;
+  const int64_t steps = ((p.wgrad ? p.rows : (int64_t)p.k) + 63) / 64;   // (wgrad: one group may have all rows)
   for (const Shape16& s : kShapes)
     if (s.mt == p.mt) p.part_floats = steps - (steps + 1) / 2 >= p.gain ? (size_t)kTile16Units * s.blocks * s.mt * s.nt : 0;
 }

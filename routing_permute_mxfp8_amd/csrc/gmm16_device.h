@@ -1,4 +1,4 @@
-// Device helpers of the 16-bit grouped products (gmm16.hip, gmm16_tile.hip).
+// Device helpers of the 16-bit grouped products (gmm16.hip, gmm16_few.hip, gmm16_tile.h).
 #pragma once
 
 #include "device_common.h"
@@ -46,6 +46,27 @@ template <> struct Mfma<_Float16> {
     else return __builtin_bit_cast(uint16_t, (_Float16)v);
   }
 };
+
+// 16 bytes at any 16-bit element.
+struct AnyChunk {
+  u32x4 v;
+} __attribute__((packed, aligned(2)));
+
+// Elements 0 .. 7 at p, of which n are the row's: the others are 0.
+template <bool VEC>
+__device__ __forceinline__ u32x4 load_chunk(const uint16_t* p, int n) {
+  u32x4 v = {};
+  if constexpr (VEC) {
+    if (n > 0) v = *reinterpret_cast<const u32x4*>(p);
+  } else if (n >= 8) {
+    v = reinterpret_cast<const AnyChunk*>(p)->v;
+  } else if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+  }
+  return v;
+}
 
 // ends[g] = tiles of MT rows of groups 0 .. g (all 64 WAVES threads; ends has room for kMaxGroups,
 // scratch for WAVES). Returns the number of tiles.

@@ -35,26 +35,6 @@ __device__ __forceinline__ int group_of_row(const int32_t* off, int groups, int 
   return n;
 }
 
-struct AnyChunk {
-  u32x4 v;
-} __attribute__((packed, aligned(2)));
-
-// Elements 0 .. 7 at p, of which n are the row's: the others are 0.
-template <bool VEC>
-__device__ __forceinline__ u32x4 load_chunk(const uint16_t* p, int n) {
-  u32x4 v = {};
-  if constexpr (VEC) {
-    if (n > 0) v = *reinterpret_cast<const u32x4*>(p);
-  } else if (n >= 8) {
-    v = reinterpret_cast<const AnyChunk*>(p)->v;
-  } else if (n > 0) {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
-  }
-  return v;
-}
-
 // RB: blocks of 8 rows that a group can have. VEC: every row is of whole 16-byte vectors.
 template <typename T, typename O, int RB, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void gmm16_few_kernel(Gmm16Params p) {

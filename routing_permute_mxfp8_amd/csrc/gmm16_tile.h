@@ -51,7 +51,7 @@ struct Tile16Args {
   bool out_fp32;
   void* out;
   float* part;           // workspace of shared items: a tile for each block, or null: items are not shared
-  int steps, gain;       // steps of an item (kWeights: on average); how many have to be saved for an item to be shared
+  int steps, gain;       // steps of an item (not kWeights); how many have to be saved for an item to be shared
 };
 
 template <int WAVES, int WC, int CB, int RB>
@@ -77,22 +77,65 @@ __device__ __forceinline__ void slot_barrier() {
 
 // ---- which item a block works at ------------------------------------------------------------
 // The items are the output's tiles by their channel blocks. Each XCD takes a contiguous share of
-// them, dealt to its blocks in turn. What is left for a last, part-filled round is shared: the
-// contraction of each of these items is cut into `parts`, one for each block; the blocks leave
-// fp32 tiles, which gmm16_join_kernel adds in order.
+// them (kWeights: of each group's, whose items are as long as the group has rows; which eighth it
+// takes moves on by one with each group), dealt to its blocks in turn. What is left for a last,
+// part-filled round is shared: the contraction of each of these items is cut into `parts`, one for
+// each block; the blocks leave fp32 tiles, which gmm16_join_kernel adds in order.
+__device__ __forceinline__ int eighth(int each, int i) { return (int)((int64_t)each * i / 8); }
 struct Share {
-  int64_t begin;          // the XCD's first item
+  int64_t begin;          // the XCD's first item (not kWeights)
   int full, rem, parts;   // whole rounds, items behind them, blocks an item of those
 };
-__device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int xcd, int per) {
+// each: items of a group (kWeights). steps: those of the longest item.
+template <int FORM>
+__device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int each, int steps, int xcd, int per) {
   Share s;
-  s.begin = total * xcd / 8;
-  const int64_t n = total * (xcd + 1) / 8 - s.begin;
+  int64_t n;
+  if constexpr (FORM == kWeights) {
+    s.begin = 0;
+    n = (int64_t)(p.groups / 8) * each;
+    for (int g = 0; g < p.groups % 8; ++g) n += eighth(each, (xcd + g) % 8 + 1) - eighth(each, (xcd + g) % 8);
+  } else {
+    s.begin = total * xcd / 8;
+    n = total * (xcd + 1) / 8 - s.begin;
+  }
   s.full = (int)(n / per);
   s.rem = (int)(n - (int64_t)s.full * per);
-  s.parts = s.rem ? min(per / s.rem, p.steps / 4) : 1;   // (a part has four steps at least)
-  if (!p.part || s.parts < 2 || p.steps - (p.steps + s.parts - 1) / s.parts < p.gain) s.parts = 1;
+  s.parts = s.rem ? min(per / s.rem, steps / 4) : 1;   // (a part has four steps at least)
+  if (!p.part || s.parts < 2 || steps - (steps + s.parts - 1) / s.parts < p.gain) s.parts = 1;
   return s;
+}
+
+// Number n of the XCD's items among all.
+template <int FORM>
+__device__ __forceinline__ int64_t item_of(const Share& s, int each, int xcd, int64_t n) {
+  if constexpr (FORM != kWeights) return s.begin + n;
+  int g = (int)(n / each) * 8;   // (the XCD takes `each` items of eight groups in a row)
+  int left = (int)(n % each);
+  for (;; ++g) {
+    const int first = eighth(each, (xcd + g) % 8), size = eighth(each, (xcd + g) % 8 + 1) - first;
+    if (left < size) return (int64_t)g * each + first + left;
+    left -= size;
+  }
+}
+
+// The steps of the longest item: kWeights: of the largest group (all threads; scratch for WAVES).
+template <int FORM, int WAVES>
+__device__ __forceinline__ int longest(const Tile16Args& p, int* scratch) {
+  if (FORM != kWeights || !p.part) return p.steps;
+  int most = 0;
+  for (int g = threadIdx.x; g < p.groups; g += 64 * WAVES) {
+    int lo, hi;
+    group_rows(p.off, g, p.rows, &lo, &hi);
+    most = max(most, hi - lo);
+  }
+  for (int s = 1; s < 64; s *= 2) most = max(most, __shfl_xor(most, s, 64));
+  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) most = max(most, scratch[w]);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane((most + kCon - 1) / kCon);
 }
 
 // Item `it`: (group, first row, rows, tile and channel block). Four row tiles run through the
@@ -153,25 +196,40 @@ __device__ __forceinline__ Item16 item16(const int4& v, int ncb) {
   return r;
 }
 
+// Four neighbouring values at any element of a row, `left` of which are the row's.
+template <typename V>
+struct AnyFour {
+  V v;
+} __attribute__((packed, aligned(sizeof(V) / 4)));
+template <typename O, typename V>
+__device__ __forceinline__ void store_any(O* to, int left, V v) {
+  if (left >= 4) {
+    reinterpret_cast<AnyFour<V>*>(to)->v = v;
+  } else {
+    O one[4];
+    __builtin_memcpy(one, &v, sizeof(v));
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < left) to[i] = one[i];
+  }
+}
+
 // ---- output -----------------------------------------------------------------------------------
 // A row block's accumulators: lane (g, r) holds row r, channels 4 g + 0..3 of each 16-channel block: 64
 // neighbouring bytes of a row in fp32. Of 16-bit values those of two blocks are exchanged until a
 // lane has 8 neighbouring channels and a row's 64 bytes are in lanes l, l + 32, l + 16, l + 48
 // (pieces of 8 bytes would be write requests of their own to the L2). ODD: the output's rows are no
-// whole 16-byte vectors, and stored by elements.
+// whole 16-byte vectors: a lane's 4 channels are one store at any element (store_any).
 template <bool ODD, typename T, int CB>
 __device__ __forceinline__ void store_rows(const Tile16Args& p, const v4f (&acc)[CB], bool valid, int64_t row, int c0) {
   const int g4 = (threadIdx.x & 63) >> 4;
   if constexpr (ODD) {
 #pragma unroll
-    for (int i = 0; i < CB; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = c0 + 16 * i + 4 * g4 + e;
-        if (!valid || c >= p.nc) continue;
-        if (p.out_fp32) ((float*)p.out)[row * p.nc + c] = acc[i][e];
-        else ((uint16_t*)p.out)[row * p.nc + c] = Mfma<T>::template out<uint16_t>(acc[i][e]);
-      }
+    for (int i = 0; i < CB; ++i) {
+      const int c = c0 + 16 * i + 4 * g4, left = valid ? p.nc - c : 0;
+      if (p.out_fp32) store_any((float*)p.out + row * p.nc + c, left, acc[i]);
+      else store_any((uint16_t*)p.out + row * p.nc + c, left, uint2{Mfma<T>::pair(acc[i][0], acc[i][1]), Mfma<T>::pair(acc[i][2], acc[i][3])});
+    }
   } else if (p.out_fp32) {
     float* to = (float*)p.out + row * p.nc;
 #pragma unroll
@@ -210,7 +268,7 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
 
   const int tiles = FORM == kWeights ? p.groups * nrt : count_tiles<MT, WAVES>(p.off, p.groups, p.rows, ends, reinterpret_cast<int*>(list));
   const int xcd = blockIdx.x & 7, slot_in = blockIdx.x >> 3, per = gridDim.x >> 3;
-  const Share share = share_of(p, (int64_t)tiles * ncb, xcd, per);
+  const Share share = share_of<FORM>(p, (int64_t)tiles * ncb, nrt * ncb, longest<FORM, WAVES>(p, reinterpret_cast<int*>(list)), xcd, per);
   const bool shared = share.parts > 1 && slot_in < share.rem * share.parts;   // the block's last item is a part of one
   const int count = share.full + (share.parts > 1 ? shared : slot_in < share.rem);
   if (count == 0) return;   // the whole block
@@ -219,7 +277,7 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     if (tid < kList && first + tid < count) {
       const int n = first + tid;
       const int in = n == share.full && shared ? slot_in % share.rem : slot_in;
-      list[tid] = describe16<FORM, MT>(p, ends, tiles, nrt, ncb, share.begin + (int64_t)n * per + in);
+      list[tid] = describe16<FORM, MT>(p, ends, tiles, nrt, ncb, item_of<FORM>(share, nrt * ncb, xcd, (int64_t)n * per + in));
     }
     __syncthreads();
   };
@@ -573,9 +631,9 @@ __global__ __launch_bounds__(64 * WAVES) void gmm16_join_kernel(Tile16Args p, in
   int tiles = p.groups * nrt;
   if constexpr (FORM != kWeights) tiles = count_tiles<S::kMT, WAVES>(p.off, p.groups, p.rows, ends, scratch);
   const int xcd = blockIdx.x & 7, r = blockIdx.x >> 3, per = blocks >> 3;
-  const Share share = share_of(p, (int64_t)tiles * ncb, xcd, per);
+  const Share share = share_of<FORM>(p, (int64_t)tiles * ncb, nrt * ncb, longest<FORM, WAVES>(p, scratch), xcd, per);
   if (share.parts < 2 || r >= share.rem) return;
-  const Item16 it = item16<FORM>(describe16<FORM, S::kMT>(p, ends, tiles, nrt, ncb, share.begin + (int64_t)share.full * per + r), ncb);
+  const Item16 it = item16<FORM>(describe16<FORM, S::kMT>(p, ends, tiles, nrt, ncb, item_of<FORM>(share, nrt * ncb, xcd, (int64_t)share.full * per + r)), ncb);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = blockIdx.y;
   v4f acc[CB] = {};
   for (int part = 0; part < share.parts; ++part) {
@@ -662,7 +720,7 @@ hipError_t launch_tile16_form(const Gmm16Params& p, hipStream_t stream) {
   Tile16Args a{};
   a.row = (const uint16_t*)p.a; a.chan = (const uint16_t*)p.b; a.pitch_row = p.pitch_a; a.pitch_chan = p.pitch_b;
   a.off = p.off; a.groups = p.groups; a.rows = (int)p.rows; a.out_fp32 = p.out_fp32; a.out = p.out;
-  if (FORM == kWeights) { a.nc = p.k; a.nr = p.n; a.con = a.con_t = kCon; a.steps = (int)(p.rows / p.groups / kCon); }
+  if (FORM == kWeights) { a.nc = p.k; a.nr = p.n; a.con = a.con_t = kCon; a.steps = 0; }
   else { a.nc = p.n; a.nr = 1; a.con = (p.k + 7) / 8 * 8; a.con_t = p.k; a.steps = (a.con + kCon - 1) / kCon; }
   a.part = p.part; a.gain = p.gain;
   return p.half ? launch_tile16_odd<FORM, _Float16>(a, p.mt, p.odd, stream) : launch_tile16_odd<FORM, __bf16>(a, p.mt, p.odd, stream);
