@@ -506,11 +506,15 @@ moe::Gmm16Params gmm16_params(int dtype, int out_dtype, int64_t rows, const int3
   return p;
 }
 
-void carve_gmm16(Carver& cv, moe::Gmm16Params& p) {
-  moe::gmm16_plan(p);
+void carve_gmm16(Carver& cv, moe::Gmm16Params& p) {   // (of a plan)
   if (p.part_floats) p.part = cv.take<float>(p.part_floats);
   if (p.copy_a) p.a16 = cv.take<uint16_t>(p.copy_a);
   if (p.copy_b) p.b16 = cv.take<uint16_t>(p.copy_b);
+}
+
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
 }
 
 moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size_t workspace_bytes, hipStream_t stream) {
@@ -518,6 +522,7 @@ moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size
     return fail(MOE_ERR_INVALID_ARG, "%s: both operands and out must be non-NULL", who);
   if (misaligned(2, {p.a, p.b}) || misaligned(p.out_fp32 ? 4 : 2, {p.out}) || misaligned(4, {p.off}))
     return fail(MOE_ERR_INVALID_ARG, "%s: tensors must be aligned to their elements", who);
+  moe::gmm16_plan(p);
   Carver cv(nullptr);
   carve_gmm16(cv, p);
   if (cv.off > 0) {
@@ -525,6 +530,11 @@ moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size
     Carver wc(workspace);
     carve_gmm16(wc, p);
   }
+  const int64_t weights = (int64_t)p.groups * p.n * p.k, out_size = p.out_fp32 ? 4 : 2;
+  const int64_t a_bytes = 2 * p.rows * (p.wgrad ? p.n : p.k), b_bytes = 2 * (p.wgrad ? p.rows * p.k : weights);
+  const int64_t out_bytes = out_size * (p.wgrad ? weights : p.rows * p.n);
+  if (overlap(p.out, out_bytes, p.a, a_bytes) || overlap(p.out, out_bytes, p.b, b_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "%s: out overlaps an operand", who);
   hipError_t e = moe::launch_gmm16(p, stream);
   if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s launch: %s", who, hipGetErrorString(e));
   return ok();
@@ -1248,6 +1258,7 @@ moe_status moe_grouped_matmul_workspace_size(int64_t rows, int64_t num_groups, i
   Carver cv(nullptr);
   moe::Gmm16Params p = gmm16_params(MOE_DTYPE_BF16, MOE_DTYPE_FP32, rows, nullptr, num_groups, n, k);
   p.trans = transpose_w != 0;
+  moe::gmm16_plan(p);
   carve_gmm16(cv, p);
   *bytes = cv.off;
   return ok();
@@ -1273,6 +1284,7 @@ moe_status moe_grouped_matmul_wgrad_workspace_size(int64_t rows, int64_t num_gro
   Carver cv(nullptr);
   moe::Gmm16Params p = gmm16_params(MOE_DTYPE_BF16, MOE_DTYPE_FP32, rows, nullptr, num_groups, n, k);
   p.wgrad = true;
+  moe::gmm16_plan(p);
   carve_gmm16(cv, p);
   *bytes = cv.off;
   return ok();

@@ -171,9 +171,11 @@ constexpr Shape16 kShapes[] = {{256, 256, 1, 1.80f, 4.0f}, {192, 256, 1, 1.45f, 
 double tiles_of(double mean, int mt, bool one) {
   if (one) return std::ceil(mean / mt);
   if (mean <= 0) return 0;
+  if (mean > 256.0 * mt) return mean / mt + 0.5;   // (the sum's value to 1 in 1000)
   const double sd = std::sqrt(mean);
-  double sum = 1.0 - std::exp(-mean);   // groups with rows at all
-  for (double at = mt; at < mean + 6 * sd; at += mt) sum += 0.5 * std::erfc((at + 0.5 - mean) / (std::sqrt(2.0) * sd));
+  const double sure = std::floor(std::max(0.0, mean - 6 * sd) / mt);   // tiles that all groups fill
+  double sum = sure > 0 ? sure : 1.0 - std::exp(-mean);                // (groups with rows at all)
+  for (double at = mt * std::max(1.0, sure); at < mean + 6 * sd; at += mt) sum += 0.5 * std::erfc((at + 0.5 - mean) / (std::sqrt(2.0) * sd));
   return sum;
 }
 

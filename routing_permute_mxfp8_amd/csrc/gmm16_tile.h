@@ -24,8 +24,7 @@
 #pragma once
 
 #include <algorithm>
-#include <map>
-#include <mutex>
+#include <atomic>
 
 #include "gmm16_device.h"
 #include "internal.h"
@@ -652,22 +651,19 @@ __global__ __launch_bounds__(64 * WAVES) void gmm16_join_kernel(Tile16Args p, in
 }
 
 // Blocks of a launch (the device's compute units, rounded up to whole XCDs' shares, and no more than
-// the workspace of shared items is laid out for); the kernel's LDS size set once for each device.
-inline hipError_t tile16_grid(const void* kernel, int lds, int* grid) {
-  static std::mutex mu;
-  static std::map<std::pair<int, const void*>, int> known;
+// the workspace of shared items is laid out for); the kernel's LDS size set. `known`: what was found
+// for the first devices, a kernel's own, 0 at the start.
+constexpr int kDevices = 64;
+inline hipError_t tile16_grid(const void* kernel, int lds, std::atomic<int> (&known)[kDevices], int* grid) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  auto at = known.find({dev, kernel});
-  if (at == known.end()) {
-    int cus = 0;
-    if ((e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds)) != hipSuccess) return e;
-    if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
-    at = known.emplace(std::make_pair(dev, kernel), std::min((cus + 7) / 8 * 8, kTile16Units)).first;
-  }
-  *grid = at->second;
+  if (dev < kDevices && (*grid = known[dev].load(std::memory_order_relaxed)) > 0) return hipSuccess;
+  int cus = 0;
+  if ((e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds)) != hipSuccess) return e;
+  if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
+  *grid = std::min((cus + 7) / 8 * 8, kTile16Units);
+  if (dev < kDevices) known[dev].store(*grid, std::memory_order_relaxed);
   return hipSuccess;
 }
 
@@ -678,9 +674,10 @@ hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
   static_assert(S::kMT >= 64 || FORM != kWeights, "a transposed operand is 64 wide at least");
   static_assert((FORM == kForward || S::kLA * (512 / S::kNT) % 8 == 0) && (FORM != kWeights || S::kLB * (512 / S::kMT) % 8 == 0),
                 "a wave's loads of a transposed operand begin at a multiple of 8 rows");
+  static std::atomic<int> known[kDevices];
   int grid = 0;
   const auto kernel = gmm16_tile_kernel<FORM, WAVES, WC, CB, RB, BLOCKS, ONCE, DMA, ODD, T>;
-  hipError_t e = tile16_grid(reinterpret_cast<const void*>(kernel), S::kLds, &grid);
+  hipError_t e = tile16_grid(reinterpret_cast<const void*>(kernel), S::kLds, known, &grid);
   if (e != hipSuccess) return e;
   grid *= BLOCKS;
   kernel<<<grid, 64 * WAVES, S::kLds, stream>>>(a);

@@ -1,6 +1,7 @@
 """Host-side refusals of the norm and of the 16-bit products: wrong arguments return an error with a
 message before any launch, so these run without a GPU."""
 import ctypes
+import time
 import os
 
 import pytest
@@ -110,6 +111,30 @@ def test_workspaces(lib):
     assert lib.moe_grouped_matmul_workspace_size(1, 1, 4, 4, 2, ctypes.byref(b)) == 1
     assert lib.moe_grouped_matmul_workspace_size(1, 1, 4, 4, 0, None) == 1
     assert lib.moe_grouped_matmul_wgrad_workspace_size(1, 1, 4, 4, None) == 1
+
+
+def test_an_output_that_overlaps_an_operand_is_refused(lib):
+    """Small and large forms, the output at, in front of and behind an operand's first byte."""
+    for rows, n, k in ((4, 64, 256), (640, 64, 256)):
+        apart = dict(x=FAKE << 20, w=FAKE << 21, out=FAKE << 22)
+        for at in (apart["x"], apart["x"] + 2 * rows * k - 2, apart["x"] - 2 * rows * n + 2, apart["w"], apart["w"] + 2 * 4 * n * k - 2):
+            assert product(lib, **{**apart, "rows": rows, "n": n, "k": k, "out": at}) == 1
+            assert "overlaps" in lib.moe_last_error().decode()
+        for at in (apart["x"], apart["x"] + 2 * rows * n - 2, apart["w"], apart["w"] - 2 * 4 * n * k + 2):
+            assert wgrad(lib, **{**apart, "rows": rows, "n": n, "k": k, "out": at}) == 1
+            assert "overlaps" in lib.moe_last_error().decode()
+
+
+def test_planning_takes_no_time(lib):
+    """The choice of a tile is not slower for more rows: the most rows, and every number of groups up to 8."""
+    b, took = ctypes.c_size_t(), []
+    for _ in range(3):
+        t = time.perf_counter()
+        for groups in range(1, 9):
+            for trans in (0, 1):
+                assert lib.moe_grouped_matmul_workspace_size((1 << 24) - 2, groups, 4096, 7168, trans, ctypes.byref(b)) == 0
+        took.append(time.perf_counter() - t)
+    assert min(took) < 0.02   # (a sum over all tiles would take 0.3 s)
 
 
 def test_nothing_to_do_launches_nothing(lib):
