@@ -510,10 +510,11 @@ moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales,
 /*   grad_weight = sum over the rows of grad_y xh, in fp32, in a fixed order                         */
 /*   grad_y, h, grad_h, grad_x  device, [rows, cols] of dtype; grad_h, the gradient of h from          */
 /*                elsewhere (the residual stream), may be NULL. grad_x is the gradient of x and of      */
-/*                the residual alike. It may be the same buffer as grad_y or grad_h.                     */
+/*                the residual alike.                                                                    */
 /*   grad_weight  device, fp32 [cols]; zeros for rows = 0                                                 */
 /* Limits: rows in [0, MOE_MAX_FLAT_ROWS), cols in [1, MOE_NORM_MAX_COLS]; codes 8-byte aligned, the other   */
-/* tensors as their elements.                                                                               */
+/* tensors as their elements. An output may be exactly an input's buffer (y or h: x or residual; grad_x:      */
+/* grad_y, h or grad_h), else apart from all inputs.                                                         */
 /* ------------------------------------------------------------------------ */
 #define MOE_NORM_MAX_COLS 16384
 moe_status moe_rms_norm(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const void* weight,
@@ -541,8 +542,11 @@ moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* 
 /*                off[num_groups]) take no part and their out rows are left as they were.               */
 /*                NULL: all rows are one group (num_groups must be 1).                                   */
 /* Limits: n and k in [1, 1048576]; num_groups in [1, 1024]; rows in [0, MOE_MAX_FLAT_ROWS). Any          */
-/* sizes and element-aligned addresses are taken; n and k that are multiples of 8 and 16-byte              */
-/* aligned tensors are much faster. out must not overlap an operand.                                        */
+/* sizes and element-aligned addresses are taken. Up to 16 rows forward (32, of few weights) need no       */
+/* workspace. Beyond that an n or k along which an operand's rows lie that is no multiple of 8 costs a      */
+/* copy of that operand in the workspace, and operands that are not 16-byte aligned a kernel that is        */
+/* many times slower. An out that overlaps an operand: MOE_ERR_INVALID_ARG. The results do not depend on      */
+/* the workspace's contents and are the same bits in every call.                                             */
 /* ------------------------------------------------------------------------ */
 moe_status moe_grouped_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int transpose_w,
                                              size_t* bytes /* host out */);

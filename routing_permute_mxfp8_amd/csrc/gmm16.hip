@@ -5,10 +5,15 @@
 // Products of 16-bit values are exact in fp32; they are added in fp32 by the MFMAs and rounded to
 // the output's type once.
 //
-// The kernel of this file takes every shape: operands are read by elements, whatever their
-// strides, and staged in LDS with the contraction innermost, as V_MFMA_F32_16X16X32 takes them:
-// lane l holds elements 8 (l / 16) .. + 7 of row l % 16. A block of four waves makes a tile of 64 x 64
-// outputs, 32 x 32 a wave.
+// Three kernels: gmm16_few.hip for forward products of few rows, whose operands go straight to
+// registers; gmm16_tile.h for the rest, whose operands are staged in LDS; and the one of this file for
+// operands that do not start at a multiple of 16 bytes (views into other tensors), of any strides.
+// This file chooses among them and the tile, and copies rows of odd lengths to padded ones.
+//
+// The kernel of this file stages operands by elements, with the contraction innermost, as
+// V_MFMA_F32_16X16X32 takes them: lane l holds elements 8 (l / 16) .. + 7 of row l % 16. A block of
+// four waves makes a tile of 64 x 64 outputs, 32 x 32 a wave. It is bound by the staging's 2-byte
+// loads (32768 rows on 16 groups of 4096 x 7168: 54 ms, where the staged tiles take 1.6).
 
 #include <algorithm>
 #include <cmath>
@@ -205,8 +210,9 @@ double estimate(const Gmm16Params& p, const Shape16& s) {
 
 // The tile with the least estimate. Groups of about 256 rows, e.g., take two tiles of 160 rows rather
 // than one and often a second of 256 (8192 rows on 32 groups of 4096 x 7168, forward and transposed:
-// 577 and 618 us, with 192 rows 605 and 662, with 256 591 and 657, with 128 718 and 760). Limits: where rows outside the groups or a few large groups make the mean a poor
-// guide, the tile is larger or smaller than it should be.
+// 577 and 618 us, with 192 rows 605 and 662, with 256 591 and 657, with 128 718 and 760). Limits:
+// where rows outside the groups or a few large groups make the mean a poor guide, the tile is larger
+// or smaller than it should be.
 int tile_rows(const Gmm16Params& p) {
   int best = 0;
   double least = 0;

@@ -1,7 +1,7 @@
 // 16-bit grouped products with both operands staged in LDS (the kernel of the three files
 // gmm16_forward.hip, gmm16_transposed.hip and gmm16_weights.hip).
 //
-// A work item is a tile of MT output rows by NT output channels, computed by four or eight waves, each
+// A work item is a tile of MT output rows by NT output channels, computed by four waves, each
 // holding CB x RB accumulators of 16 channels x 16 rows (V_MFMA_F32_16X16X32: lane l holds 8
 // contraction elements, 8 (l / 16) on, of row l % 16 of an operand; weights in the A slot, so that
 // a lane holds 4 neighbouring channels of one row). Blocks are persistent and XCD-aware.
@@ -21,6 +21,22 @@
 // 16 channels, lane j gets the 4 contraction elements of channel j). 32 lanes a clock are served,
 // rows 0 - 3 and 8 - 11 of 32 bytes each: 64-byte blocks of row r are exchanged by r % 4, their halves
 // by r / 8 % 2, so that these lie in different banks.
+//
+// What bounds it: large products the card's power, at which it runs its clock down (1.66 GHz with
+// the MFMAs at work 70 % of the cycles, forward, 32768 rows on 16 groups of 4096 x 7168: 1.56 ms, 1.23
+// PFLOP/s; the MFMAs alone, of random operands in registers, 2.06), then the items' ends: an item's
+// stores and the next one's zeros take 5 us beside 1.8 a step, which a contraction of a few steps
+// shows (gradient by the weights, 256 rows a group: 4 - 6 steps, 14.6 us an item). Products of few
+// rows the weights' stream (256 rows on 64 groups: 3.76 GB in 0.54 ms, 7.0 TB/s). Why tiles of up to
+// 256 x 256 and one block a unit: a step of it reads each operand for 256 of the other, and the L1
+// is then busy half of a step's time; tiles of 128 x 256 take 1.08 us a step, 1.2 times as long for
+// the same work.
+//
+// Measured along the way, 32768 rows as above (forward / transposed) and the weights' gradient of 16
+// groups, 7168 x 2048 (ms): LDS-staged 32 x 32 MFMAs, direct-to-LDS loads 1.83 / 2.00 / 1.75; loads
+// through registers, spread over a slot's time 1.73 / 1.88 / 0.89; 16 x 16 x 32 MFMAs in place 1.73 /
+// 1.73 / 0.86; each load and write to LDS between MFMAs of their own 1.66 / 1.66 / 0.80; now 1.56 / 1.62 /
+// 0.78.
 #pragma once
 
 #include <algorithm>
@@ -80,14 +96,14 @@ __device__ __forceinline__ void slot_barrier() {
 // takes moves on by one with each group), dealt to its blocks in turn. What is left for a last,
 // part-filled round is shared: the contraction of each of these items is cut into `parts`, one for
 // each block; the blocks leave fp32 tiles, which gmm16_join_kernel adds in order.
-__device__ __forceinline__ int eighth(int each, int i) { return (int)((int64_t)each * i / 8); }
+__host__ __device__ __forceinline__ int eighth(int each, int i) { return (int)((int64_t)each * i / 8); }
 struct Share {
   int64_t begin;          // the XCD's first item (not kWeights)
   int full, rem, parts;   // whole rounds, items behind them, blocks an item of those
 };
 // each: items of a group (kWeights). steps: those of the longest item.
 template <int FORM>
-__device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int each, int steps, int xcd, int per) {
+__host__ __device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int each, int steps, int xcd, int per) {
   Share s;
   int64_t n;
   if constexpr (FORM == kWeights) {
@@ -100,7 +116,7 @@ __device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, in
   }
   s.full = (int)(n / per);
   s.rem = (int)(n - (int64_t)s.full * per);
-  s.parts = s.rem ? min(per / s.rem, steps / 4) : 1;   // (a part has four steps at least)
+  s.parts = s.rem ? (per / s.rem < steps / 4 ? per / s.rem : steps / 4) : 1;   // (a part has four steps at least)
   if (!p.part || s.parts < 2 || steps - (steps + s.parts - 1) / s.parts < p.gain) s.parts = 1;
   return s;
 }
@@ -668,7 +684,7 @@ inline hipError_t tile16_grid(const void* kernel, int lds, std::atomic<int> (&kn
 }
 
 template <int FORM, int WAVES, int WC, int CB, int RB, int BLOCKS, bool ONCE, bool DMA, bool ODD, typename T>
-hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
+hipError_t launch_tile16(Tile16Args a, hipStream_t stream) {
   using S = Tile16<WAVES, WC, CB, RB>;
   static_assert(S::kLds * BLOCKS <= 160 * 1024, "LDS of a compute unit");
   static_assert(S::kMT >= 64 || FORM != kWeights, "a transposed operand is 64 wide at least");
@@ -680,6 +696,16 @@ hipError_t launch_tile16(const Tile16Args& a, hipStream_t stream) {
   hipError_t e = tile16_grid(reinterpret_cast<const void*>(kernel), S::kLds, known, &grid);
   if (e != hipSuccess) return e;
   grid *= BLOCKS;
+  // Where the number of items does not depend on the groups' sizes it is known here whether any can be
+  // shared; if not, the join's launch is saved (5 us).
+  if (a.part && (FORM == kWeights || !a.off)) {
+    const int ncb = (a.nc + S::kNT - 1) / S::kNT, nrt = (a.nr + S::kMT - 1) / S::kMT;
+    const int tiles = FORM == kWeights ? a.groups * nrt : (a.rows + S::kMT - 1) / S::kMT;
+    const int steps = FORM == kWeights ? (a.rows + kCon - 1) / kCon : a.steps;   // (kWeights: at most)
+    bool any = false;
+    for (int xcd = 0; xcd < 8; ++xcd) any |= share_of<FORM>(a, (int64_t)tiles * ncb, nrt * ncb, steps, xcd, grid / 8).parts > 1;
+    if (!any) a.part = nullptr;
+  }
   kernel<<<grid, 64 * WAVES, S::kLds, stream>>>(a);
   if ((e = hipGetLastError()) != hipSuccess || !a.part) return e;
   gmm16_join_kernel<FORM, WAVES, WC, CB, RB, ODD, T><<<dim3(grid / 2, RB), 64 * WAVES, 0, stream>>>(a, grid);

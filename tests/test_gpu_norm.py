@@ -305,3 +305,25 @@ def test_large(rows, cols, dtype):
         want_w += terms.sum(0)
         mag += terms.abs().sum(0)
     assert bool(((gw.double() - want_w).abs() <= (rows / 256 + 54) * U * mag).all())
+
+
+@pytest.mark.parametrize("rows,cols", [(2600, 1000), (2600, 100), (700, 7168), (700, 8200), (40, 1001)])
+def test_in_place(rows, cols):
+    """The C calls with an output in an input's place, as the documentation allows, with more rows than blocks."""
+    lib, stream = rp.load(), torch.cuda.current_stream().cuda_stream
+    for dtype, code in [(torch.bfloat16, 2), (torch.float32, 0)]:
+        x, r = on(rows_of(rows, cols, dtype)), on(rows_of(rows, cols, dtype, 2))
+        w = on(weight_of(cols, dtype))
+        y, h, rstd, _, _ = rp.rms_norm(x, w, r)
+        for y_at in range(2):
+            a, b, got = x.clone(), r.clone(), torch.empty_like(rstd)
+            yp, hp = ((a, b), (b, a))[y_at]
+            assert lib.moe_rms_norm(a.data_ptr(), b.data_ptr(), code, rows, cols, w.data_ptr(), code, EPS, -1, yp.data_ptr(),
+                                    hp.data_ptr(), got.data_ptr(), None, None, stream) == 0
+            assert torch.equal(yp, y) and torch.equal(hp, h) and torch.equal(got, rstd)
+        want = rp.rms_norm_backward(y, h, w, rstd, grad_h=r)
+        ws = torch.empty(1 << 25, dtype=torch.uint8, device=DEV)
+        a, gw = h.clone(), torch.empty(cols, device=DEV)
+        assert lib.moe_rms_norm_backward(y.data_ptr(), a.data_ptr(), r.data_ptr(), code, rows, cols, w.data_ptr(), code,
+                                         rstd.data_ptr(), a.data_ptr(), gw.data_ptr(), ws.data_ptr(), ws.numel(), stream) == 0
+        assert torch.equal(a, want[0]) and torch.equal(gw, want[1])
