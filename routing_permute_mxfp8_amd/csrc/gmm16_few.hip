@@ -2,7 +2,7 @@
 // without a workspace.
 //
 // It is bound by the weights' way from memory, and small products by a launch and two trips there. A
-// block makes the outputs of 8 channels for all rows of one group. Its 8 waves take the
+// block makes the outputs of 8 channels for up to 32 rows of one group. Its 8 waves take the
 // contraction's steps of 64 in equal runs, with several steps' loads in flight, straight from memory
 // to the registers of V_MFMA_F32_16X16X32, and add their sums in LDS, always in the same order. Two
 // neighbouring rows of an operand of the MFMA are the halves of a step of one channel (or of one
@@ -26,6 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 8, kEach = 8, kStep = 64;   // waves, channels and rows of an operand, elements of a step
+constexpr int kRows = 32;                          // rows of a block, at most
 
 // The group that row r is in: the number of groups that end at or before it (all 64 lanes alike).
 __device__ __forceinline__ int group_of_row(const int32_t* off, int groups, int r) {
@@ -35,16 +36,21 @@ __device__ __forceinline__ int group_of_row(const int32_t* off, int groups, int 
   return n;
 }
 
-// RB: blocks of 8 rows that a group can have. VEC: every row is of whole 16-byte vectors.
+// RB: blocks of 8 rows that a block of threads takes. VEC: every row is of whole 16-byte vectors.
 template <typename T, typename O, int RB, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void gmm16_few_kernel(Gmm16Params p) {
   constexpr int U = RB == 4 ? 4 : 8;   // steps loaded at a time
   __shared__ v4f sums[RB * kWaves * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = (lane & 15) >> 1, q = lane >> 4, at = 32 * (lane & 1) + 8 * q, n0 = blockIdx.x * kEach;
-  // block (c, r): the group whose first row is r, if there is one
+  // one group: block (c, 0, z) takes rows 8 RB z on; groups: block (c, r) those of the group whose
+  // first row is r, if there is one
   int g = 0, lo = 0, hi = (int)p.rows;
-  if (p.off) {
+  if (p.groups == 1) {
+    if (p.off) group_rows(p.off, 0, (int)p.rows, &lo, &hi);
+    lo += 8 * RB * blockIdx.z;
+    hi = min(hi, lo + 8 * RB);
+  } else {
     g = group_of_row(p.off, p.groups, blockIdx.y);
     if (g >= p.groups) return;
     group_rows(p.off, g, (int)p.rows, &lo, &hi);
@@ -92,7 +98,7 @@ __global__ __launch_bounds__(64 * kWaves) void gmm16_few_kernel(Gmm16Params p) {
 
 template <typename T, typename O, bool VEC>
 hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
-  const dim3 grid((p.n + kEach - 1) / kEach, p.off ? (unsigned)p.rows : 1);
+  const dim3 grid((p.n + kEach - 1) / kEach, p.groups > 1 ? (unsigned)p.rows : 1, p.groups > 1 ? 1 : (unsigned)(p.rows + kRows - 1) / kRows);
   if (p.rows <= 8) gmm16_few_kernel<T, O, 1, VEC><<<grid, 64 * kWaves, 0, stream>>>(p);
   else if (p.rows <= 16) gmm16_few_kernel<T, O, 2, VEC><<<grid, 64 * kWaves, 0, stream>>>(p);
   else gmm16_few_kernel<T, O, 4, VEC><<<grid, 64 * kWaves, 0, stream>>>(p);
@@ -107,13 +113,19 @@ hipError_t launch(const Gmm16Params& p, hipStream_t stream) {
 
 }  // namespace
 
-// The kernel of this file takes forward products of up to 32 rows. Above 16 it reads its rows for
-// every 8 channels more often than the tiles do, which shows once the weights are many (7168 deep,
-// one group, 32 rows: 256 channels 10.5 us and 14.6 with tiles, 4096 19.5 and 22.3, 8192 34.7 and
-// 29.4; 8 groups of 4096, 32 rows: 101 and 80; 16 rows: 65 and 64, 8 rows: 58 and 63).
+// The kernel of this file takes forward products of up to 16 rows, and of more where its blocks are
+// few: beyond a block for each of the card's 256 units and a second one, reading the rows again for
+// every 8 channels costs more than the tiles' slower start. 7168 deep, one group, tiles and this
+// kernel: 256 channels, 64 rows 14.7 and 10.8 us, 256 rows 16.2 and 11.8, 512 (512 blocks) 24.1 and
+// 19.4; 2048 channels, 32 rows 17.1 and 11.9, 64 (512) 22.9 and 19.6, 96 (768) 21.8 and 26.9; 384
+// channels, 512 rows (768) 24.8 and 26.9. Groups have blocks for each of their first rows only, all
+// rows of a group in one: up to 32 rows of few weights (8 groups of 4096, 32 rows: 80 and 101; 16
+// rows: 64 and 65, 8 rows: 63 and 58).
 bool gmm16_is_few(const Gmm16Params& p) {
   if (p.wgrad || p.trans) return false;
-  return p.rows <= 16 || (p.rows <= 32 && std::min<int64_t>(p.rows, p.groups) * p.n * p.k <= 1 << 25);
+  if (p.rows <= 16) return true;
+  if (p.groups > 1) return p.rows <= kRows && std::min<int64_t>(p.rows, p.groups) * p.n * p.k <= 1 << 25;
+  return ((p.n + kEach - 1) / kEach) * ((p.rows + kRows - 1) / kRows) <= 512;
 }
 
 hipError_t launch_gmm16_few(const Gmm16Params& p, hipStream_t stream) {

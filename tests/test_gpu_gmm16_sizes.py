@@ -21,6 +21,29 @@ def test_few_rows(rows, n, k):
     product("forward", rows, 1, n, k, None, (kind + 1) % len(KINDS), seed=rows, off=1)   # no vectors
 
 
+@pytest.mark.parametrize("rows", [33, 64, 65, 100, 256, 500, 16384, 16385])
+@pytest.mark.parametrize("n,k", [(8, 64), (7, 513), (250, 1000)])
+def test_rows_in_several_blocks(rows, n, k):
+    """One group of few channels: row blocks of 32, with and without offsets that leave rows outside."""
+    if rows > 500 and n > 8:
+        return
+    kind = rows % len(KINDS)
+    product("forward", rows, 1, n, k, None, kind, seed=rows)
+    product("forward", rows, 1, n, k, [0, rows], kind, seed=rows)
+    product("forward", rows, 1, n, k, [5, rows - 6], kind, seed=rows, off=1)
+
+
+def test_one_group_needs_one_workspace():
+    """The workspace that is asked for without offsets is the one a call of one group with offsets takes."""
+    for rows, n, k in ((64, 256, 7168), (600, 256, 7168), (600, 256, 7169), (40, 4096, 512)):
+        x, w = on(values((rows, k), BF, 0)), on(values((1, n, k), BF, 1))
+        o = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+        need = rp._sized("moe_grouped_matmul_workspace_size", rows, 1, n, k, 0)
+        ws = torch.full((max(need, 256),), 255, dtype=torch.uint8, device=DEV)
+        say(f"one group {rows} {n} {k}: {need} bytes")
+        assert torch.equal(rp.grouped_matmul(x, w, o, workspace=ws), rp.grouped_matmul(x, w, workspace=ws))
+
+
 FEW = {
     "one each": [0, 1, 2, 3, 4, 5, 6, 7, 8],
     "gaps": [0, 0, 0, 3, 3, 4, 4, 13, 13],
