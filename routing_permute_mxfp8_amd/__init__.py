@@ -766,11 +766,11 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant_mode: int = Q
     with _on(index):
         y = torch.empty_like(x) if want_y else None
         h = x if residual is None else torch.empty_like(x)
-        rstd = torch.empty((n,), dtype=torch.float32, device=dev)
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
         codes = scales = None
         if quant:
-            codes = torch.empty((n, c // 2 if quant_mode == QUANT_MXFP4 else c), dtype=torch.uint8, device=dev)
-            scales = torch.empty((n, (c + 63) // 64 * 2), dtype=torch.uint8, device=dev)
+            codes = torch.empty(n, c // 2 if quant_mode == QUANT_MXFP4 else c, dtype=torch.uint8, device=dev)
+            scales = torch.empty(n, (c + 63) // 64 * 2, dtype=torch.uint8, device=dev)
         _check(lib.moe_rms_norm(x.data_ptr(), _raw(residual), _DT[x.dtype], n, c, weight.data_ptr(), _DT[weight.dtype],
                                 eps, quant_mode, _raw(y), h.data_ptr(), rstd.data_ptr(), _raw(codes), _raw(scales),
                                 _raw_stream(index)))
@@ -789,7 +789,7 @@ def rms_norm_backward(grad_y, h, weight, rstd, *, grad_h=None):
     nbytes = _sized("moe_rms_norm_backward_workspace_size", n, c)
     with _on(index):
         grad_x = torch.empty_like(h)
-        grad_weight = torch.empty((c,), dtype=torch.float32, device=h.device)
+        grad_weight = torch.empty(c, dtype=torch.float32, device=h.device)
         ws = _workspace(nbytes, h.device)
         _check(lib.moe_rms_norm_backward(grad_y.data_ptr(), h.data_ptr(), _raw(grad_h), _DT[h.dtype], n, c,
                                          weight.data_ptr(), _DT[weight.dtype], rstd.data_ptr(), grad_x.data_ptr(),
@@ -852,7 +852,7 @@ def grouped_matmul(x, w, group_offsets=None, *, transpose_w: bool = False, out_d
     nbytes = _sized("moe_grouped_matmul_workspace_size", rows, g, n, k, int(bool(transpose_w)))
     with _on(index):
         if out is None:
-            out = torch.empty((rows, n), dtype=od, device=x.device)
+            out = torch.empty(rows, n, dtype=od, device=x.device)
         ws = workspace
         if nbytes and (ws is None or ws.numel() < nbytes):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
@@ -884,7 +884,7 @@ def grouped_matmul_wgrad(grad_out, x, group_offsets=None, *, out_dtype=None, out
     nbytes = _sized("moe_grouped_matmul_wgrad_workspace_size", rows, g, n, k)
     with _on(index):
         if out is None:
-            out = torch.empty(shape, dtype=od, device=x.device)
+            out = torch.empty(*shape, dtype=od, device=x.device)
         ws = workspace
         if nbytes and (ws is None or ws.numel() < nbytes):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
