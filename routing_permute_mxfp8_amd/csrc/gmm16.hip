@@ -180,7 +180,8 @@ double tiles_of(double mean, int mt, bool one) {
   const double sd = std::sqrt(mean);
   const double sure = std::floor(std::max(0.0, mean - 6 * sd) / mt);   // tiles that all groups fill
   double sum = sure > 0 ? sure : 1.0 - std::exp(-mean);                // (groups with rows at all)
-  for (double at = mt * std::max(1.0, sure); at < mean + 6 * sd; at += mt) sum += 0.5 * std::erfc((at + 0.5 - mean) / (std::sqrt(2.0) * sd));
+  for (double at = mt * std::max(1.0, sure); at < mean + 6 * sd; at += mt)
+    sum += 0.5 * std::erfc((at + 0.5 - mean) / (std::sqrt(2.0) * sd));
   return sum;
 }
 
@@ -263,7 +264,8 @@ hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {
     q.b = p.b16;
   }
   q.odd = !on16(p.out) || (p.wgrad ? p.k : p.n) % (p.out_fp32 ? 4 : 8) != 0;
-  return p.wgrad ? launch_gmm16_weights(q, stream) : p.trans ? launch_gmm16_transposed(q, stream) : launch_gmm16_forward(q, stream);
+  if (p.wgrad) return launch_gmm16_weights(q, stream);
+  return p.trans ? launch_gmm16_transposed(q, stream) : launch_gmm16_forward(q, stream);
 }
 
 }  // namespace moe

@@ -98,7 +98,8 @@ __global__ __launch_bounds__(64 * kWaves) void gmm16_few_kernel(Gmm16Params p) {
 
 template <typename T, typename O, bool VEC>
 hipError_t launch_as(const Gmm16Params& p, hipStream_t stream) {
-  const dim3 grid((p.n + kEach - 1) / kEach, p.groups > 1 ? (unsigned)p.rows : 1, p.groups > 1 ? 1 : (unsigned)(p.rows + kRows - 1) / kRows);
+  const unsigned strips = (p.n + kEach - 1) / kEach, rows = (unsigned)p.rows;
+  const dim3 grid(strips, p.groups > 1 ? rows : 1, p.groups > 1 ? 1 : (rows + kRows - 1) / kRows);
   if (p.rows <= 8) gmm16_few_kernel<T, O, 1, VEC><<<grid, 64 * kWaves, 0, stream>>>(p);
   else if (p.rows <= 16) gmm16_few_kernel<T, O, 2, VEC><<<grid, 64 * kWaves, 0, stream>>>(p);
   else gmm16_few_kernel<T, O, 4, VEC><<<grid, 64 * kWaves, 0, stream>>>(p);

@@ -103,7 +103,8 @@ struct Share {
 };
 // each: items of a group (kWeights). steps: those of the longest item.
 template <int FORM>
-__host__ __device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int each, int steps, int xcd, int per) {
+__host__ __device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t total, int each, int steps, int xcd,
+                                                   int per) {
   Share s;
   int64_t n;
   if constexpr (FORM == kWeights) {
@@ -243,7 +244,8 @@ __device__ __forceinline__ void store_rows(const Tile16Args& p, const v4f (&acc)
     for (int i = 0; i < CB; ++i) {
       const int c = c0 + 16 * i + 4 * g4, left = valid ? p.nc - c : 0;
       if (p.out_fp32) store_any((float*)p.out + row * p.nc + c, left, acc[i]);
-      else store_any((uint16_t*)p.out + row * p.nc + c, left, uint2{Mfma<T>::pair(acc[i][0], acc[i][1]), Mfma<T>::pair(acc[i][2], acc[i][3])});
+      else store_any((uint16_t*)p.out + row * p.nc + c, left,
+                     uint2{Mfma<T>::pair(acc[i][0], acc[i][1]), Mfma<T>::pair(acc[i][2], acc[i][3])});
     }
   } else if (p.out_fp32) {
     float* to = (float*)p.out + row * p.nc;
@@ -266,8 +268,9 @@ __device__ __forceinline__ void store_rows(const Tile16Args& p, const v4f (&acc)
 }
 
 // The body gets the slots (both of the channels' operand, both of the rows') and the rest of LDS as
-// restrict pointers, which is what they are: apart. A slot is never read while loads into it are in flight, and so the compiler, which
-// makes an LDS read wait for the direct-to-LDS loads that may write there, has nothing to wait for.
+// restrict pointers, which is what they are: apart. A slot is never read while loads into it are in
+// flight, and so the compiler, which makes an LDS read wait for the direct-to-LDS loads that may
+// write there, has nothing to wait for.
 template <int FORM, int WAVES, int WC, int CB, int RB, bool ONCE, bool DMA, bool ODD, typename T>
 __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __restrict__ a0, uint8_t* __restrict__ a1,
                                             uint8_t* __restrict__ b0, uint8_t* __restrict__ b1,
@@ -281,9 +284,10 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
   int* const ends = reinterpret_cast<int*>(lds + S::kEnds);
   int4* const list = reinterpret_cast<int4*>(lds + S::kItems);
 
-  const int tiles = FORM == kWeights ? p.groups * nrt : count_tiles<MT, WAVES>(p.off, p.groups, p.rows, ends, reinterpret_cast<int*>(list));
+  int* const scratch = reinterpret_cast<int*>(list);   // (until the list is filled)
+  const int tiles = FORM == kWeights ? p.groups * nrt : count_tiles<MT, WAVES>(p.off, p.groups, p.rows, ends, scratch);
   const int xcd = blockIdx.x & 7, slot_in = blockIdx.x >> 3, per = gridDim.x >> 3;
-  const Share share = share_of<FORM>(p, (int64_t)tiles * ncb, nrt * ncb, longest<FORM, WAVES>(p, reinterpret_cast<int*>(list)), xcd, per);
+  const Share share = share_of<FORM>(p, (int64_t)tiles * ncb, nrt * ncb, longest<FORM, WAVES>(p, scratch), xcd, per);
   const bool shared = share.parts > 1 && slot_in < share.rem * share.parts;   // the block's last item is a part of one
   const int count = share.full + (share.parts > 1 ? shared : slot_in < share.rem);
   if (count == 0) return;   // the whole block
@@ -292,7 +296,8 @@ __device__ __forceinline__ void tile16_body(const Tile16Args& p, uint8_t* __rest
     if (tid < kList && first + tid < count) {
       const int n = first + tid;
       const int in = n == share.full && shared ? slot_in % share.rem : slot_in;
-      list[tid] = describe16<FORM, MT>(p, ends, tiles, nrt, ncb, item_of<FORM>(share, nrt * ncb, xcd, (int64_t)n * per + in));
+      const int64_t it = item_of<FORM>(share, nrt * ncb, xcd, (int64_t)n * per + in);
+      list[tid] = describe16<FORM, MT>(p, ends, tiles, nrt, ncb, it);
     }
     __syncthreads();
   };
@@ -648,7 +653,8 @@ __global__ __launch_bounds__(64 * WAVES) void gmm16_join_kernel(Tile16Args p, in
   const int xcd = blockIdx.x & 7, r = blockIdx.x >> 3, per = blocks >> 3;
   const Share share = share_of<FORM>(p, (int64_t)tiles * ncb, nrt * ncb, longest<FORM, WAVES>(p, scratch), xcd, per);
   if (share.parts < 2 || r >= share.rem) return;
-  const Item16 it = item16<FORM>(describe16<FORM, S::kMT>(p, ends, tiles, nrt, ncb, item_of<FORM>(share, nrt * ncb, xcd, (int64_t)share.full * per + r)), ncb);
+  const int64_t n = item_of<FORM>(share, nrt * ncb, xcd, (int64_t)share.full * per + r);
+  const Item16 it = item16<FORM>(describe16<FORM, S::kMT>(p, ends, tiles, nrt, ncb, n), ncb);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = blockIdx.y;
   v4f acc[CB] = {};
   for (int part = 0; part < share.parts; ++part) {
@@ -703,7 +709,8 @@ hipError_t launch_tile16(Tile16Args a, hipStream_t stream) {
     const int tiles = FORM == kWeights ? a.groups * nrt : (a.rows + S::kMT - 1) / S::kMT;
     const int steps = FORM == kWeights ? (a.rows + kCon - 1) / kCon : a.steps;   // (kWeights: at most)
     bool any = false;
-    for (int xcd = 0; xcd < 8; ++xcd) any |= share_of<FORM>(a, (int64_t)tiles * ncb, nrt * ncb, steps, xcd, grid / 8).parts > 1;
+    for (int xcd = 0; xcd < 8; ++xcd)
+      any |= share_of<FORM>(a, (int64_t)tiles * ncb, nrt * ncb, steps, xcd, grid / 8).parts > 1;
     if (!any) a.part = nullptr;
   }
   kernel<<<grid, 64 * WAVES, S::kLds, stream>>>(a);

@@ -154,10 +154,8 @@ __device__ __forceinline__ int quantise8(const float (&y)[8], uint8_t* codes, in
 
 constexpr int rows_of(int lanes) { return lanes ? 256 / lanes : 1; }
 
-// Sum of v over a row's lanes, the same in all: LANES lanes of a block of 256 threads, or (LANES = 0)
-// the whole block, whatever its size. slot: one of two sets of 16 values of LDS, used in
-// turn by a block's rows (a wave that is behind may still read the last row's).
-template <int STEP, typename S>   // v + the v of the lane that step exchanges with this one
+// v + the v of the lane that step STEP exchanges with this one.
+template <int STEP, typename S>
 __device__ __forceinline__ S add_step(S v) {
   constexpr int kWords = sizeof(S) / 4;
   typedef uint32_t words __attribute__((ext_vector_type(2)));
@@ -179,6 +177,9 @@ __device__ __forceinline__ S add_step(S v) {
   else return __builtin_bit_cast(S, (uint32_t)a[0]) + __builtin_bit_cast(S, (uint32_t)b[0]);
 }
 
+// Sum of v over a row's lanes, the same in all: LANES lanes of a block of 256 threads, or (LANES = 0)
+// the whole block, whatever its size. slot: one of two sets of 16 values of LDS, used in turn by
+// a block's rows (a wave that is behind may still read the last row's).
 template <int LANES, typename S>
 __device__ __forceinline__ S row_sum(S v, S* slot) {
   v = add_step<8>(add_step<4>(add_step<2>(add_step<1>(v))));
