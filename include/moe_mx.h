@@ -542,11 +542,11 @@ moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* 
 /*                off[num_groups]) take no part and their out rows are left as they were.               */
 /*                NULL: all rows are one group (num_groups must be 1).                                   */
 /* Limits: n and k in [1, 1048576]; num_groups in [1, 1024]; rows in [0, MOE_MAX_FLAT_ROWS). Any          */
-/* sizes and element-aligned addresses are taken. Up to 16 rows forward, and more of few weights, need no    */
-/* workspace. Beyond that an n or k along which an operand's rows lie that is no multiple of 8 costs a      */
-/* copy of that operand in the workspace, and operands that are not 16-byte aligned a kernel that is        */
-/* many times slower. An out that overlaps an operand: MOE_ERR_INVALID_ARG. The results do not depend on      */
-/* the workspace's contents and are the same bits in every call.                                             */
+/* sizes and element-aligned addresses are taken. An n or k along which an operand's rows lie that is no   */
+/* multiple of 8 costs a copy of that operand in the workspace (not forward up to 32 rows of few            */
+/* weights); operands that are not 16-byte aligned take a kernel that is many times slower (not forward      */
+/* up to 16 rows). An out that overlaps an operand: MOE_ERR_INVALID_ARG. The results do not depend on the    */
+/* workspace's contents and are the same bits in every call.                                                */
 /* ------------------------------------------------------------------------ */
 moe_status moe_grouped_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int transpose_w,
                                              size_t* bytes /* host out */);

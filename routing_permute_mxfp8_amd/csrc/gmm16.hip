@@ -189,23 +189,33 @@ double tiles_of(double mean, int mt, bool one) {
 // of 256 x 256, 64 MB written and read, some 30 us in all.
 constexpr int kGain = 16;
 
+// Items of a call with tiles of shape s, and steps of one, as expected.
+struct Load16 {
+  double items, steps;
+};
+Load16 load_of(const Gmm16Params& p, const Shape16& s) {
+  const double mean = (double)p.rows / p.groups;
+  const double columns = std::ceil((double)(p.wgrad ? p.k : p.n) / s.nt);
+  const double rows = p.wgrad ? p.groups * std::ceil((double)p.n / s.mt) : p.groups * tiles_of(mean, s.mt, p.groups == 1);
+  return {rows * columns, std::max(1.0, std::ceil((p.wgrad ? mean : (double)p.k) / 64))};
+}
+
+// Blocks that share an item of the last, part-filled round of `rem` items: 1 where that saves too little.
+double parts_of(double rem, double steps, double units) {
+  const double parts = rem > 0 ? std::min(std::floor(units / rem), std::floor(steps / 4)) : 1;
+  return parts >= 2 && steps - std::ceil(steps / parts) >= kGain ? parts : 1;
+}
+
 // Microseconds of a call with tiles of shape s, but for the memory traffic, which they share.
 double estimate(const Gmm16Params& p, const Shape16& s) {
-  const double mean = (double)p.rows / p.groups;
-  const double steps = std::max(1.0, std::ceil((p.wgrad ? mean : (double)p.k) / 64));
-  const double columns = std::ceil((double)(p.wgrad ? p.k : p.n) / s.nt);
-  const double items = p.groups * columns * (p.wgrad ? std::ceil((double)p.n / s.mt) : tiles_of(mean, s.mt, p.groups == 1));
+  const auto [items, steps] = load_of(p, s);
   const double units = (double)kTile16Units * s.blocks;
-  const double full = std::floor(items / units), rem = items - full * units;
+  const double full = std::floor(items / units), rem = items - full * units, parts = parts_of(rem, steps, units);
   double t = full * (steps * s.step + s.item);
-  if (rem > 0) {
-    const double parts = std::min(std::floor(units / rem), std::floor(steps / 4));
-    const double one = steps * s.step * (rem <= kTile16Units ? 0.5 + 0.5 / s.blocks : 1.0);   // fewer blocks a unit
-    if (parts >= 2 && steps - std::ceil(steps / parts) >= kGain)
-      t += std::ceil(steps / parts) * s.step + s.item + 6 + rem * parts * s.mt * s.nt * 8 / 5e6;
-    else
-      t += one + s.item;
-  }
+  if (parts >= 2)
+    t += std::ceil(steps / parts) * s.step + s.item + 6 + rem * parts * s.mt * s.nt * 8 / 5e6;
+  else if (rem > 0)
+    t += steps * s.step * (rem <= kTile16Units ? 0.5 + 0.5 / s.blocks : 1.0) + s.item;   // (fewer blocks a unit)
   return t;
 }
 
@@ -241,17 +251,27 @@ void gmm16_plan(Gmm16Params& p) {
   p.copy_a = p.pitch_a != cols_a ? (size_t)p.rows * p.pitch_a : 0;
   p.copy_b = p.pitch_b != cols_b ? (size_t)rows_b * p.pitch_b : 0;
   p.gain = kGain;
-  const int64_t steps = ((p.wgrad ? p.rows : (int64_t)p.k) + 63) / 64;   // (wgrad: one group may have all rows)
-  for (const Shape16& s : kShapes)
-    if (s.mt == p.mt) p.part_floats = steps - (steps + 1) / 2 >= p.gain ? (size_t)kTile16Units * s.blocks * s.mt * s.nt : 0;
+  // Parts of shared items, where some are expected: the join is a launch, needed or not (24 steps, 64
+  // to 365 items: 15 us shared and 23 not, 20 not shared and 23 with a join for nothing). A group
+  // that is longer than the mean may want parts in the gradient by weights (launch_tile16 knows the
+  // number of items there).
+  for (const Shape16& s : kShapes) {
+    if (s.mt != p.mt) continue;
+    const double units = (double)kTile16Units * s.blocks;
+    const auto [items, steps] = load_of(p, s);
+    const bool share = p.wgrad ? (p.rows + 63) / 64 - 4 >= kGain : parts_of(items - std::floor(items / units) * units, steps, units) >= 2;
+    p.part_floats = share ? (size_t)units * s.mt * s.nt : 0;
+  }
 }
 
 hipError_t launch_gmm16(const Gmm16Params& p, hipStream_t stream) {
   if (p.rows <= 0 && !p.wgrad) return hipSuccess;
   if (p.few) return launch_gmm16_few(p, stream);
   const auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  if (!((p.copy_a || on16(p.a)) && (p.copy_b || on16(p.b))))
+  if (!((p.copy_a || on16(p.a)) && (p.copy_b || on16(p.b)))) {
+    if (!p.wgrad && !p.trans && p.rows <= 16) return launch_gmm16_few(p, stream);   // (at any element as well)
     return p.half ? launch_as<_Float16>(p, stream) : launch_as<__bf16>(p, stream);
+  }
   Gmm16Params q = p;
   hipError_t e;
   if (p.copy_a) {

@@ -114,19 +114,30 @@ hipError_t launch(const Gmm16Params& p, hipStream_t stream) {
 
 }  // namespace
 
-// The kernel of this file takes forward products of up to 16 rows, and of more where its blocks are
-// few: beyond a block for each of the card's 256 units and a second one, reading the rows again for
-// every 8 channels costs more than the tiles' slower start. 7168 deep, one group, tiles and this
-// kernel: 256 channels, 64 rows 14.7 and 10.8 us, 256 rows 16.2 and 11.8, 512 (512 blocks) 24.1 and
-// 19.4; 2048 channels, 32 rows 17.1 and 11.9, 64 (512) 22.9 and 19.6, 96 (768) 21.8 and 26.9; 384
-// channels, 512 rows (768) 24.8 and 26.9. Groups have blocks for each of their first rows only, all
-// rows of a group in one: up to 32 rows of few weights (8 groups of 4096, 32 rows: 80 and 101; 16
-// rows: 64 and 65, 8 rows: 63 and 58).
+// The kernel of this file takes forward products whose blocks are few: a block takes 2 ns of the
+// card's time (3.5 ns for more than 8 rows) even where it has little to read, and where it has much
+// it reads the rows again for every 8 channels. Tiles and this kernel (us):
+//   7168 deep, one group: 256 channels, 64 rows 14.7 and 10.8, 256 rows (256 blocks) 16.2 and 11.8,
+//   512 (512 blocks) 24.1 and 19.4; 2048 channels, 64 rows (512) 22.9 and 19.6, 96 (768) 21.8 and
+//   26.9; 8 groups of 4096, 16 rows 64 and 65, 32 rows 80 and 101;
+//   8 rows, one group of 4096 channels (512 blocks), 64 deep 5.3 and 3.4; 32768 (4096), 64 deep 5.4 and
+//   10.3, 288: 8.7 and 11.4, 1024: 19.9 and 13.7; 50 groups of 4400 (4400), 288 deep 11.5 and 13.3,
+//   576: 15.7 and 15.9, 1024: 23.3 and 17.3;
+//   16 rows on 50 groups of 512 (1024), 64 deep 5.8 and 5.7, 1024: 16.0 and 7.2; of 4400 (8800), 1024
+//   deep 36 and 40, 2048: 71 and 52;
+//   32 rows on 50 groups of 512 (2048), 288 deep 7.7 and 9.1, 576: 12.0 and 10.3; on 4 of 4400 (17600),
+//   1024 deep 17.5 and 25.1.
+// Rows of x that are no whole 16-byte vectors would have the tiles wait for a copy of the weights (32
+// rows on 5 groups of 1000, 1001 deep: 27 and 12 us).
 bool gmm16_is_few(const Gmm16Params& p) {
   if (p.wgrad || p.trans) return false;
-  if (p.rows <= 16) return true;
-  if (p.groups > 1) return p.rows <= kRows && std::min<int64_t>(p.rows, p.groups) * p.n * p.k <= 1 << 25;
-  return ((p.n + kEach - 1) / kEach) * ((p.rows + kRows - 1) / kRows) <= 512;
+  const int64_t strips = (p.n + kEach - 1) / kEach;
+  const int64_t blocks = strips * (p.groups > 1 ? p.rows : (p.rows + kRows - 1) / kRows);
+  if (p.k % 8 != 0 && p.rows <= kRows && std::min<int64_t>(p.rows, p.groups) * p.n * p.k <= 1 << 25) return true;
+  if (p.rows <= 8) return blocks <= 1024 || p.k >= 512;
+  if (p.rows <= 16) return blocks <= 1024 || p.k >= 2048;
+  if (p.groups == 1) return blocks <= 512;
+  return p.rows <= kRows && (blocks <= 1024 || (p.k >= 512 && blocks <= 2048));
 }
 
 hipError_t launch_gmm16_few(const Gmm16Params& p, hipStream_t stream) {

@@ -44,6 +44,11 @@ def test_one_group_needs_one_workspace():
         assert torch.equal(rp.grouped_matmul(x, w, o, workspace=ws), rp.grouped_matmul(x, w, workspace=ws))
 
 
+def ragged(rows, groups, seed):
+    rng = np.random.default_rng(seed)
+    return [0, *np.sort(rng.integers(0, rows + 1, groups - 1)).tolist(), rows]
+
+
 FEW = {
     "one each": [0, 1, 2, 3, 4, 5, 6, 7, 8],
     "gaps": [0, 0, 0, 3, 3, 4, 4, 13, 13],
@@ -62,6 +67,16 @@ def test_few_rows_of_groups(name, n, k):
     for kind in range(4):
         product("forward", rows, 8, n, k, off, kind, seed=kind)
     product("forward", rows, 8, n, k, off, 0, off=5)
+
+
+@pytest.mark.parametrize("rows,groups,n,k", [(8, 1, 16400, 64), (8, 12, 1200, 504), (12, 12, 1200, 2040), (16, 12, 1200, 2056),
+                                             (16, 3, 1203, 72), (30, 30, 300, 504), (32, 30, 520, 520), (32, 1, 4200, 72)])
+def test_few_rows_of_many_channels(rows, groups, n, k):
+    """Around the sizes where tiles take over from the kernel of few rows, aligned and not."""
+    off = None if groups == 1 else ragged(rows, groups, n)
+    for kind in (0, 1):
+        product("forward", rows, groups, n, k, off, kind)
+    product("forward", rows, groups, n, k, off, 2, off=3)
 
 
 def test_few_rows_of_many_groups():
@@ -88,11 +103,6 @@ def test_few_rows_bad_offsets_and_bad_neighbours():
     assert torch.equal(got[:4], clean[:4]) and bool(got[4:7].isnan().all())
     keep = torch.arange(20) != 7
     assert torch.equal(got[7:, keep], clean[7:, keep]) and bool(got[7:, 7].isnan().all())
-
-
-def ragged(rows, groups, seed):
-    rng = np.random.default_rng(seed)
-    return [0, *np.sort(rng.integers(0, rows + 1, groups - 1)).tolist(), rows]
 
 
 @pytest.mark.parametrize("form", ["forward", "transposed"])
