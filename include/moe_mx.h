@@ -558,6 +558,13 @@ moe_status moe_grouped_matmul_wgrad_workspace_size(int64_t rows, int64_t num_gro
 moe_status moe_grouped_matmul_wgrad(const void* grad_out, const void* x, int dtype, int64_t rows,
                                     const int32_t* group_offsets, int64_t num_groups, int64_t n, int64_t k, void* out,
                                     int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* moe_grouped_matmul_plan: how a call of these sizes is computed, for tests and profiles (no launch). */
+/*   form         0 forward, 1 with transpose_w, 2 the gradient by w (rows, n, k as in those calls)       */
+/*   tile_rows    host out: output rows of a tile; 0: the kernel of few rows, which has none              */
+/*   shared       host out: 1 where blocks may share a tile's contraction and join their sums, else 0     */
+/* Operands that need 16-byte alignment and do not have it take the kernel without tiles all the same.    */
+moe_status moe_grouped_matmul_plan(int form, int64_t rows, int64_t num_groups, int64_t n, int64_t k,
+                                   int* tile_rows /* host out */, int* shared /* host out */);
 
 /* ------------------------------------------------------------------------ */
 /* Measured peaks for the roofline report (one launch each; the caller times   */

@@ -120,6 +120,7 @@ _SIGS = {
     "moe_grouped_matmul": ([_VP, _INT, _I64, _VP, _I64, _VP, _INT, _I64, _I64, _VP, _INT, _VP, _SZ, _VP], _INT),
     "moe_grouped_matmul_wgrad_workspace_size": ([_I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
     "moe_grouped_matmul_wgrad": ([_VP, _VP, _INT, _I64, _VP, _I64, _I64, _I64, _VP, _INT, _VP, _SZ, _VP], _INT),
+    "moe_grouped_matmul_plan": ([_INT, _I64, _I64, _I64, _I64, ctypes.POINTER(_INT), ctypes.POINTER(_INT)], _INT),
     "moe_probe_stream": ([_INT, _VP, _VP, _I64, _VP], _INT),
     "moe_probe_mfma": ([_INT, _VP, ctypes.POINTER(_I64), ctypes.POINTER(ctypes.c_double), _VP], _INT),
 }

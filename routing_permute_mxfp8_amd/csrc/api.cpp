@@ -1301,6 +1301,19 @@ moe_status moe_grouped_matmul_wgrad(const void* grad_out, const void* x, int dty
   return run_gmm16("moe_grouped_matmul_wgrad", p, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
+moe_status moe_grouped_matmul_plan(int form, int64_t rows, int64_t num_groups, int64_t n, int64_t k, int* tile_rows,
+                                   int* shared) {
+  if (!tile_rows || !shared) return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul_plan: tile_rows and shared must be non-NULL");
+  if (form < 0 || form > 2) return fail(MOE_ERR_INVALID_ARG, "moe_grouped_matmul_plan: form %d not 0, 1 or 2", form);
+  if (moe_status s = check_gmm16("moe_grouped_matmul_plan", MOE_DTYPE_BF16, MOE_DTYPE_BF16, rows, num_groups, n, k)) return s;
+  moe::Gmm16Params p = gmm16_params(MOE_DTYPE_BF16, MOE_DTYPE_BF16, rows, nullptr, num_groups, n, k);
+  p.trans = form == 1; p.wgrad = form == 2;
+  moe::gmm16_plan(p);
+  *tile_rows = p.few ? 0 : p.mt;
+  *shared = p.part_floats > 0;
+  return ok();
+}
+
 moe_status moe_probe_stream(int mode, const void* src, void* dst, int64_t bytes, void* stream) {
   if (mode < 0 || mode > 2) return fail(MOE_ERR_INVALID_ARG, "moe_probe_stream: mode %d not 0, 1 or 2", mode);
   if (bytes <= 0 || bytes % 16 != 0) return fail(MOE_ERR_SHAPE, "moe_probe_stream: bytes must be a positive multiple of 16");
