@@ -41,6 +41,12 @@ namespace {
 // are not written.
 template <typename T> using Raw8 = uint32_t __attribute__((ext_vector_type(2 * sizeof(T))));
 
+// They at a multiple of 16 bytes, which is what with_access looks for: an fp32 Raw8 would promise 32.
+template <typename T> struct Whole8 {
+  typedef uint32_t type __attribute__((ext_vector_type(2 * sizeof(T)), aligned(16)));
+  static_assert(alignof(type) == 16);
+};
+
 template <typename T> __device__ __forceinline__ float value(Raw8<T> r, int i) {
   if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
   else if constexpr (__is_same(T, _Float16)) return (float)__builtin_bit_cast(_Float16, (uint16_t)(r[i / 2] >> (i % 2 * 16)));
@@ -84,7 +90,7 @@ template <Access ACC, typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
   Raw8<T> r = {};
   if constexpr (ACC != ANY) {
-    if (n > 0) r = __builtin_nontemporal_load(reinterpret_cast<const Raw8<T>*>(p));
+    if (n > 0) r = __builtin_nontemporal_load(reinterpret_cast<const typename Whole8<T>::type*>(p));
   } else if (n >= 8) {
     r = reinterpret_cast<const AnyRaw8<T>*>(p)->v;
   } else if constexpr (sizeof(T) == 4) {
@@ -102,9 +108,9 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
 template <Access ACC, typename T>
 __device__ __forceinline__ void store8(T* p, int n, Raw8<T> r) {
   if constexpr (ACC == STREAM) {
-    __builtin_nontemporal_store(r, reinterpret_cast<Raw8<T>*>(p));
+    __builtin_nontemporal_store(r, reinterpret_cast<typename Whole8<T>::type*>(p));
   } else if constexpr (ACC == WHOLE) {
-    *reinterpret_cast<Raw8<T>*>(p) = r;
+    *reinterpret_cast<typename Whole8<T>::type*>(p) = r;
   } else if (n >= 8) {
     reinterpret_cast<AnyRaw8<T>*>(p)->v = r;
   } else if constexpr (sizeof(T) == 4) {
@@ -124,7 +130,7 @@ __device__ __forceinline__ void load_weight(const void* w, bool fp32, int c, int
   const auto load = [&]<typename W>(const W* p) {
     Raw8<W> r = {};
     if constexpr (ACC == ANY) r = load8<ANY>(p, n);
-    else if (n > 0) r = *reinterpret_cast<const Raw8<W>*>(p);   // (every block's: through the caches)
+    else if (n > 0) r = *reinterpret_cast<const typename Whole8<W>::type*>(p);   // (every block's: through the caches)
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = value<W>(r, i);
   };
