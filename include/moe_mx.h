@@ -514,7 +514,8 @@ moe_status moe_mxfp4_matmul(const void* x, int x_dtype, const uint8_t* x_scales,
 /*   grad_weight  device, fp32 [cols]; zeros for rows = 0                                                 */
 /* Limits: rows in [0, MOE_MAX_FLAT_ROWS), cols in [1, MOE_NORM_MAX_COLS]; codes 8-byte aligned, the other   */
 /* tensors as their elements. An output may be exactly an input's buffer (y or h: x or residual; grad_x:      */
-/* grad_y, h or grad_h), else apart from all inputs.                                                         */
+/* grad_y, h or grad_h), else apart from all inputs; the outputs, and the workspace, are apart from each      */
+/* other. Others: MOE_ERR_INVALID_ARG.                                                                       */
 /* ------------------------------------------------------------------------ */
 #define MOE_NORM_MAX_COLS 16384
 moe_status moe_rms_norm(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const void* weight,

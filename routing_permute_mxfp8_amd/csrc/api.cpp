@@ -475,6 +475,30 @@ bool misaligned(size_t to, std::initializer_list<const void*> ps) {
   return false;
 }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
+}
+
+// A tensor of a call, null or of 0 bytes where it takes no part. rows: a matrix of rows, in whose exact
+// place an output of rows may be.
+struct Place {
+  const void* at;
+  int64_t bytes;
+  bool rows;
+};
+// Whether an output shares memory with another, or with an input in a way that is not allowed.
+bool outputs_clash(std::initializer_list<Place> outs, std::initializer_list<Place> ins) {
+  for (const Place* o = outs.begin(); o != outs.end(); ++o) {
+    if (!o->at) continue;
+    for (const Place* q = o + 1; q != outs.end(); ++q)
+      if (q->at && overlap(o->at, o->bytes, q->at, q->bytes)) return true;
+    for (const Place& q : ins)
+      if (q.at && overlap(o->at, o->bytes, q.at, q.bytes) && !(o->rows && q.rows && o->at == q.at)) return true;
+  }
+  return false;
+}
+
 moe_status check_norm(const char* who, int dtype, int64_t rows, int64_t cols, int weight_dtype) {
   if (rows < 0 || rows >= MOE_MAX_FLAT_ROWS)
     return fail(MOE_ERR_SHAPE, "%s: rows %lld outside [0, %d)", who, (long long)rows, MOE_MAX_FLAT_ROWS);
@@ -510,11 +534,6 @@ void carve_gmm16(Carver& cv, moe::Gmm16Params& p) {   // (of a plan)
   if (p.part_floats) p.part = cv.take<float>(p.part_floats);
   if (p.copy_a) p.a16 = cv.take<uint16_t>(p.copy_a);
   if (p.copy_b) p.b16 = cv.take<uint16_t>(p.copy_b);
-}
-
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a_bytes > 0 && b_bytes > 0 && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
 }
 
 moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size_t workspace_bytes, hipStream_t stream) {
@@ -1206,6 +1225,12 @@ moe_status moe_rms_norm(const void* x, const void* residual, int dtype, int64_t 
   if (misaligned(sz, {x, residual, y, h}) || misaligned(weight_dtype == MOE_DTYPE_FP32 ? 4 : 2, {weight}) ||
       misaligned(4, {rstd}) || (quant && misaligned(8, {codes})))
     return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm: tensors must be aligned to their elements, codes to 8 bytes");
+  const int64_t all = rows * cols * (int64_t)sz, scale_bytes = rows * scale_cols(cols);
+  if (outputs_clash({{y, all, true}, {residual ? h : nullptr, all, true}, {rstd, 4 * rows, false},
+                     {quant ? codes : nullptr, quant_mode == MOE_QUANT_MXFP4_E2M1 ? rows * cols / 2 : rows * cols, false},
+                     {quant ? scales : nullptr, scale_bytes, false}},
+                    {{x, all, true}, {residual, all, true}, {weight, cols * (weight_dtype == MOE_DTYPE_FP32 ? 4 : 2), false}}))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm: an output overlaps another, or an input other than exactly (y or h: x or residual)");
   moe::NormParams p;
   p.x = x; p.residual = residual; p.weight = weight; p.dtype = dtype; p.weight_dtype = weight_dtype; p.rows = rows;
   p.cols = (int)cols; p.eps = eps; p.y = y; p.h = h; p.rstd = rstd; p.codes = codes; p.scales = scales;
@@ -1240,6 +1265,12 @@ moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* 
   Carver need(nullptr);
   need.take<float>((size_t)p.parts * cols);
   if (moe_status s = check_ws("moe_rms_norm_backward", need.off, workspace, workspace_bytes)) return s;
+  const int64_t all = rows * cols * (int64_t)sz;
+  if (outputs_clash({{grad_x, all, true}, {grad_weight, 4 * cols, false}, {workspace, (int64_t)need.off, false}},
+                    {{grad_y, all, true}, {h, all, true}, {grad_h, all, true}, {rstd, 4 * rows, false},
+                     {weight, cols * (weight_dtype == MOE_DTYPE_FP32 ? 4 : 2), false}}))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rms_norm_backward: an output or the workspace overlaps another, or an input other than exactly "
+                "(grad_x: grad_y, h or grad_h)");
   Carver cv(workspace);
   p.part = cv.take<float>((size_t)p.parts * cols);
   p.grad_y = grad_y; p.h = h; p.grad_h = grad_h; p.weight = weight; p.rstd = rstd; p.dtype = dtype;
