@@ -546,8 +546,9 @@ moe_status moe_rms_norm_backward(const void* grad_y, const void* h, const void* 
 /* sizes and element-aligned addresses are taken. An n or k along which an operand's rows lie that is no   */
 /* multiple of 8 costs a copy of that operand in the workspace (not forward up to 32 rows of few            */
 /* weights); operands that are not 16-byte aligned take a kernel that is many times slower (not forward      */
-/* up to 16 rows). An out that overlaps an operand: MOE_ERR_INVALID_ARG. The results do not depend on the    */
-/* workspace's contents and are the same bits in every call.                                                */
+/* up to 16 rows). An out that overlaps an operand or the offsets, and a workspace that overlaps any of       */
+/* them: MOE_ERR_INVALID_ARG. The results do not depend on the workspace's contents and are the same bits     */
+/* in every call.                                                                                           */
 /* ------------------------------------------------------------------------ */
 moe_status moe_grouped_matmul_workspace_size(int64_t rows, int64_t num_groups, int64_t n, int64_t k, int transpose_w,
                                              size_t* bytes /* host out */);

@@ -554,6 +554,10 @@ moe_status run_gmm16(const char* who, moe::Gmm16Params& p, void* workspace, size
   const int64_t out_bytes = out_size * (p.wgrad ? weights : p.rows * p.n);
   if (overlap(p.out, out_bytes, p.a, a_bytes) || overlap(p.out, out_bytes, p.b, b_bytes))
     return fail(MOE_ERR_INVALID_ARG, "%s: out overlaps an operand", who);
+  const int64_t off_bytes = p.off ? 4 * ((int64_t)p.groups + 1) : 0, used = (int64_t)cv.off;
+  if (overlap(p.out, out_bytes, p.off, off_bytes) || overlap(workspace, used, p.out, out_bytes) ||
+      overlap(workspace, used, p.a, a_bytes) || overlap(workspace, used, p.b, b_bytes) || overlap(workspace, used, p.off, off_bytes))
+    return fail(MOE_ERR_INVALID_ARG, "%s: out overlaps the offsets, or the workspace overlaps another tensor", who);
   hipError_t e = moe::launch_gmm16(p, stream);
   if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s launch: %s", who, hipGetErrorString(e));
   return ok();
