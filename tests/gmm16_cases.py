@@ -50,6 +50,13 @@ _WEIGHTS = [
 ]
 
 
+# (form, tile, rows of each group, groups, n, k): every block has more items than it describes at a time (64)
+MANY_ITEMS = [(form, *c) for form in FORMS[:2] for c in [
+    (32, 8, 1000, 8200, 8), (64, 3000, 1000, 8, 8), (128, 64, 1000, 4104, 8), (160, 256, 500, 4104, 8),
+    (192, 150, 1000, 4104, 8), (256, 30000, 50, 520, 8)]] + [
+    ("weights", 64, 8, 500, 8200, 8), ("weights", 128, 8, 500, 2056, 264), ("weights", 256, 8, 500, 4104, 264)]
+
+
 def offsets(rows, groups):
     """Group offsets near the mean: some rows in front of the first group and behind the last, of four
     groups and more the second empty. None for one group."""

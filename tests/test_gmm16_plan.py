@@ -6,7 +6,7 @@ import os
 import pytest
 
 import routing_permute_mxfp8_amd as rp
-from gmm16_cases import FORMS, cases
+from gmm16_cases import FORMS, MANY_ITEMS, cases
 
 
 @pytest.fixture(scope="module")
@@ -26,6 +26,16 @@ def plan(lib, form, rows, groups, n, k):
 @pytest.mark.parametrize("form,tile,shared,rows,groups,n,k", cases())
 def test_the_cases_reach_their_tiles(lib, form, tile, shared, rows, groups, n, k):
     assert plan(lib, form, rows, groups, n, k) == (tile, shared)
+
+
+@pytest.mark.parametrize("form,tile,each,groups,n,k", MANY_ITEMS)
+def test_the_cases_of_many_items(lib, form, tile, each, groups, n, k):
+    """They reach their tiles, and 256 units of three, two or one blocks at a time have over 64 items for each."""
+    assert plan(lib, form, each * groups, groups, n, k)[0] == tile
+    up = lambda a, b: -(-a // b)  # noqa: E731
+    width, blocks = (256, 1) if tile > 64 else (128, {64: 2, 32: 3}[tile])
+    items = groups * (up(n, tile) * up(k, width) if form == "weights" else up(each, tile) * up(n, width))
+    assert items > 65 * 256 * blocks
 
 
 @pytest.mark.parametrize("form", FORMS)

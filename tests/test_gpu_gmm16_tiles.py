@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import routing_permute_mxfp8_amd as rp
-from gmm16_cases import cases, offsets
+from gmm16_cases import MANY_ITEMS, cases, offsets
 from gpu_support import DEV, say
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +98,23 @@ def test_tile(form, tile, shared, rows, groups, n, k, dtype):
     if form != "weights":   # rows outside the groups
         for out in outs:
             assert bool((out[:spans[0][0]] == 7).all()) and bool((out[spans[-1][1]:] == 7).all())
+
+
+@pytest.mark.parametrize("form,tile,each,groups,n,k", MANY_ITEMS)
+def test_many_items(form, tile, each, groups, n, k):
+    """Blocks with more items than they describe at a time: whole numbers, whose sums fp32 holds exactly."""
+    say(f"{form} tile {tile}: {groups} groups of {each} rows, n {n}, k {k}")
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    draw = lambda *s: torch.randint(-7, 8, s, generator=gen, device=DEV).to(BF)  # noqa: E731
+    o = torch.arange(0, each * groups + 1, each, dtype=torch.int32, device=DEV)
+    if form == "weights":
+        a, b = draw(groups * each, n), draw(groups * each, k)
+        got = rp.grouped_matmul_wgrad(a, b, o)
+        want = torch.bmm(a.float().view(groups, each, n).transpose(1, 2).contiguous(), b.float().view(groups, each, k))
+        assert torch.equal(got, want.to(BF))
+        return
+    trans = form == "transposed"
+    x, w = draw(groups * each, k), draw(groups, k, n) if trans else draw(groups, n, k)
+    got = rp.grouped_matmul(x, w, o, transpose_w=trans)
+    right = w.float() if trans else w.float().transpose(1, 2).contiguous()
+    assert torch.equal(got.view(groups, each, n), torch.bmm(x.float().view(groups, each, k), right).to(BF))
