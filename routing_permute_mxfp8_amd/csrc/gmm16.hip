@@ -185,10 +185,6 @@ double tiles_of(double mean, int mt, bool one) {
   return sum;
 }
 
-// Steps that sharing an item between blocks has to save: the join takes a launch and, for 256 tiles
-// of 256 x 256, 64 MB written and read, some 30 us in all.
-constexpr int kGain = 16;
-
 // Items of a call with tiles of shape s, and steps of one, as expected.
 struct Load16 {
   double items, steps;
@@ -203,7 +199,7 @@ Load16 load_of(const Gmm16Params& p, const Shape16& s) {
 // Blocks that share an item of the last, part-filled round of `rem` items: 1 where that saves too little.
 double parts_of(double rem, double steps, double units) {
   const double parts = rem > 0 ? std::min(std::floor(units / rem), std::floor(steps / 4)) : 1;
-  return parts >= 2 && steps - std::ceil(steps / parts) >= kGain ? parts : 1;
+  return parts >= 2 && steps - std::ceil(steps / parts) >= kGain16 ? parts : 1;
 }
 
 // Microseconds of a call with tiles of shape s, but for the memory traffic, which they share.
@@ -250,7 +246,6 @@ void gmm16_plan(Gmm16Params& p) {
   p.pitch_b = (cols_b + 7) / 8 * 8;
   p.copy_a = p.pitch_a != cols_a ? (size_t)p.rows * p.pitch_a : 0;
   p.copy_b = p.pitch_b != cols_b ? (size_t)rows_b * p.pitch_b : 0;
-  p.gain = kGain;
   // Parts of shared items, where some are expected: the join is a launch, needed or not (24 steps, 64
   // to 365 items: 15 us shared and 23 not, 20 not shared and 23 with a join for nothing). A group
   // that is longer than the mean may want parts in the gradient by weights (launch_tile16 knows the
@@ -259,7 +254,7 @@ void gmm16_plan(Gmm16Params& p) {
     if (s.mt != p.mt) continue;
     const double units = (double)kTile16Units * s.blocks;
     const auto [items, steps] = load_of(p, s);
-    const bool share = p.wgrad ? (p.rows + 63) / 64 - 4 >= kGain : parts_of(items - std::floor(items / units) * units, steps, units) >= 2;
+    const bool share = p.wgrad ? (p.rows + 63) / 64 - 4 >= kGain16 : parts_of(items - std::floor(items / units) * units, steps, units) >= 2;
     p.part_floats = share ? (size_t)units * s.mt * s.nt : 0;
   }
 }

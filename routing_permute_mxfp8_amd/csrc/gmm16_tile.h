@@ -66,7 +66,7 @@ struct Tile16Args {
   bool out_fp32;
   void* out;
   float* part;           // workspace of shared items: a tile for each block, or null: items are not shared
-  int steps, gain;       // steps of an item (not kWeights); how many have to be saved for an item to be shared
+  int steps;             // of an item (not kWeights)
 };
 
 template <int WAVES, int WC, int CB, int RB>
@@ -118,7 +118,7 @@ __host__ __device__ __forceinline__ Share share_of(const Tile16Args& p, int64_t 
   s.full = (int)(n / per);
   s.rem = (int)(n - (int64_t)s.full * per);
   s.parts = s.rem ? (per / s.rem < steps / 4 ? per / s.rem : steps / 4) : 1;   // (a part has four steps at least)
-  if (!p.part || s.parts < 2 || steps - (steps + s.parts - 1) / s.parts < p.gain) s.parts = 1;
+  if (!p.part || s.parts < 2 || steps - (steps + s.parts - 1) / s.parts < kGain16) s.parts = 1;
   return s;
 }
 
@@ -752,7 +752,7 @@ hipError_t launch_tile16_form(const Gmm16Params& p, hipStream_t stream) {
   a.off = p.off; a.groups = p.groups; a.rows = (int)p.rows; a.out_fp32 = p.out_fp32; a.out = p.out;
   if (FORM == kWeights) { a.nc = p.k; a.nr = p.n; a.con = a.con_t = kCon; a.steps = 0; }
   else { a.nc = p.n; a.nr = 1; a.con = (p.k + 7) / 8 * 8; a.con_t = p.k; a.steps = (a.con + kCon - 1) / kCon; }
-  a.part = p.part; a.gain = p.gain;
+  a.part = p.part;
   return p.half ? launch_tile16_odd<FORM, _Float16>(a, p.mt, p.odd, stream) : launch_tile16_odd<FORM, __bf16>(a, p.mt, p.odd, stream);
 }
 

@@ -377,9 +377,8 @@ struct Gmm16Params {
   bool out_fp32 = false;           // else the operands' type
   void* out = nullptr;
   // what gmm16_plan makes of the sizes:
-  int mt = 0;                      // rows of a tile of the LDS-staged kernels, 0: the kernel for every shape
+  int mt = 0;                      // rows of a tile of the LDS-staged kernels (unless few)
   int pitch_a = 0, pitch_b = 0;    // elements from one row of a, b to the next there, multiples of 8
-  int gain = 0;                    // steps that sharing an item between blocks has to save
   size_t part_floats = 0, copy_a = 0, copy_b = 0;   // workspace: fp32 parts; elements of copies with those pitches
   // and the workspace
   float* part = nullptr;
@@ -389,6 +388,9 @@ struct Gmm16Params {
   bool few = false;                // the kernel of few rows takes it
 };
 constexpr int kTile16Units = 256;  // compute units that the workspace of shared items is laid out for
+// Steps that sharing an item between blocks has to save: the join takes a launch and, for 256 tiles
+// of 256 x 256, 64 MB written and read, some 30 us in all.
+constexpr int kGain16 = 16;
 void gmm16_plan(Gmm16Params& p);
 bool gmm16_is_few(const Gmm16Params& p);
 hipError_t launch_gmm16_few(const Gmm16Params& p, hipStream_t stream);
