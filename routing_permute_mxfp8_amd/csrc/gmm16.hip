@@ -197,6 +197,9 @@ Load16 load_of(const Gmm16Params& p, const Shape16& s) {
 }
 
 // Blocks that share an item of the last, part-filled round of `rem` items: 1 where that saves too little.
+// An expectation: where there are many groups of unknown sizes it says little about the remainder, so
+// that a call may get parts and a join for nothing (5 us: 8192 rows on 32 groups, 4096 to 7168, expect
+// 1792.02 items) or none where some would have helped.
 double parts_of(double rem, double steps, double units) {
   const double parts = rem > 0 ? std::min(std::floor(units / rem), std::floor(steps / 4)) : 1;
   return parts >= 2 && steps - std::ceil(steps / parts) >= kGain16 ? parts : 1;
@@ -217,9 +220,11 @@ double estimate(const Gmm16Params& p, const Shape16& s) {
 
 // The tile with the least estimate. Groups of about 256 rows, e.g., take two tiles of 160 rows rather
 // than one and often a second of 256 (8192 rows on 32 groups of 4096 x 7168, forward and transposed:
-// 577 and 618 us, with 192 rows 605 and 662, with 256 591 and 657, with 128 718 and 760). Limits:
+// 570 and 583 us, with 192 rows 608 and 626, with 256 625 and 622, with 128 728 and 731). Limits:
 // where rows outside the groups or a few large groups make the mean a poor guide, the tile is larger
-// or smaller than it should be.
+// or smaller than it should be; and the model is that of long contractions: a 256 x 256 item of four
+// steps of the gradient by weights takes 14.6 us and not its 11.2 (the estimates of a call's tiles are
+// off alike).
 int tile_rows(const Gmm16Params& p) {
   int best = 0;
   double least = 0;

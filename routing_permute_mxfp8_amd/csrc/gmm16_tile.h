@@ -22,9 +22,9 @@
 // rows 0 - 3 and 8 - 11 of 32 bytes each: 64-byte blocks of row r are exchanged by r % 4, their halves
 // by r / 8 % 2, so that these lie in different banks.
 //
-// What bounds it: large products the card's power, at which it runs its clock down (1.66 GHz with
-// the MFMAs at work 70 % of the cycles, forward, 32768 rows on 16 groups of 4096 x 7168: 1.56 ms, 1.23
-// PFLOP/s; the MFMAs alone, of random operands in registers, 2.06), then the items' ends: an item's
+// What bounds it: large products the card's power, at which it runs its clock down (1.66 to
+// 1.81 GHz by the board, with the MFMAs at work 69 % of the cycles, forward, 32768 rows on 16 groups of
+// 4096 x 7168: 1.55 to 1.66 ms, 1.25 to 1.16 PFLOP/s; the MFMAs alone, of random operands in registers, 2.06), then the items' ends: an item's
 // stores and the next one's zeros take 5 us beside 1.8 a step, which a contraction of a few steps
 // shows (gradient by the weights, 256 rows a group: 4 - 6 steps, 14.6 us an item). Products of few
 // rows the weights' stream (256 rows on 64 groups: 3.76 GB in 0.54 ms, 7.0 TB/s). Why tiles of up to
